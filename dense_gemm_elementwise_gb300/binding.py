@@ -38,9 +38,20 @@ OP = {"accum": GE_ACCFETCH, "load": GE_LOAD, "scalar": GE_SCALAR, "broadcast": G
 EXPORTS = ["gemm_epi_plan_create", "gemm_epi_plan_create_ex", "gemm_epi_validate", "gemm_epi_run",
            "gemm_epi_unfused_workspace_bytes", "gemm_epi_run_unfused", "gemm_epi_plan_destroy",
            "gemm_epi_plan_info", "gemm_epi_status_string", "gemm_epi_last_error",
-           "gemm_epi_run_unfused_noalloc", "gemm_epi_grouped_plan_create", "gemm_epi_grouped_run"]
+           "gemm_epi_run_unfused_noalloc", "gemm_epi_grouped_plan_create", "gemm_epi_grouped_run",
+           "gemm_epi_xent_plan_create", "gemm_epi_xent_workspace_bytes", "gemm_epi_xent_loss",
+           "gemm_epi_xent_step", "gemm_epi_xent_plan_destroy", "gemm_epi_norm_plan_create",
+           "gemm_epi_norm_workspace_bytes", "gemm_epi_norm_run", "gemm_epi_norm_grad",
+           "gemm_epi_norm_plan_destroy"]
 GE_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 GE_MAX_GROUPS = 4096
+GE_XENT_SUM, GE_XENT_MEAN = 0, 1
+GE_INDEX_I64, GE_INDEX_I32 = 0, 1
+GE_NORM_NONE, GE_NORM_RMS, GE_NORM_LAYER = 0, 1, 2
+GE_NORM_MAX_D = 32768
+REDUCTION = {"sum": GE_XENT_SUM, "mean": GE_XENT_MEAN}
+INDEX = {"i64": GE_INDEX_I64, "i32": GE_INDEX_I32}
+NORM = {"none": GE_NORM_NONE, "rms": GE_NORM_RMS, "layer": GE_NORM_LAYER}
 
 
 class ge_node(ctypes.Structure):
@@ -77,6 +88,23 @@ class ge_plan_info(ctypes.Structure):
                 ("cta_group", "tile_m", "tile_n", "tile_k", "stages", "epi_chunk", "aux_stages",
                  "grid", "num_tiles", "smem_bytes", "n_instr", "n_regs", "num_sms",
                  "epi_variant", "cluster_n", "epi_warps", "raster_group")]
+
+
+class ge_xent_desc(ctypes.Structure):
+    _fields_ = [("ab", ctypes.c_int32), ("index", ctypes.c_int32), ("reduction", ctypes.c_int32),
+                ("timeout_ms", ctypes.c_int32), ("max_ctas", ctypes.c_int32),
+                ("logit_scale", ctypes.c_float), ("z_loss", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("ldh", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("lddh", ctypes.c_int64), ("lddw", ctypes.c_int64),
+                ("buffer_bytes", ctypes.c_int64)]
+
+
+class ge_norm_desc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int32), ("w", ctypes.c_int32), ("pre", ctypes.c_int32),
+                ("post", ctypes.c_int32), ("eps_pre", ctypes.c_float), ("eps_post", ctypes.c_float),
+                ("alpha", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("rows_per_gate", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldy", ctypes.c_int64), ("ldh", ctypes.c_int64)]
 
 
 class GemmEpiError(RuntimeError):
@@ -125,6 +153,27 @@ def _load():
     L.gemm_epi_plan_destroy.argtypes = [P]
     L.gemm_epi_plan_info.restype = ctypes.c_int
     L.gemm_epi_plan_info.argtypes = [P, ctypes.POINTER(ge_plan_info)]
+    f32, sz = ctypes.c_float, ctypes.c_size_t
+    L.gemm_epi_xent_plan_create.restype = ctypes.c_int
+    L.gemm_epi_xent_plan_create.argtypes = [pp, i64, i64, i64, ctypes.POINTER(ge_xent_desc)]
+    L.gemm_epi_xent_workspace_bytes.restype = sz
+    L.gemm_epi_xent_workspace_bytes.argtypes = [P, ctypes.c_int]
+    L.gemm_epi_xent_loss.restype = ctypes.c_int
+    L.gemm_epi_xent_loss.argtypes = [P] * 9 + [sz, P]
+    L.gemm_epi_xent_step.restype = ctypes.c_int
+    L.gemm_epi_xent_step.argtypes = [P] * 5 + [f32] + [P] * 6 + [sz, P]
+    L.gemm_epi_xent_plan_destroy.restype = None
+    L.gemm_epi_xent_plan_destroy.argtypes = [P]
+    L.gemm_epi_norm_plan_create.restype = ctypes.c_int
+    L.gemm_epi_norm_plan_create.argtypes = [pp, i64, i64, ctypes.POINTER(ge_norm_desc)]
+    L.gemm_epi_norm_workspace_bytes.restype = sz
+    L.gemm_epi_norm_workspace_bytes.argtypes = [P]
+    L.gemm_epi_norm_run.restype = ctypes.c_int
+    L.gemm_epi_norm_run.argtypes = [P] * 9
+    L.gemm_epi_norm_grad.restype = ctypes.c_int
+    L.gemm_epi_norm_grad.argtypes = [P] * 14 + [sz, P]
+    L.gemm_epi_norm_plan_destroy.restype = None
+    L.gemm_epi_norm_plan_destroy.argtypes = [P]
     L.gemm_epi_status_string.restype = ctypes.c_char_p
     L.gemm_epi_status_string.argtypes = [ctypes.c_int]
     L.gemm_epi_last_error.restype = ctypes.c_int
@@ -301,6 +350,144 @@ def prepare_run(plan, A, B, aux, scalars, outs, stream=None):
             _stream(stream))
     fn = lib.gemm_epi_run
     return lambda: fn(*args)
+
+
+# ------------------------------------------------------- vocabulary loss --
+
+def make_xent_desc(ab, index="i64", ldh=0, ldw=0, lddh=0, lddw=0, logit_scale=1.0, z_loss=0.0,
+                   reduction="mean", buffer_bytes=0, timeout_ms=0, max_ctas=0):
+    d = ge_xent_desc()
+    d.ab = DTYPE[ab] if isinstance(ab, str) else ab
+    d.index = INDEX[index] if isinstance(index, str) else index
+    d.reduction = REDUCTION[reduction] if isinstance(reduction, str) else reduction
+    d.timeout_ms, d.max_ctas = timeout_ms, max_ctas
+    d.logit_scale, d.z_loss = logit_scale, z_loss
+    d.ldh, d.ldw, d.lddh, d.lddw = ldh, ldw, lddh, lddw
+    d.buffer_bytes = buffer_bytes
+    return d
+
+
+def gemm_epi_xent_plan_create(T, V, D, desc):
+    """Returns the plan handle; raises GemmEpiError with the status code."""
+    h = ctypes.c_void_p()
+    st = lib.gemm_epi_xent_plan_create(ctypes.byref(h), T, V, D, ctypes.byref(desc))
+    if st != GE_OK:
+        raise GemmEpiError(st, "gemm_epi_xent_plan_create")
+    return h
+
+
+def gemm_epi_xent_plan_destroy(plan):
+    lib.gemm_epi_xent_plan_destroy(plan)
+
+
+def gemm_epi_xent_workspace_bytes(plan, grads):
+    return lib.gemm_epi_xent_workspace_bytes(plan, int(bool(grads)))
+
+
+def _bytes_of(workspace, workspace_bytes):
+    if workspace_bytes is None:
+        return workspace.numel() * workspace.element_size()
+    return workspace_bytes
+
+
+def _checked(st, where, check=True):
+    if check and st != GE_OK:
+        raise GemmEpiError(st, where)
+    return st
+
+
+def prepare_xent_loss(plan, H, W, target, weight, loss, lse, total, workspace, workspace_bytes=None,
+                      stream=None):
+    """As prepare_run, for gemm_epi_xent_loss."""
+    args = (plan, _addr(H), _addr(W), _addr(target), _addr(weight), _addr(loss), _addr(lse),
+            _addr(total), _addr(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream))
+    fn = lib.gemm_epi_xent_loss
+    return lambda: fn(*args)
+
+
+def gemm_epi_xent_loss(plan, H, W, target, weight, loss, lse, total, workspace,
+                       workspace_bytes=None, stream=None, check=True):
+    return _checked(prepare_xent_loss(plan, H, W, target, weight, loss, lse, total, workspace,
+                                      workspace_bytes, stream)(), "gemm_epi_xent_loss", check)
+
+
+def prepare_xent_step(plan, H, W, target, weight, grad_scale, loss, lse, total, dH, dW, workspace,
+                      workspace_bytes=None, stream=None):
+    """As prepare_run, for gemm_epi_xent_step."""
+    args = (plan, _addr(H), _addr(W), _addr(target), _addr(weight), float(grad_scale), _addr(loss),
+            _addr(lse), _addr(total), _addr(dH), _addr(dW), _addr(workspace),
+            _bytes_of(workspace, workspace_bytes), _stream(stream))
+    fn = lib.gemm_epi_xent_step
+    return lambda: fn(*args)
+
+
+def gemm_epi_xent_step(plan, H, W, target, weight, grad_scale, loss, lse, total, dH, dW, workspace,
+                       workspace_bytes=None, stream=None, check=True):
+    return _checked(prepare_xent_step(plan, H, W, target, weight, grad_scale, loss, lse, total, dH,
+                                      dW, workspace, workspace_bytes, stream)(),
+                    "gemm_epi_xent_step", check)
+
+
+# --------------------------------------------------- norms around a block --
+
+def make_norm_desc(x, w, pre="rms", post="rms", eps_pre=1e-5, eps_post=1e-5, alpha=1.0,
+                   rows_per_gate=0, ldx=0, ldb=0, ldy=0, ldh=0):
+    d = ge_norm_desc()
+    d.x = DTYPE[x] if isinstance(x, str) else x
+    d.w = DTYPE[w] if isinstance(w, str) else w
+    d.pre = NORM[pre] if isinstance(pre, str) else pre
+    d.post = NORM[post] if isinstance(post, str) else post
+    d.eps_pre, d.eps_post, d.alpha = eps_pre, eps_post, alpha
+    d.rows_per_gate = rows_per_gate
+    d.ldx, d.ldb, d.ldy, d.ldh = ldx, ldb, ldy, ldh
+    return d
+
+
+def gemm_epi_norm_plan_create(T, D, desc):
+    """Returns the plan handle; raises GemmEpiError with the status code."""
+    h = ctypes.c_void_p()
+    st = lib.gemm_epi_norm_plan_create(ctypes.byref(h), T, D, ctypes.byref(desc))
+    if st != GE_OK:
+        raise GemmEpiError(st, "gemm_epi_norm_plan_create")
+    return h
+
+
+def gemm_epi_norm_plan_destroy(plan):
+    lib.gemm_epi_norm_plan_destroy(plan)
+
+
+def gemm_epi_norm_workspace_bytes(plan):
+    return lib.gemm_epi_norm_workspace_bytes(plan)
+
+
+def prepare_norm_run(plan, x, b, gate, w_post, w_pre, y, h, stream=None):
+    """As prepare_run, for gemm_epi_norm_run."""
+    args = (plan, _addr(x), _addr(b), _addr(gate), _addr(w_post), _addr(w_pre), _addr(y), _addr(h),
+            _stream(stream))
+    fn = lib.gemm_epi_norm_run
+    return lambda: fn(*args)
+
+
+def gemm_epi_norm_run(plan, x, b, gate, w_post, w_pre, y, h, stream=None, check=True):
+    return _checked(prepare_norm_run(plan, x, b, gate, w_post, w_pre, y, h, stream)(),
+                    "gemm_epi_norm_run", check)
+
+
+def prepare_norm_grad(plan, dy, dh, y, b, gate, w_post, w_pre, dx, db, dgate, dw_post, dw_pre,
+                      workspace, workspace_bytes=None, stream=None):
+    """As prepare_run, for gemm_epi_norm_grad."""
+    args = (plan, _addr(dy), _addr(dh), _addr(y), _addr(b), _addr(gate), _addr(w_post),
+            _addr(w_pre), _addr(dx), _addr(db), _addr(dgate), _addr(dw_post), _addr(dw_pre),
+            _addr(workspace), _bytes_of(workspace, workspace_bytes), _stream(stream))
+    fn = lib.gemm_epi_norm_grad
+    return lambda: fn(*args)
+
+
+def gemm_epi_norm_grad(plan, dy, dh, y, b, gate, w_post, w_pre, dx, db, dgate, dw_post, dw_pre,
+                       workspace, workspace_bytes=None, stream=None, check=True):
+    return _checked(prepare_norm_grad(plan, dy, dh, y, b, gate, w_post, w_pre, dx, db, dgate,
+                                      dw_post, dw_pre, workspace, workspace_bytes, stream)(),
+                    "gemm_epi_norm_grad", check)
 
 
 def gemm_epi_status_string(status):

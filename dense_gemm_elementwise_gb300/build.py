@@ -1,6 +1,6 @@
 """Build ``libgemm_epi.so`` in-tree with nvcc for sm_103a.
 
-The four translation units compile in parallel; the shared library links the
+The translation units compile in parallel; the shared library links the
 CUDA runtime statically and reaches the driver (tensor-map encoding) through
 the runtime's entry-point query, so it needs no libcuda at link time.
 """
@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libgemm_epi.so")
-UNITS = ["plan", "unfused", "jit", "k_cg1_n64", "k_cg1_n128", "k_cg1_n256", "k_cg2_n128", "k_cg2_n256"]
+UNITS = ["plan", "unfused", "jit", "k_cg1_n64", "k_cg1_n128", "k_cg1_n256", "k_cg2_n128", "k_cg2_n256",
+         "norm", "xent", "k_xent_cg1", "k_xent_cg2"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -23,6 +23,7 @@
 
 #include "catalog.cuh"
 #include "common.cuh"
+#include "host.h"
 #include "launch.h"
 #include "program.cuh"
 
@@ -698,6 +699,36 @@ void log_plan(const gemm_epi_plan *pl) {
 }
 
 }  // namespace
+
+// ------------------------------------------- shared with the other operators --
+namespace ge {
+
+int current_device(int *dev, int *sms, int *max_smem) { return check_device(dev, sms, max_smem); }
+
+uint32_t *status_block() {
+  void *sym = nullptr;
+  if (cudaGetSymbolAddress(&sym, g_ge_status) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return static_cast<uint32_t *>(sym);
+}
+
+bool encode_rows(CUtensorMap *m, int dtype, const void *ptr, uint64_t d0, uint64_t d1, uint64_t d2,
+                 uint64_t pitch, uint64_t slice, uint32_t b0, uint32_t b1) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t es = static_cast<uint64_t>(esize(dtype));
+  cuuint64_t dims[3] = {d0, d1, d2};
+  cuuint64_t strides[2] = {pitch * es, slice * es};
+  cuuint32_t box[3] = {b0, b1, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, tma_dtype(dtype), 3, const_cast<void *>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace ge
 
 // ------------------------------------------------------------- C ABI --
 extern "C" {

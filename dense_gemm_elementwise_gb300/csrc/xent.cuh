@@ -1,0 +1,51 @@
+// xent.cuh -- parameters and handles of the vocabulary loss's products.
+#pragma once
+
+#include "common.cuh"
+
+namespace ge {
+
+// What one product's epilogue does with its accumulator.
+enum XentMode {
+  X_STATS = 0,   // logits: each row's maximum and sum of exponentials, the target's logit
+  X_DLOGIT = 1,  // logits again: their gradient, rounded, into the piece buffer
+  X_OUT = 2,     // a gradient: scaled, rounded, stored (dW)
+  X_PART = 3,    // fp32 partial sums (dH), stored or added to what is there
+};
+
+constexpr int kXentBoxes = 2;            // output boxes per epilogue group, at most
+constexpr uint32_t kXentBox = 128 * 128; // one box: 128 rows of 128 bytes
+
+struct XentParams {
+  CUtensorMap tmA, tmB, tmOut;
+  uint32_t *status;
+  uint64_t timeout_ns;
+  const int32_t *rows;     // rows that take part (device)
+  int32_t M, N, K;         // sizes at most; the rows replace M (K for X_OUT)
+  int32_t num_n_blk, raster_group;
+  int32_t kb_split, splits;  // k-blocks per slice of K and slices (X_PART)
+  int32_t stages, boxes;
+  int32_t bf16;
+  int32_t b_row0;          // first vocabulary row of this piece
+  int32_t accumulate;      // X_PART: add to the slices
+  uint32_t off_B, off_out, off_bar;
+  float c;                 // logit_scale
+  float c2;                // logit_scale * log2(e)
+  const int32_t *target;   // gathered rows: the target, ...
+  float2 *stats;           // [2 * blocks of BN columns][M]: maximum (log2 units), sum
+  float *at_target;        // ... the target's logit
+  const float *lse2;       // ... log2-sum-exp2 of its logits
+  const float2 *coef;      // ... factors of p and of the target's 1
+  const float *out_scale;  // one float
+  // X_OUT: the TMA engine writes whole 16-byte units, so it is given the columns
+  // up to the last whole unit and the threads write the rest of each row
+  int32_t tma_cols;
+  uint16_t *out;
+  int64_t ld_out;
+};
+
+const void *xent_kernel_cg1(int mode);  // 128 x 128 tiles, one CTA
+const void *xent_kernel_cg2(int mode);  // 256 x 256 tiles, a CTA pair
+constexpr int kXentThreads = 32 * (2 + 8);  // producer, MMA, 8 epilogue warps
+
+}  // namespace ge

@@ -1,0 +1,471 @@
+// xent_kernel.cuh -- the products of the vocabulary loss on sm_103a.
+//
+// One persistent, warp-specialised kernel in four modes (XentMode):
+//   X_STATS   H @ W^T, K-major operands: logits that never leave the SM.  An
+//             epilogue thread owns one row of the tile and half of its
+//             columns: it takes their maximum, then the sum of
+//             2^(x - maximum), reading the accumulator from TMEM twice (64
+//             loads cost less than rescaling a running sum) and leaves the
+//             pair for the kernel that joins the tiles.
+//   X_DLOGIT  the same product: 2^(x - lse) * coef, less the target's 1, rounded
+//             to 16 bits into the piece buffer.
+//   X_OUT     dl^T @ H: dl read M-major, H N-major, the accumulator times one
+//             scale into dW.
+//   X_PART    dl @ W: dl K-major, W N-major, fp32 sums into slices, one
+//             per range of K (few rows make few tiles: K is split over the
+//             SMs), added by the TMA engine to earlier pieces' sums.  One
+//             tile of a launch owns each element of its slice, so the order
+//             of the additions is that of the launches.
+// Warps: 0 loads operands (TMA, an S-stage ring), 1 allocates TMEM and issues
+// tcgen05.mma into one of two accumulators, 2..9 are two epilogue groups of
+// four warps that take the tile's column steps in turn.  The number of rows that
+// take part is read from device memory, so a batch with ignored targets costs
+// what its other rows cost.  Mainloop and roles follow gemm_kernel.cuh; the
+// epilogue groups store through their own boxes.
+//
+// The products are bound by the tensor pipe when the batch is long and by
+// reading W when it is short.
+//
+// Every wait is bounded, as in gemm_kernel.cuh: an epilogue group agrees on the
+// outcome of its wait before its next barrier, so none of its warps is left alone.
+#pragma once
+
+#include "gemm_kernel.cuh"
+#include "xent.cuh"
+
+namespace ge {
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void group_barrier(int id) {
+  __syncwarp();
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+  __syncwarp();
+}
+
+// whether every thread of the group says yes
+__device__ __forceinline__ bool group_agrees(int id, bool yes) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(yes ? 1u : 0u)
+      : "memory");
+  __syncwarp();
+  return r != 0;
+}
+
+__device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *m, uint32_t src, int32_t x, int32_t y,
+                                                  int32_t z) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.bulk_group [%0, {%2, %3, %4}], [%1];" ::
+                   "l"(reinterpret_cast<uint64_t>(m)),
+               "r"(src), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack16(bool bf16, float lo, float hi) {
+  uint32_t r;
+  if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// barrier block
+constexpr uint32_t kXFull = 0, kXEmpty = 64, kXTmemFull = 128, kXTmemEmpty = 144, kXDrain = 160,
+                   kXTmemSlot = 168, kXAbort = 172;
+
+struct XentTile {
+  int z, mb, nb, kb0, kb1;
+};
+
+template <int CG, int BN, int MODE>
+__global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
+  using T = TileCfg<CG, BN>;
+  constexpr bool kAmn = MODE == X_OUT;                      // A is M-major
+  constexpr bool kBk = MODE == X_STATS || MODE == X_DLOGIT;  // B is K-major
+  constexpr int kEpi0 = 2;                                   // first epilogue warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG > 1 ? cluster_ctarank() : 0u;
+  const int unit = blockIdx.x / CG, n_units = gridDim.x / CG;
+  const uint32_t bar = sb + p.off_bar;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + p.off_bar + kXTmemSlot);
+  volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + p.off_bar + kXAbort);
+
+  if (warp == 0) {
+    if (lane < p.stages) {
+      mbar_init(bar + kXFull + 8 * lane, 1);
+      mbar_init(bar + kXEmpty + 8 * lane, 1);
+    }
+    if (lane < 2) {
+      mbar_init(bar + kXTmemFull + 8 * lane, 1);
+      mbar_init(bar + kXTmemEmpty + 8 * lane, 8 * CG);
+    }
+    if (lane == 0) {
+      mbar_init(bar + kXDrain, 1);
+      *abort_flag = 0u;
+      prefetch_tensormap(&p.tmA);
+      prefetch_tensormap(&p.tmB);
+    }
+    fence_mbarrier_init();
+    __syncwarp();
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_u32(tmem_slot), T::kTmemCols);
+    tmem_relinquish<CG>();
+  }
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG > 1) cluster_sync_all(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+  griddep_wait();
+
+  const Waiter wt{abort_flag, p.status, p.timeout_ns};
+  const int rows = __ldcg(p.rows);
+  const int M = MODE == X_OUT ? p.M : min(rows, p.M);
+  const int num_m_blk = (M + T::kMmaM - 1) / T::kMmaM;
+  // with no rows dW is 0: one k-block is run and its product dropped
+  const int num_kb = MODE == X_OUT ? max(1, (min(rows, p.K) + BK - 1) / BK) : (p.K + BK - 1) / BK;
+  const int per_slice = num_m_blk * p.num_n_blk;
+  const int num_tiles = MODE == X_PART ? per_slice * p.splits : per_slice;
+  const int my_tiles = unit < num_tiles ? (num_tiles - 1 - unit) / n_units + 1 : 0;
+  auto tile = [&](int i) {
+    XentTile t;
+    const int at = unit + i * n_units;
+    tile_coords(num_m_blk, p.num_n_blk, p.raster_group, at, t.z, t.mb, t.nb);
+    t.kb0 = MODE == X_PART ? t.z * p.kb_split : 0;
+    t.kb1 = MODE == X_PART ? min(num_kb, t.kb0 + p.kb_split) : num_kb;
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0, fills = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        const XentTile t = tile(i);
+        const int m0 = t.mb * T::kMmaM + static_cast<int>(rank) * BM;
+        const int n0 = t.nb * BN + static_cast<int>(rank) * T::kBnLocal;
+        const int nk = t.kb1 - t.kb0;
+        for (int kb = 0; kb < nk; ++kb) {
+          if (!wt.wait(bar + kXEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
+            ok = false;
+            break;
+          }
+          // odd tiles walk K backwards: a wave starts on what the last one left in L2
+          const int kx = (t.kb0 + ((i & 1) ? nk - 1 - kb : kb)) * BK;
+          const uint32_t full = bar + kXFull + 8 * stage;
+          const uint32_t sa = sb + stage * T::kABytes, sbb = sb + p.off_B + stage * T::kBBytes;
+          constexpr uint32_t kTx = CG * (T::kABytes + T::kBBytes);
+          uint32_t fb = full;
+          if constexpr (CG == 2) {
+            fb = mapa_shared(full, 0);
+            if (rank == 0) mbar_arrive_expect_tx(full, kTx);
+          } else {
+            mbar_arrive_expect_tx(full, kTx);
+          }
+          auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
+            if constexpr (CG == 2) tma_load_3d_pair(dst, m, fb, x, y, 0);
+            else tma_load_3d(dst, m, fb, x, y, 0);
+          };
+          if constexpr (kAmn) {
+            load(sa, &p.tmA, m0, kx);
+            load(sa + 8192, &p.tmA, m0 + 64, kx);
+          } else {
+            load(sa, &p.tmA, kx, m0);
+          }
+          if constexpr (kBk) {
+            load(sbb, &p.tmB, kx, p.b_row0 + n0);
+          } else {
+            // dH: the k rows of B are the piece's vocabulary rows
+            const int ky = MODE == X_PART ? p.b_row0 + kx : kx;
+#pragma unroll
+            for (int j = 0; j < T::kBAtoms; ++j) load(sbb + j * 8192, &p.tmB, n0 + 64 * j, ky);
+          }
+          ++fills;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      griddep_launch_dependents();
+      if (ok) {
+        for (int i = 0; i < p.stages; ++i) {
+          if (!wt.wait(bar + kXEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        for (int f = max(fills - p.stages, 0); f < fills; ++f)
+          wt.drain(bar + kXFull + 8 * (f % p.stages), static_cast<uint32_t>(f / p.stages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      const uint32_t id = make_idesc_f16(p.bf16 != 0, T::kMmaM, BN, kAmn, !kBk);
+      constexpr uint32_t kAk16 = (kAmn ? 2048u : 32u) >> 4, kBk16 = (kBk ? 32u : 2048u) >> 4;
+      const uint64_t a_desc0 = smem_desc_sw128(sb, kAmn ? 8192u : 16u, 1024u);
+      const uint64_t b_desc0 = smem_desc_sw128(sb + p.off_B, kBk ? 16u : 8192u, 1024u);
+      int stage = 0, abuf = 0;
+      uint32_t phase = 0, aphase = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        const XentTile t = tile(i);
+        if (!wt.wait<CG == 2>(bar + kXTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * BN);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wt.wait(bar + kXFull + 8 * stage, phase, SITE_MMA_FULL)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (T::kABytes >> 4));
+          const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage * (T::kBBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < BK / UMMA_K; ++k)
+            umma_f16<CG>(d, ad + kAk16 * k, bd + kBk16 * k, id, (kb > t.kb0 || k != 0) ? 1u : 0u);
+          umma_commit<CG>(bar + kXEmpty + 8 * stage);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit<CG>(bar + kXTmemFull + 8 * abuf);
+        abuf ^= 1;
+        if (abuf == 0) aphase ^= 1u;
+      }
+      if (ok) {
+        for (int i = 0; i < 2; ++i) {
+          if (!wt.wait<CG == 2>(bar + kXTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) break;
+          abuf ^= 1;
+          if (abuf == 0) aphase ^= 1u;
+        }
+      } else {
+        umma_commit<CG>(bar + kXDrain);
+        wt.drain(bar + kXDrain, 0u);
+      }
+    }
+  } else {
+    // --------------------------------------------------------- epilogue --
+    const int q = warp & 3;                   // TMEM lane quarter
+    const int grp = (warp - kEpi0) >> 2;      // takes column steps grp, grp + 2, ...
+    const int bid = 1 + grp;                  // the group's barrier
+    const bool storer = ((warp - kEpi0) & 3) == 0 && lane == 0;
+    const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
+    const int row = q * 32 + lane;            // of the CTA's 128 accumulator rows
+    const uint32_t sw = static_cast<uint32_t>(row & 7);
+    const uint32_t boxes = sb + p.off_out + grp * p.boxes * kXentBox;
+    int abuf = 0, step = 0;
+    uint32_t aphase = 0;
+    for (int i = 0; i < my_tiles; ++i) {
+      const XentTile t = tile(i);
+      const int m = t.mb * T::kMmaM + static_cast<int>(rank) * BM + row;
+      const int n0 = t.nb * BN;
+      const bool live = m < M;
+      // what the row needs, on its way while the tile's product finishes
+      int target = -1;
+      float lse2 = 0.f, out_scale = 0.f;
+      float2 coef = make_float2(0.f, 0.f);
+      if (MODE == X_STATS || MODE == X_DLOGIT) {
+        if (live) target = p.target[m] - p.b_row0 - n0;
+        if (MODE == X_DLOGIT && live) {
+          lse2 = p.lse2[m];
+          coef = p.coef[m];
+        }
+      }
+      if (MODE == X_OUT) out_scale = rows > 0 ? *p.out_scale : 0.f;
+      const bool got = wt.wait(bar + kXTmemFull + 8 * abuf, aphase, SITE_EPI_TMEM_FULL);
+      if (!group_agrees(bid, got)) break;
+      tc_fence_after();
+      const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN);
+      const int limit = p.N - n0;  // columns of the tile that exist
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t tb = bar + kXTmemEmpty + 8 * abuf;
+          if constexpr (CG == 2) mbar_arrive_remote(mapa_shared(tb, 0));
+          else mbar_arrive(tb);
+        }
+      };
+
+      if constexpr (MODE == X_STATS) {
+        float v[32];
+        auto read = [&](int c0) {
+          tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
+          tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+          tmem_wait_ld();
+        };
+        float top = -INFINITY;
+        for (int c0 = grp * 32; c0 < BN; c0 += 64) {
+          read(c0);
+          if (c0 + 32 > limit) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e >= limit) v[e] = p.c2 < 0.f ? INFINITY : -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e] * p.c2);
+          const int at = target - c0;
+          if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+            float x = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x = at == e ? v[e] : x;
+            if (at >= 0 && at < 32) p.at_target[m] = x * p.c;
+          }
+        }
+        const float off = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int c0 = grp * 32; c0 < BN; c0 += 64) {
+          read(c0);
+          if (c0 + 64 >= BN) release();
+          if (c0 + 32 > limit) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e >= limit) v[e] = p.c2 < 0.f ? INFINITY : -INFINITY;
+          }
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            s0 += ex2(fmaf(v[e], p.c2, -off));
+            s1 += ex2(fmaf(v[e + 1], p.c2, -off));
+            s2 += ex2(fmaf(v[e + 2], p.c2, -off));
+            s3 += ex2(fmaf(v[e + 3], p.c2, -off));
+          }
+          sum += (s0 + s1) + (s2 + s3);
+        }
+        if (live) p.stats[(2 * int64_t(t.nb) + grp) * p.M + m] = make_float2(top, sum);
+      } else {
+        constexpr int kStep = MODE == X_PART ? 32 : 64;  // columns of a box: 128 bytes
+        for (int c0 = grp * kStep; c0 < BN; c0 += 2 * kStep, ++step) {
+          uint32_t box = boxes;
+          if (p.boxes == 2) {
+            box += (step & 1) * kXentBox;
+            if (storer) bulk_wait_group_read<1>();
+          } else {
+            if (storer) bulk_wait_group_read<0>();
+          }
+          group_barrier(bid);  // the box has been read by its last store
+          const uint32_t line = box + row * 128;
+#pragma unroll
+          for (int h = 0; h < kStep; h += 32) {
+            float v[32];
+            tmem_ld16(acc + c0 + h, *reinterpret_cast<float(*)[16]>(v));
+            tmem_ld16(acc + c0 + h + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+            tmem_wait_ld();
+            if (h + 32 == kStep && c0 + 2 * kStep >= BN) release();
+            if constexpr (MODE == X_PART) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                st_shared16(line + ((static_cast<uint32_t>(j) ^ sw) << 4), __float_as_uint(v[4 * j]),
+                            __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                            __float_as_uint(v[4 * j + 3]));
+            } else {
+              if constexpr (MODE == X_DLOGIT) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], p.c2, -lse2)) * coef.x;
+                const int at = target - c0 - h;
+                if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (at == e) v[e] -= coef.y;
+                }
+                // rows and columns that do not exist read as 0 in the products to come
+                if (!live || c0 + h + 32 > limit) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!live || c0 + h + e >= limit) v[e] = 0.f;
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = rows > 0 ? v[e] * out_scale : 0.f;
+                const int col = n0 + c0 + h;
+                if (col + 32 > p.tma_cols && col < p.N && live) {
+                  uint16_t *o = p.out + (int64_t(p.b_row0) + m) * p.ld_out;
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (col + e >= p.tma_cols && col + e < p.N)
+                      o[col + e] = static_cast<uint16_t>(pack16(p.bf16, v[e], 0.f));
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                st_shared16(line + ((static_cast<uint32_t>(j + h / 8) ^ sw) << 4),
+                            pack16(p.bf16, v[8 * j], v[8 * j + 1]), pack16(p.bf16, v[8 * j + 2], v[8 * j + 3]),
+                            pack16(p.bf16, v[8 * j + 4], v[8 * j + 5]), pack16(p.bf16, v[8 * j + 6], v[8 * j + 7]));
+            }
+          }
+          fence_proxy_async_smem();
+          group_barrier(bid);
+          if (storer) {
+            const int x = n0 + c0;
+            const int y = t.mb * T::kMmaM + static_cast<int>(rank) * BM + (MODE == X_OUT ? p.b_row0 : 0);
+            // nothing is stored outside the tensor's columns: the box would be clipped whole
+            if (MODE == X_DLOGIT || x < (MODE == X_OUT ? p.tma_cols : p.N)) {
+              if (MODE == X_PART && p.accumulate) tma_reduce_add_3d(&p.tmOut, box, x, y, t.z);
+              else tma_store_3d(&p.tmOut, box, x, y, MODE == X_PART ? t.z : 0);
+            }
+            bulk_commit_group();
+          }
+        }
+      }
+      abuf ^= 1;
+      if (abuf == 0) aphase ^= 1u;
+    }
+    if (storer) bulk_wait_group<0>();
+    __syncwarp();
+  }
+
+  // ------------------------------------------------------------ teardown --
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG > 1) cluster_sync_all(); else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem_base, T::kTmemCols);
+  }
+}
+
+template <int CG, int BN>
+const void *pick_xent(int mode) {
+  switch (mode) {
+    case X_STATS: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_STATS>);
+    case X_DLOGIT: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_DLOGIT>);
+    case X_OUT: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_OUT>);
+    case X_PART: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_PART>);
+    default: return nullptr;
+  }
+}
+
+}  // namespace ge

@@ -393,6 +393,171 @@ void gemm_epi_plan_destroy(gemm_epi_plan *plan);
 /* Fill `info` with the plan's choices.  Errors: GE_ERR_INVALID. */
 int gemm_epi_plan_info(const gemm_epi_plan *plan, ge_plan_info *info);
 
+/*
+ * Vocabulary loss: softmax cross entropy of T hidden states against a
+ * vocabulary of V rows, without keeping the logits, and its gradients.
+ *
+ *   l     = logit_scale * H @ W^T            (T, V), fp32, never stored whole
+ *   lse_i = log sum_v exp(l_iv)
+ *   loss_i = weight_i * (lse_i - l_i,target_i + z_loss * lse_i^2)
+ *   total = sum_i loss_i                      (GE_XENT_SUM)
+ *         = sum_i loss_i / sum_i weight_i     (GE_XENT_MEAN; 0 if the weights sum to 0)
+ *   dl    = d(grad_scale * total) / dl,   dH = logit_scale * dl @ W,
+ *   dW    = logit_scale * dl^T @ H
+ *
+ * H is (T, D) with row pitch ldh, W is (V, D) with row pitch ldw, both of
+ * type `ab`; dH and dW have the same shapes and type with pitches lddh and
+ * lddw.  D is contiguous; pitches are multiples of 16 bytes and at least D;
+ * T, V and D need not be multiples of anything.
+ *
+ * A row whose target lies outside [0, V) (the customary ignore index among
+ * them) takes no part: its H may hold anything, NaN included, its loss_i and
+ * lse_i are 0, its row of dH is 0, its weight does not count.  Its products
+ * are not computed either: the rows that count are gathered on the device.
+ * A logit that is NaN or +infinity makes its row's loss NaN and reaches the
+ * gradients as in the formulas.
+ *
+ * Arithmetic: exact products summed in fp32, softmax statistics in fp32,
+ * sums over rows in fp64.  dl is rounded once to `ab` on its way into the
+ * gradient products, scaled by a power of two (found on the device) that
+ * keeps it clear of fp16's subnormals; dH and dW are summed in fp32 and rounded
+ * once.  Results are bit-for-bit repeatable for a given plan and device.
+ *
+ * The vocabulary is worked through in pieces, so that the 16-bit values kept
+ * between two kernels take at most buffer_bytes.
+ */
+typedef enum { GE_XENT_SUM = 0, GE_XENT_MEAN = 1 } ge_xent_reduction;
+typedef enum { GE_INDEX_I64 = 0, GE_INDEX_I32 = 1 } ge_index;
+
+typedef struct {
+  int32_t ab;           /* GE_F16 or GE_BF16: H, W, dH and dW                      */
+  int32_t index;        /* ge_index: type of the targets                           */
+  int32_t reduction;    /* ge_xent_reduction                                       */
+  int32_t timeout_ms;   /* 0 = 1000; bound on every device-side wait               */
+  int32_t max_ctas;     /* 0 = one CTA per SM, else a cap on the products' grids   */
+  float logit_scale;    /* 0 = 1                                                   */
+  float z_loss;         /* weight of lse^2; 0 = none                               */
+  int32_t reserved;     /* 0                                                       */
+  int64_t ldh, ldw;     /* row pitches in elements; 0 = D                          */
+  int64_t lddh, lddw;
+  int64_t buffer_bytes; /* 0 = 1 GiB; at least 256 columns for all T rows are kept */
+} ge_xent_desc;
+
+typedef struct gemm_epi_xent_plan gemm_epi_xent_plan;
+
+/*
+ * Validate and build a plan.  Host only (no device memory); not thread-safe,
+ * one plan per host thread, like the GEMM's.  Errors: GE_ERR_INVALID (NULL,
+ * bad option, non-finite scale), _UNSUPPORTED (types), _SHAPE (T, V or D
+ * <= 0 or above 2^31 - 1, a pitch below D), _MISALIGNED (a pitch that is not
+ * whole 16-byte units), _ARCH, _SMEM, _CUDA.
+ */
+int gemm_epi_xent_plan_create(gemm_epi_xent_plan **plan, int64_t T, int64_t V, int64_t D,
+                              const ge_xent_desc *desc);
+
+/* Bytes of caller-owned device workspace for _loss (grads == 0) or _step. */
+size_t gemm_epi_xent_workspace_bytes(const gemm_epi_xent_plan *plan, int grads);
+
+/*
+ * The loss alone (evaluation, scoring).
+ *   target   T indices;  weight   T floats or NULL (all 1)
+ *   loss, lse   T floats each;  total   one float; each may be NULL
+ * Asynchronous on `stream`, nothing synchronises or allocates; a run with
+ * the pointers of the previous one can be captured into a CUDA graph, and so can
+ * any other (its tensor maps travel with the launches).
+ * Errors: GE_ERR_INVALID, _MISSING_ARG (H, W or target NULL), _MISALIGNED
+ * (a pointer that is not 16-byte aligned), _WORKSPACE, _CUDA; a device-side
+ * timeout is reported later by gemm_epi_last_error.
+ */
+int gemm_epi_xent_loss(gemm_epi_xent_plan *plan, const void *H, const void *W, const void *target,
+                       const float *weight, float *loss, float *lse, float *total, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * The loss and its gradients: grad_scale is the gradient that arrives at
+ * `total` (1, or a loss scale).  Either of dH and dW may be NULL (a frozen
+ * side), not both (GE_ERR_MISSING_ARG).  The outputs must not overlap the
+ * inputs.  Otherwise as gemm_epi_xent_loss.
+ */
+int gemm_epi_xent_step(gemm_epi_xent_plan *plan, const void *H, const void *W, const void *target,
+                       const float *weight, float grad_scale, float *loss, float *lse,
+                       float *total, void *dH, void *dW, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+void gemm_epi_xent_plan_destroy(gemm_epi_xent_plan *plan);
+
+/*
+ * Norms around a block, fused with its gate and residual scale: the output
+ * b of a block joins the residual stream x, and the stream is normalised for
+ * the next block, in one pass.
+ *
+ *   y = x + alpha * gate[row / rows_per_gate] * (N_post(b) * w_post)
+ *   h = N_pre(y) * w_pre                     (y before its rounding)
+ *   N of a row v: GE_NORM_NONE  v
+ *                 GE_NORM_RMS   v / sqrt(mean(v^2) + eps)
+ *                 GE_NORM_LAYER (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps)
+ *
+ * x, b, y, h and their gradients are (T, D) of type `x` with row pitches
+ * ldx, ldb, ldy, ldh; gate is (ceil(T / rows_per_gate), D), packed, w_post and w_pre
+ * (D,), all three and their gradients of type `w`.  rows_per_gate 1 is a
+ * gate for every row, the sequence length one per sequence, T one for all.
+ * Any D up to GE_NORM_MAX_D and any pitch: rows that are whole 16-byte units are
+ * moved 16 bytes at a time, others element by element.  Arithmetic in fp32,
+ * one rounding per output.
+ */
+typedef enum { GE_NORM_NONE = 0, GE_NORM_RMS = 1, GE_NORM_LAYER = 2 } ge_norm_kind;
+#define GE_NORM_MAX_D 32768
+
+typedef struct {
+  int32_t x;               /* GE_F16, GE_BF16 or GE_F32                              */
+  int32_t w;               /* GE_F16, GE_BF16 or GE_F32                              */
+  int32_t pre;             /* GE_NORM_RMS or GE_NORM_LAYER                           */
+  int32_t post;            /* ge_norm_kind                                           */
+  float eps_pre, eps_post; /* >= 0                                                   */
+  float alpha;             /* residual scale                                         */
+  int32_t reserved;        /* 0                                                      */
+  int64_t rows_per_gate;   /* 0: no gate                                             */
+  int64_t ldx, ldb, ldy, ldh; /* row pitches in elements; 0 = D                      */
+} ge_norm_desc;
+
+typedef struct gemm_epi_norm_plan gemm_epi_norm_plan;
+
+/* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID (NULL, bad kind or
+ * option), _UNSUPPORTED (types), _SHAPE (T or D <= 0, D above GE_NORM_MAX_D, T above 2^31 - 1,
+ * a pitch below D), _ARCH, _CUDA. */
+int gemm_epi_norm_plan_create(gemm_epi_norm_plan **plan, int64_t T, int64_t D,
+                              const ge_norm_desc *desc);
+
+/* Bytes of caller-owned device workspace for gemm_epi_norm_grad. */
+size_t gemm_epi_norm_workspace_bytes(const gemm_epi_norm_plan *plan);
+
+/*
+ * One launch on `stream`.  b NULL: y = x (the first norm of a network).
+ * gate must be given exactly when rows_per_gate > 0 and b is given; w_post
+ * (post not GE_NORM_NONE) and w_pre may be NULL (all 1); y or h may be NULL
+ * (not both).  y may be x or b, h may be b: a row is read whole before it is written.
+ * Errors: GE_ERR_INVALID, _MISSING_ARG, _MISALIGNED, _CUDA.
+ */
+int gemm_epi_norm_run(gemm_epi_norm_plan *plan, const void *x, const void *b, const void *gate,
+                      const void *w_post, const void *w_pre, void *y, void *h, void *stream);
+
+/*
+ * The gradients, from dy (what arrives at y from the stream; NULL: 0), dh
+ * (what arrives at h), and y and b as the forward pass read and wrote them;
+ * row statistics are computed again from the rows, which are read anyway.
+ *   dx = dy + dN_pre(dh * w_pre)    db = d(N_post)(alpha * gate * w_post * dx)
+ *   dgate, dw_post, dw_pre: sums over the rows that share them
+ * b NULL: dx (and dw_pre) alone.  db, dgate, dw_post and dw_pre may be NULL.  Two
+ * launches; sums over rows run in a fixed order, no atomics.  dx may be dy or dh, db may be
+ * b or dh, dx and db not the same.  Errors: as gemm_epi_norm_run, and GE_ERR_WORKSPACE.
+ */
+int gemm_epi_norm_grad(gemm_epi_norm_plan *plan, const void *dy, const void *dh, const void *y,
+                       const void *b, const void *gate, const void *w_post, const void *w_pre,
+                       void *dx, void *db, void *dgate, void *dw_post, void *dw_pre,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+void gemm_epi_norm_plan_destroy(gemm_epi_norm_plan *plan);
+
 /* Static name of a status code ("GE_OK", ...); never NULL. */
 const char *gemm_epi_status_string(int status);
 
