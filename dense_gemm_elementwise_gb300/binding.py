@@ -48,7 +48,7 @@ GE_MAX_GROUPS = 4096
 GE_XENT_SUM, GE_XENT_MEAN = 0, 1
 GE_INDEX_I64, GE_INDEX_I32 = 0, 1
 GE_NORM_NONE, GE_NORM_RMS, GE_NORM_LAYER = 0, 1, 2
-GE_NORM_MAX_D = 32768
+GE_NORM_MAX_D = 16384
 REDUCTION = {"sum": GE_XENT_SUM, "mean": GE_XENT_MEAN}
 INDEX = {"i64": GE_INDEX_I64, "i32": GE_INDEX_I32}
 NORM = {"none": GE_NORM_NONE, "rms": GE_NORM_RMS, "layer": GE_NORM_LAYER}

@@ -18,7 +18,7 @@ OBJ = os.path.join(HERE, "_build")
 LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libgemm_epi.so")
 UNITS = ["plan", "unfused", "jit", "k_cg1_n64", "k_cg1_n128", "k_cg1_n256", "k_cg2_n128", "k_cg2_n256",
-         "norm", "xent", "k_xent_cg1", "k_xent_cg2"]
+         "norm", "k_norm_run", "k_norm_grad", "k_norm_grad_whole", "xent", "k_xent_cg1", "k_xent_cg2"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

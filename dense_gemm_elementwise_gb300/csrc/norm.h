@@ -1,0 +1,38 @@
+// norm.h -- parameters and handles of the norms around a block.
+#pragma once
+
+#include <stdint.h>
+
+namespace ge {
+
+constexpr int kChunk = 8;        // columns a thread holds per chunk
+constexpr int kMaxThreads = 1024;
+constexpr int kMaxAhead = 3;     // rows in the ring of a thread
+constexpr int kSumBytes = 2 * (kMaxThreads / 32) * 16;  // shared memory of the rows' sums
+
+struct NormParams {
+  const void *x, *b, *gate, *w_post, *w_pre;
+  void *y, *h;
+  // gradients
+  const void *dy, *dh, *yin;
+  void *dx, *db, *dgate;
+  float *part_pre, *part_post;  // [units][D]
+  int64_t ldx, ldb, ldy, ldh;
+  int64_t rows_per_gate;
+  int32_t T, D, wt;
+  int32_t pre, post;
+  float eps_pre, eps_post, alpha, inv_d;
+  int32_t row_threads;   // threads that share a row: a power of two up to 32, or whole warps
+  int32_t ahead;         // rows of the ring
+  int32_t keep_w;        // the factors of a column are kept in shared memory
+  int32_t w_vec;         // rows of gate and the vectors are whole 16-byte units
+  // units of the gradient pass
+  int32_t units, rows_per_unit, units_per_group;  // units_per_group 0: a unit holds whole groups
+};
+
+// nv chunks per thread (1 or 2); vec: rows are whole 16-byte units
+const void *norm_kernel_run(int dt, int nv, bool vec);
+const void *norm_kernel_grad(int dt, int nv, bool vec);
+const void *norm_kernel_grad_whole(int dt, int nv, bool vec);  // units hold whole gate groups
+
+}  // namespace ge

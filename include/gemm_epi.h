@@ -506,7 +506,7 @@ void gemm_epi_xent_plan_destroy(gemm_epi_xent_plan *plan);
  * one rounding per output.
  */
 typedef enum { GE_NORM_NONE = 0, GE_NORM_RMS = 1, GE_NORM_LAYER = 2 } ge_norm_kind;
-#define GE_NORM_MAX_D 32768
+#define GE_NORM_MAX_D 16384
 
 typedef struct {
   int32_t x;               /* GE_F16, GE_BF16 or GE_F32                              */
