@@ -1,7 +1,8 @@
 #include "norm_kernel.cuh"
 namespace ge {
-const void *norm_kernel_grad_whole(int dt, int nv, bool vec) {
-  if (nv == 1) return vec ? pick_grad<1, true, true>(dt) : pick_grad<1, false, true>(dt);
-  return vec ? pick_grad<2, true, true>(dt) : pick_grad<2, false, true>(dt);
+const void *norm_kernel_grad_whole(int dt, int nv, int threads, bool vec) {
+  if (vec) return nv == 1 ? pick_grad<1, P_RING, kVecThreads, true>(dt) : nv == 2 ? pick_grad<2, P_RING, kVecThreads, true>(dt) : pick_grad<4, P_DIRECT, kVecThreads, true>(dt);
+  if (nv == 1) return threads <= kVecThreads ? pick_grad<1, P_STRIDED, kVecThreads, true>(dt) : pick_grad<1, P_STRIDED, kMaxThreads, true>(dt);
+  return pick_grad<2, P_STRIDED, kMaxThreads, true>(dt);
 }
 }  // namespace ge

@@ -18,66 +18,82 @@ using namespace ge;
 namespace {
 
 // Adds the units' partial rows.  grid.y 0: dw_pre and dw_post; grid.y 1 + g: the
-// gate of group g (units that hold part of one group).  Each of the 32 threads
-// of a column adds every 32nd unit, then the 32 sums are added in order.
+// gate of group g (units that hold part of one group).  A thread adds every 32nd unit
+// of four columns, then the 32 sums of a column are added in order.  It is bound by the
+// latency of its loads: 16 bytes at a time and four units ahead.
 struct SumParams {
   const float *part_pre, *part_post;
+  int64_t ld_part;
   const void *gate, *w_post;
   void *dgate, *dw_post, *dw_pre;
   float alpha;
   int32_t D, wt, units, units_per_group;
 };
 
-constexpr int kSumCols = 32, kSumLanes = 32;
+constexpr int kSumCols = 32, kSumQuads = kSumCols / 4, kSumLanes = 32;
 
-__global__ void __launch_bounds__(kSumCols *kSumLanes) norm_sum_kernel(const __grid_constant__ SumParams p) {
+__global__ void __launch_bounds__(kSumQuads *kSumLanes) norm_sum_kernel(const __grid_constant__ SumParams p) {
   __shared__ float part[2][kSumLanes][kSumCols + 1];
   griddep_wait();
   griddep_launch_dependents();
-  const int col = blockIdx.x * kSumCols + threadIdx.x, lane = threadIdx.y;
+  const int quad = threadIdx.x % kSumQuads, lane = threadIdx.x / kSumQuads;
+  const int col = blockIdx.x * kSumCols + quad * 4;
+  // rows of partial sums are padded to whole quads of columns
   const bool on = col < p.D;
-  float a = 0.f, b = 0.f;
+  float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+  auto add = [](float (&s)[4], const float4 &v) { s[0] += v.x, s[1] += v.y, s[2] += v.z, s[3] += v.w; };
   if (blockIdx.y == 0) {
-    for (int u = lane; on && u < p.units; u += kSumLanes) {
-      const int64_t at = int64_t(u) * p.D + col;
-      if (p.dw_pre) a += p.part_pre[at];
-      if (p.dw_post) {
-        const float q = p.part_post[at];
-        // units of whole groups have their gates in the sum already
-        b += p.gate && p.units_per_group ? q * getw(p.wt, p.gate, int64_t(u / p.units_per_group) * p.D + col) : q;
+    const bool pre = p.dw_pre != nullptr, post = p.dw_post != nullptr;
+    const bool gated = p.gate && p.units_per_group;  // units of whole groups have their gates in the sum already
+#pragma unroll 4
+    for (int u = lane; u < (on ? p.units : 0); u += kSumLanes) {
+      const int64_t at = int64_t(u) * p.ld_part + col;
+      if (pre) add(a, *reinterpret_cast<const float4 *>(p.part_pre + at));
+      if (post) {
+        float4 q = *reinterpret_cast<const float4 *>(p.part_post + at);
+        if (gated) {
+          const int64_t g = int64_t(u / p.units_per_group) * p.D;
+          q.x *= getw(p.wt, p.gate, g + col);
+          q.y *= getw(p.wt, p.gate, g + min(col + 1, p.D - 1));
+          q.z *= getw(p.wt, p.gate, g + min(col + 2, p.D - 1));
+          q.w *= getw(p.wt, p.gate, g + min(col + 3, p.D - 1));
+        }
+        add(b, q);
       }
     }
   } else {
-    const int g = blockIdx.y - 1;
-    for (int s = lane; on && s < p.units_per_group; s += kSumLanes) {
-      const int u = g * p.units_per_group + s;
-      a += p.part_post[int64_t(u) * p.D + col];
-    }
+    const int64_t first = int64_t(blockIdx.y - 1) * p.units_per_group;
+#pragma unroll 4
+    for (int s = lane; s < (on ? p.units_per_group : 0); s += kSumLanes)
+      add(a, *reinterpret_cast<const float4 *>(p.part_post + (first + s) * p.ld_part + col));
   }
-  part[0][lane][threadIdx.x] = a;
-  part[1][lane][threadIdx.x] = b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    part[0][lane][quad * 4 + i] = a[i];
+    part[1][lane][quad * 4 + i] = b[i];
+  }
   __syncthreads();
-  if (lane || !on) return;
-  a = b = 0.f;
-  for (int l = 0; l < kSumLanes; ++l) {
-    a += part[0][l][threadIdx.x];
-    b += part[1][l][threadIdx.x];
-  }
+  if (threadIdx.x >= 2 * kSumCols) return;
+  const int which = threadIdx.x / kSumCols, c = threadIdx.x % kSumCols, at = blockIdx.x * kSumCols + c;
+  if (at >= p.D) return;
+  float s = 0.f;
+#pragma unroll
+  for (int l = 0; l < kSumLanes; ++l) s += part[which][l][c];
   if (blockIdx.y == 0) {
-    if (p.dw_pre) putw(p.wt, p.dw_pre, col, a);
-    if (p.dw_post) putw(p.wt, p.dw_post, col, p.alpha * b);
-  } else {
-    const float w = p.w_post ? getw(p.wt, p.w_post, col) : 1.f;
-    putw(p.wt, p.dgate, int64_t(blockIdx.y - 1) * p.D + col, p.alpha * w * a);
+    if (which == 0 && p.dw_pre) putw(p.wt, p.dw_pre, at, s);
+    if (which == 1 && p.dw_post) putw(p.wt, p.dw_post, at, p.alpha * s);
+  } else if (which == 0) {
+    const float w = p.w_post ? getw(p.wt, p.w_post, at) : 1.f;
+    putw(p.wt, p.dgate, int64_t(blockIdx.y - 1) * p.D + at, p.alpha * w * s);
   }
 }
 
 enum NormPass { PASS_RUN = 0, PASS_GRAD = 1, PASS_GRAD_WHOLE = 2 };
 
-const void *pick_kernel(int dt, int nv, bool vec, int pass) {
-  return pass == PASS_RUN    ? norm_kernel_run(dt, nv, vec)
-         : pass == PASS_GRAD ? norm_kernel_grad(dt, nv, vec)
-                             : norm_kernel_grad_whole(dt, nv, vec);
+const void *pick_kernel(int dt, int nv, int threads, bool vec, int pass) {
+  return pass == PASS_RUN    ? norm_kernel_run(dt, nv, threads, vec)
+         : pass == PASS_GRAD ? norm_kernel_grad(dt, nv, threads, vec)
+                             : norm_kernel_grad_whole(dt, nv, threads, vec);
 }
 
 bool valid_type(int t) { return t == GE_F16 || t == GE_BF16 || t == GE_F32; }
@@ -87,7 +103,7 @@ int64_t size_of(int t) { return t == GE_F32 ? 4 : 2; }
 // rows of the ring.
 struct RowShape {
   const void *fn = nullptr;
-  int nv = 1, row_threads = 32, threads = 32, grid = 1, ahead = 1, keep_w = 0, smem = 0;
+  int nv = 1, row_threads = 32, threads = 32, grid = 1, ahead = 1, smem = 0;
 };
 
 cudaError_t launch(const void *fn, dim3 grid, dim3 block, int smem, void *params, cudaStream_t s) {
@@ -120,34 +136,44 @@ namespace {
 
 int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out) {
   const int chunks = static_cast<int>(ceil_div(pl->D, kChunk));
+  const int tensors = pass == PASS_RUN ? 2 : 4;
   RowShape r;
-  // one chunk per thread while a row fits a CTA's threads, then more; rows of
-  // up to a warp's chunks share warps
-  r.nv = chunks <= kMaxThreads ? 1 : 2;
+  // Rows of whole 16-byte units: two chunks per thread spread the cost of the row's sums (shuffles, a
+  // barrier) over 16 columns, but rows too few to fill the GPU, and rows of
+  // up to a warp's chunks, take one; what 512 threads cannot hold so takes four.
+  // Rows of other units: one up to 1024 threads, since each element has a register
+  // of its own on its way.
+  const bool vec = pl->vec;
+  const int64_t few = 4 * int64_t(pl->sms);
+  if (vec) r.nv = chunks <= 32 || (pl->T <= few && chunks <= kVecThreads) ? 1 : (chunks <= 2 * kVecThreads ? 2 : 4);
+  else r.nv = chunks <= kMaxThreads ? 1 : 2;
   const int want = static_cast<int>(ceil_div(chunks, r.nv));
   r.row_threads = static_cast<int>(round_up(want, 32));
-  if (want < 32) {
+  if (want < 32) {  // rows share warps
     r.row_threads = 1;
     while (r.row_threads < want) r.row_threads *= 2;
   }
-  const int rows = std::max(1, 256 / r.row_threads);
-  r.threads = r.row_threads * rows;
-  // shared memory: factors in fp32 if they leave room for a row, then as many rows
-  // as let two CTAs share an SM
-  const int factors = r.threads * r.nv * 4 * 16;
-  const int per_row = r.threads * r.nv * (pass == PASS_RUN ? 2 : 4) * static_cast<int>(size_of(pl->d.x)) * kChunk;
-  // rows too wide for that (fp32 gradients) are read as rows of odd units are
-  const bool vec = pl->vec && kSumBytes + per_row <= max_smem;
-  r.fn = pick_kernel(pl->d.x, r.nv, vec, pass);
-  r.keep_w = kSumBytes + factors + (vec ? per_row : 0) <= max_smem;
-  const int fixed = kSumBytes + (r.keep_w ? factors : 0);
+  // several short rows to a CTA of up to 256 threads, once there are enough of them
+  // for every SM; whole warps
+  int64_t cta_rows = std::max(1, 256 / r.row_threads);
+  cta_rows = std::min<int64_t>(cta_rows, std::max<int64_t>(ceil_div(pl->T, few), r.row_threads < 32 ? 32 / r.row_threads : 1));
+  if (r.row_threads < 32) cta_rows = round_up(cta_rows, 32 / r.row_threads);
+  r.threads = r.row_threads * static_cast<int>(cta_rows);
+  const int rows = r.threads / r.row_threads;
+  r.fn = pick_kernel(pl->d.x, r.nv, r.threads, vec, pass);
+  // shared memory: sums, factors in fp32, and as many rows of the ring as let two CTAs
+  // (three of the forward pass) share an SM, one at least: 512 threads' fp32 rows and
+  // factors take 224 KiB
+  const int fixed = kSumBytes + r.threads * r.nv * (pass == PASS_GRAD_WHOLE ? 6 : 4) * 16;
+  const int per_row = r.threads * r.nv * tensors * static_cast<int>(size_of(pl->d.x)) * kChunk;
   r.ahead = 1;
   r.smem = fixed;
-  if (vec) {
-    const int room = r.threads <= kMaxThreads / 2 ? max_smem / 2 : max_smem;
+  if (vec && r.nv < 4) {
+    const int room = max_smem / std::max(1, std::min(pass == PASS_RUN ? 3 : 2, 768 / r.threads));
     while (r.ahead < kMaxAhead && fixed + (r.ahead + 1) * per_row <= room) ++r.ahead;
     r.smem = fixed + r.ahead * per_row;
   }
+  if (r.smem > max_smem) return GE_ERR_SMEM;
   int per_sm = 0;
   if (cudaFuncSetAttribute(r.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, r.fn, r.threads, static_cast<size_t>(r.smem)) !=
@@ -164,7 +190,6 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
 void set_shape(NormParams *p, const RowShape &r) {
   p->row_threads = r.row_threads;
   p->ahead = r.ahead;
-  p->keep_w = r.keep_w;
 }
 
 // Units of the gradient pass: as many as the GPU holds at once, rounded so that
@@ -251,14 +276,14 @@ int gemm_epi_norm_plan_create(gemm_epi_norm_plan **plan, int64_t T, int64_t D, c
   p.T = static_cast<int32_t>(T);
   p.D = static_cast<int32_t>(D);
   p.wt = d.w;
+  p.w_vec = (D * size_of(d.w)) % 16 == 0;
+  p.ld_part = round_up(D, 8);
   p.pre = d.pre;
   p.post = d.post;
   p.eps_pre = d.eps_pre;
   p.eps_post = d.eps_post;
   p.alpha = d.alpha;
   p.inv_d = static_cast<float>(1.0 / static_cast<double>(D));
-  // 8 columns from a multiple of 8: two words of fp32, one of 16-bit types
-  p.w_vec = (D * size_of(d.w)) % 16 == 0;
   share_rows(pl);
   if (p.units_per_group == 0) st = shape_of(pl, PASS_GRAD_WHOLE, smem, &pl->bwd);
   if (st != GE_OK) {
@@ -273,7 +298,7 @@ void gemm_epi_norm_plan_destroy(gemm_epi_norm_plan *plan) { delete plan; }
 
 size_t gemm_epi_norm_workspace_bytes(const gemm_epi_norm_plan *pl) {
   if (!pl) return 0;
-  return 2u * sizeof(float) * static_cast<size_t>(pl->p.units) * static_cast<size_t>(pl->D);
+  return 2u * sizeof(float) * static_cast<size_t>(pl->p.units) * static_cast<size_t>(pl->p.ld_part);
 }
 
 int gemm_epi_norm_run(gemm_epi_norm_plan *pl, const void *x, const void *b, const void *gate,
@@ -340,7 +365,7 @@ int gemm_epi_norm_grad(gemm_epi_norm_plan *pl, const void *dy, const void *dh, c
   p.dgate = dgate;
   set_shape(&p, pl->bwd);
   p.part_pre = static_cast<float *>(workspace);
-  p.part_post = b ? p.part_pre + static_cast<size_t>(p.units) * static_cast<size_t>(pl->D) : nullptr;
+  p.part_post = b ? p.part_pre + static_cast<size_t>(p.units) * static_cast<size_t>(p.ld_part) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int lanes = pl->bwd.threads / pl->bwd.row_threads;
   const int grid = static_cast<int>(ceil_div(p.units, lanes));
@@ -351,6 +376,7 @@ int gemm_epi_norm_grad(gemm_epi_norm_plan *pl, const void *dy, const void *dh, c
   std::memset(static_cast<void *>(&q), 0, sizeof(q));
   q.part_pre = p.part_pre;
   q.part_post = p.part_post;
+  q.ld_part = p.ld_part;
   q.gate = gate;
   q.w_post = w_post;
   q.dgate = dgate;
@@ -364,7 +390,7 @@ int gemm_epi_norm_grad(gemm_epi_norm_plan *pl, const void *dy, const void *dh, c
   const int groups = gates ? p.units / p.units_per_group : 0;
   const cudaError_t e = launch(reinterpret_cast<const void *>(norm_sum_kernel),
                                dim3(static_cast<unsigned>(ceil_div(p.D, kSumCols)), static_cast<unsigned>(1 + groups)),
-                               dim3(kSumCols, kSumLanes), 0, &q, s);
+                               dim3(kSumQuads * kSumLanes), 0, &q, s);
   return e == cudaSuccess ? GE_OK : GE_ERR_CUDA;
 }
 

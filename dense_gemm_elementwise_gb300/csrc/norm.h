@@ -6,7 +6,12 @@
 namespace ge {
 
 constexpr int kChunk = 8;        // columns a thread holds per chunk
-constexpr int kMaxThreads = 1024;
+constexpr int kVecThreads = 512;   // threads of a CTA whose rows are whole 16-byte units, at most
+constexpr int kMaxThreads = 1024;  // ... of other rows
+// The forward pass is held to the registers of a CTA of 768 (85), so that three CTAs of 256 share
+// an SM: 8192 x 4096 bf16 in 47.0 us against 48.9 with two.  The gradients keep 128
+// (222 us against 306 for 16384 x 4096, whose sums then spill).
+constexpr int kRunBound = 768;
 constexpr int kMaxAhead = 3;     // rows in the ring of a thread
 constexpr int kSumBytes = 2 * (kMaxThreads / 32) * 16;  // shared memory of the rows' sums
 
@@ -16,7 +21,8 @@ struct NormParams {
   // gradients
   const void *dy, *dh, *yin;
   void *dx, *db, *dgate;
-  float *part_pre, *part_post;  // [units][D]
+  float *part_pre, *part_post;  // [units][ld_part]
+  int64_t ld_part;
   int64_t ldx, ldb, ldy, ldh;
   int64_t rows_per_gate;
   int32_t T, D, wt;
@@ -24,15 +30,15 @@ struct NormParams {
   float eps_pre, eps_post, alpha, inv_d;
   int32_t row_threads;   // threads that share a row: a power of two up to 32, or whole warps
   int32_t ahead;         // rows of the ring
-  int32_t keep_w;        // the factors of a column are kept in shared memory
-  int32_t w_vec;         // rows of gate and the vectors are whole 16-byte units
+  int32_t w_vec;         // gate's rows and the vectors are whole 16-byte units
   // units of the gradient pass
   int32_t units, rows_per_unit, units_per_group;  // units_per_group 0: a unit holds whole groups
 };
 
-// nv chunks per thread (1 or 2); vec: rows are whole 16-byte units
-const void *norm_kernel_run(int dt, int nv, bool vec);
-const void *norm_kernel_grad(int dt, int nv, bool vec);
-const void *norm_kernel_grad_whole(int dt, int nv, bool vec);  // units hold whole gate groups
+// nv chunks per thread; threads of a CTA; vec: rows are whole 16-byte units (nv 1 and 2
+// with a ring, 4 without; else 1 or 2)
+const void *norm_kernel_run(int dt, int nv, int threads, bool vec);
+const void *norm_kernel_grad(int dt, int nv, int threads, bool vec);
+const void *norm_kernel_grad_whole(int dt, int nv, int threads, bool vec);  // units hold whole gate groups
 
 }  // namespace ge

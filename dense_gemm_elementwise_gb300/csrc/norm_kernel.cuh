@@ -39,11 +39,23 @@ template <> struct Elem<GE_F16> {
   using T = __half;
   static __device__ __forceinline__ float get(T v) { return __half2float(v); }
   static __device__ __forceinline__ T put(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ float2 get2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2 *>(&v)); }
+  static __device__ __forceinline__ uint32_t put2(float2 v) {
+    const __half2 h = __float22half2_rn(v);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
 };
 template <> struct Elem<GE_BF16> {
   using T = __nv_bfloat16;
   static __device__ __forceinline__ float get(T v) { return __bfloat162float(v); }
   static __device__ __forceinline__ T put(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ float2 get2(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+  static __device__ __forceinline__ uint32_t put2(float2 v) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    return *reinterpret_cast<const uint32_t *>(&h);
+  }
 };
 template <> struct Elem<GE_F32> {
   using T = float;
@@ -51,49 +63,68 @@ template <> struct Elem<GE_F32> {
   static __device__ __forceinline__ T put(float v) { return v; }
 };
 
-// Which columns a thread holds.  Rows of whole 16-byte units: 8 in a run, moved
-// 16 bytes at a time.  Other rows: every row_threads-th column, so that the
-// threads of a warp read neighbouring elements (8 in a run would have each
-// load touch four times the cache lines; 3001 x 1111 fp16 took 20.7 us so).
-template <bool kVec>
+// Two fp32 operations per instruction: these kernels do about 40 for every
+// element of 2 bytes, and the instructions issued were what bound them (0.7
+// of the schedulers' slots at 0.6 of the memory's rate).
+union Pair { float2 f; unsigned long long u; };
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  Pair x{a}, y{b}, z{c}, r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(x.u), "l"(y.u), "l"(z.u));
+  return r.f;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  Pair x{a}, y{b}, r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
+  return r.f;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  Pair x{a}, y{b}, r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(x.u), "l"(y.u));
+  return r.f;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+constexpr int kPairs = kChunk / 2;
+
+// How a thread reaches its columns.
+//   P_RING     rows of whole 16-byte units: 8 columns in a run, moved 16 bytes at
+//              a time, rows on their way in a ring in shared memory
+//   P_DIRECT   the same for rows too wide for a ring, read when they are wanted
+//              (each thread then has 8 or 16 loads in flight)
+//   P_STRIDED  other rows: every row_threads-th column, so that the threads of a
+//              warp read neighbouring elements (8 in a run would have each load
+//              touch four times the cache lines)
+enum Path { P_RING = 0, P_DIRECT = 1, P_STRIDED = 2 };
+
+template <int PATH>
 struct Columns {
   int t, per;
   __device__ __forceinline__ int operator()(int k, int i) const {
-    return kVec ? (t + k * per) * kChunk + i : (k * kChunk + i) * per + t;
+    return PATH == P_STRIDED ? (k * kChunk + i) * per + t : (t + k * per) * kChunk + i;
   }
 };
 
-template <int DT, int NV, bool kVec>
-__device__ __forceinline__ void load_row(const void *base, int64_t off, const Columns<kVec> &col, int D, bool on,
-                                         float (&v)[NV][kChunk]) {
+// row: the row's first element
+template <int DT, int NV, int PATH>
+__device__ __forceinline__ void store_row(typename Elem<DT>::T *row, const Columns<PATH> &col, int D,
+                                          const float2 (&v)[NV][kPairs]) {
   using E = Elem<DT>;
-  const typename E::T *p = static_cast<const typename E::T *>(base) + off;
-  if (!on) D = 0;
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[k][i] = col(k, i) < D ? E::get(p[col(k, i)]) : 0.f;
-}
-
-template <int DT, int NV, bool kVec>
-__device__ __forceinline__ void store_row(void *base, int64_t off, const Columns<kVec> &col, int D,
-                                          const float (&v)[NV][kChunk]) {
-  using E = Elem<DT>;
-  using T = typename E::T;
-  T *p = static_cast<T *>(base) + off;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if (kVec && col(k, 0) + kChunk <= D) {
-      constexpr int kWords = kChunk * sizeof(T) / 16;
-      union { uint4 w[kWords]; T e[kChunk]; } u;
+    if (PATH != P_STRIDED && col(k, 0) + kChunk <= D) {
+      uint4 *q = reinterpret_cast<uint4 *>(row + col(k, 0));
+      if constexpr (DT == GE_F32) {
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) u.e[i] = E::put(v[k][i]);
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint4 *>(p + col(k, 0))[i] = u.w[i];
+        for (int j = 0; j < 2; ++j)
+          q[j] = make_uint4(__float_as_uint(v[k][2 * j].x), __float_as_uint(v[k][2 * j].y),
+                            __float_as_uint(v[k][2 * j + 1].x), __float_as_uint(v[k][2 * j + 1].y));
+      } else {
+        *q = make_uint4(E::put2(v[k][0]), E::put2(v[k][1]), E::put2(v[k][2]), E::put2(v[k][3]));
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < kChunk; ++i)
-        if (col(k, i) < D) p[col(k, i)] = E::put(v[k][i]);
+        if (col(k, i) < D) row[col(k, i)] = E::put(i & 1 ? v[k][i / 2].y : v[k][i / 2].x);
     }
   }
 }
@@ -111,117 +142,186 @@ __device__ __forceinline__ void putw(int wt, void *base, int64_t i, float v) {
   else static_cast<float *>(base)[i] = v;
 }
 
-// w[k][i] = base[off + column], 1 where base is NULL, 0 past the end
-template <int NV, bool kVec>
-__device__ __forceinline__ void load_w(const NormParams &p, const void *base, int64_t off, const Columns<kVec> &col,
-                                       float (&w)[NV][kChunk]) {
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if (kVec && base && p.w_vec && col(k, 0) < p.D) {
-      if (p.wt == GE_F32) {
-        const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off + col(k, 0));
-        const float4 a = q[0], b = col(k, 4) < p.D ? q[1] : make_float4(0.f, 0.f, 0.f, 0.f);
-        w[k][0] = a.x, w[k][1] = a.y, w[k][2] = a.z, w[k][3] = a.w;
-        w[k][4] = b.x, w[k][5] = b.y, w[k][6] = b.z, w[k][7] = b.w;
-      } else {
-        union { uint4 v; __half h[8]; __nv_bfloat16 b[8]; } u;
-        u.v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off + col(k, 0));
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-          w[k][i] = p.wt == GE_F16 ? __half2float(u.h[i]) : __bfloat162float(u.b[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i)
-        w[k][i] = col(k, i) < p.D ? (base ? getw(p.wt, base, off + col(k, i)) : 1.f) : 0.f;
-    }
-  }
-}
-
-// Shared memory of a thread's own: `threads` 16-byte words side by side, so
-// that a warp's accesses are free of conflicts, and no barrier: nobody else
-// reads them.
+// Factors of a thread's columns, kept in fp32 in shared memory of its own:
+// `threads` 16-byte words side by side, so that a warp's accesses are free of
+// conflicts, and no barrier: nobody else reads them.
 struct Own {
-  uint4 *base;   // this thread's first word
+  float4 *base;   // this thread's first word
   int threads;
   template <int NV>
-  __device__ __forceinline__ void put(const float (&w)[NV][kChunk]) const {
+  __device__ __forceinline__ void put(const float2 (&w)[NV][kPairs]) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        reinterpret_cast<float4 *>(base)[(2 * k + j) * threads] =
-            make_float4(w[k][4 * j], w[k][4 * j + 1], w[k][4 * j + 2], w[k][4 * j + 3]);
+        base[(2 * k + j) * threads] = make_float4(w[k][2 * j].x, w[k][2 * j].y, w[k][2 * j + 1].x, w[k][2 * j + 1].y);
   }
-  // the same factors, multiplied into v
   template <int NV>
-  __device__ __forceinline__ void times(float (&v)[NV][kChunk]) const {
+  __device__ __forceinline__ void get(float2 (&w)[NV][kPairs]) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float4 f = reinterpret_cast<const float4 *>(base)[(2 * k + j) * threads];
-        v[k][4 * j] *= f.x, v[k][4 * j + 1] *= f.y, v[k][4 * j + 2] *= f.z, v[k][4 * j + 3] *= f.w;
+        const float4 f = base[(2 * k + j) * threads];
+        w[k][2 * j] = make_float2(f.x, f.y);
+        w[k][2 * j + 1] = make_float2(f.z, f.w);
       }
+  }
+  template <int NV>
+  __device__ __forceinline__ void times(float2 (&v)[NV][kPairs]) const {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float4 f = base[(2 * k + j) * threads];
+        v[k][2 * j] = mul2(v[k][2 * j], make_float2(f.x, f.y));
+        v[k][2 * j + 1] = mul2(v[k][2 * j + 1], make_float2(f.z, f.w));
+      }
+  }
+  // scale * a[off + column] (times what is there, with `into`), 0 past the end; a
+  // vector that is NULL counts as 1.
+  // Not inlined: it runs once for many rows, and its instructions would crowd
+  // out the others'; one chunk at a time, to leave the callers their registers.
+  template <int NV, int PATH>
+  __device__ __noinline__ void fill(const NormParams &p, const Columns<PATH> &col, float scale, const void *a,
+                                    int64_t off, bool into = false) const {
+#pragma unroll 1
+    for (int k = 0; k < NV; ++k) {
+      float f[kChunk];
+      if (!a) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) f[i] = 1.f;
+      } else if (PATH != P_STRIDED && p.w_vec && p.wt != GE_F32 && col(k, 0) < p.D) {
+        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a) + off + col(k, 0));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 v = p.wt == GE_F16 ? Elem<GE_F16>::get2(u[i]) : Elem<GE_BF16>::get2(u[i]);
+          f[2 * i] = v.x;
+          f[2 * i + 1] = v.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) f[i] = getw(p.wt, a, off + min(col(k, i), p.D - 1));
+      }
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) f[i] = col(k, i) < p.D ? scale * f[i] : 0.f;
+      float4 &lo = base[2 * k * threads], &hi = base[(2 * k + 1) * threads];
+      if (into) {
+        f[0] *= lo.x, f[1] *= lo.y, f[2] *= lo.z, f[3] *= lo.w;
+        f[4] *= hi.x, f[5] *= hi.y, f[6] *= hi.z, f[7] *= hi.w;
+      }
+      lo = make_float4(f[0], f[1], f[2], f[3]);
+      hi = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  }
+  // what is kept, to a row of the weights' type
+  template <int NV, int PATH>
+  __device__ __noinline__ void store(const NormParams &p, const Columns<PATH> &col, void *out, int64_t off) const {
+#pragma unroll 1
+    for (int k = 0; k < NV; ++k) {
+      const float4 lo = base[2 * k * threads], hi = base[(2 * k + 1) * threads];
+      const float f[kChunk] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (col(k, i) < p.D) putw(p.wt, out, off + col(k, i), f[i]);
+    }
   }
 };
 
-// A ring of rows on their way from memory (cp.async into the thread's own
-// words): `ahead` rows of NA tensors each.  Rows that are not whole 16-byte
-// units are read when they are wanted.
-template <int DT, int NV, bool kVec, int NA>
+// Rows on their way from memory: NA tensors of them.  P_RING: `ahead` rows, by cp.async
+// into the thread's own words of shared memory.  P_STRIDED: the next row's
+// elements in registers, asked for once the current row's have been taken.
+template <int DT, int NV, int PATH, int NA>
 struct Ring {
-  static constexpr int kWords = kChunk * sizeof(typename Elem<DT>::T) / 16;  // of one tensor's chunk
-  static constexpr int kRow = NA * NV * kWords;  // 16-byte words of a thread per row
+  using T = typename Elem<DT>::T;
+  static constexpr int kWords = kChunk * sizeof(T) / 16;  // of one tensor's chunk
+  static constexpr int kRow = NA * NV * kWords;           // 16-byte words of a thread per row
   uint4 *base;
   int threads, ahead, D;
-  Columns<kVec> col;
+  Columns<PATH> col;
+  T raw[PATH == P_STRIDED ? NA : 1][PATH == P_STRIDED ? NV : 1][kChunk];
 
-  __device__ __forceinline__ void issue(int slot, int a, const void *src, int64_t off, bool on) const {
-    if constexpr (kVec) {
-      using T = typename Elem<DT>::T;
+  __device__ __forceinline__ Ring(uint4 *base_, int threads_, int ahead_, int D_, const Columns<PATH> &col_)
+      : base(base_), threads(threads_), ahead(ahead_), D(D_), col(col_) {}
+
+  // row: the row's first element
+  __device__ __forceinline__ void issue(int slot, int a, const T *row) {
+    if constexpr (PATH == P_RING) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
           constexpr int kPer = 16 / sizeof(T);
           const int c = col(k, 0) + j * kPer;
-          const int left = on && src ? min(max(D - c, 0), kPer) * static_cast<int>(sizeof(T)) : 0;
-          const T *p = left ? static_cast<const T *>(src) + off + c : static_cast<const T *>(src);
+          // columns past the end arrive as zeros
+          const int left = min(max(D - c, 0), kPer) * static_cast<int>(sizeof(T));
           const uint32_t dst = smem_u32(base + (slot * kRow + (a * NV + k) * kWords + j) * threads);
-          if (left > 0)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(left) : "memory");
-          else
-            *reinterpret_cast<uint4 *>(base + (slot * kRow + (a * NV + k) * kWords + j) * threads) =
-                make_uint4(0u, 0u, 0u, 0u);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(left > 0 ? row + c : row),
+                       "r"(left)
+                       : "memory");
         }
+    } else if constexpr (PATH == P_STRIDED) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) raw[a][k][i] = row[min(col(k, i), D - 1)];
     }
   }
   __device__ __forceinline__ void commit() const {
-    if constexpr (kVec) asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (PATH == P_RING) asm volatile("cp.async.commit_group;" ::: "memory");
   }
   // the oldest row of the ring has landed
   __device__ __forceinline__ void wait() const {
-    if constexpr (kVec) {
+    if constexpr (PATH == P_RING) {
       if (ahead == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
       else if (ahead == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
       else asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
   }
-  __device__ __forceinline__ void get(int slot, int a, const void *src, int64_t off, bool on,
-                                      float (&v)[NV][kChunk]) const {
-    if constexpr (kVec) {
-      using T = typename Elem<DT>::T;
+  static __device__ __forceinline__ void widen(const uint4 (&w)[kWords], float2 (&v)[kPairs]) {
+    if constexpr (DT == GE_F32) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        union { uint4 w[kWords]; T e[kChunk]; } u;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) u.w[j] = base[(slot * kRow + (a * NV + k) * kWords + j) * threads];
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) v[k][i] = Elem<DT>::get(u.e[i]);
+      for (int j = 0; j < 2; ++j) {
+        v[2 * j] = make_float2(__uint_as_float(w[j % kWords].x), __uint_as_float(w[j % kWords].y));
+        v[2 * j + 1] = make_float2(__uint_as_float(w[j % kWords].z), __uint_as_float(w[j % kWords].w));
       }
     } else {
-      load_row<DT, NV, kVec>(src, off, col, D, on && src, v);
+      v[0] = Elem<DT>::get2(w[0].x);
+      v[1] = Elem<DT>::get2(w[0].y);
+      v[2] = Elem<DT>::get2(w[0].z);
+      v[3] = Elem<DT>::get2(w[0].w);
+    }
+  }
+  // row, on: where P_DIRECT finds it, and whether it is there
+  __device__ __forceinline__ void get(int slot, int a, const T *row, bool on, float2 (&v)[NV][kPairs]) const {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (PATH == P_RING) {
+        uint4 w[kWords];
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) w[j] = base[(slot * kRow + (a * NV + k) * kWords + j) * threads];
+        widen(w, v[k]);
+      } else if constexpr (PATH == P_DIRECT) {
+        if (on && col(k, 0) + kChunk <= D) {
+          uint4 w[kWords];
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) w[j] = reinterpret_cast<const uint4 *>(row + col(k, 0))[j];
+          widen(w, v[k]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            v[k][i].x = on && col(k, 2 * i) < D ? Elem<DT>::get(row[col(k, 2 * i)]) : 0.f;
+            v[k][i].y = on && col(k, 2 * i + 1) < D ? Elem<DT>::get(row[col(k, 2 * i + 1)]) : 0.f;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+          v[k][i].x = col(k, 2 * i) < D ? Elem<DT>::get(raw[a][k][2 * i]) : 0.f;
+          v[k][i].y = col(k, 2 * i + 1) < D ? Elem<DT>::get(raw[a][k][2 * i + 1]) : 0.f;
+        }
+      }
     }
   }
 };
@@ -235,61 +335,76 @@ struct RowSum {
   int per, warps, warp, lane, id, turn;
   template <int K>
   __device__ __forceinline__ void operator()(float (&v)[K]) {
+    static_assert(K >= 1 && K <= 3, "one to three sums");
+    if (per >= 32) {
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1)
-      if (s < per)
+      for (int s = 16; s > 0; s >>= 1)
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], s);
-    if (warps <= 1) return;
-    float4 *b = buf + turn * warps;
-    turn ^= 1;
-    if (lane == 0) b[warp] = make_float4(v[0], K > 1 ? v[K > 1 ? 1 : 0] : 0.f, 0.f, 0.f);
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(per) : "memory");
-    // 32 lanes add up to 32 warps' sums
-    float4 f = lane < warps ? b[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+#pragma unroll 1
+      for (int s = per >> 1; s > 0; s >>= 1)
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      f.x += __shfl_xor_sync(0xffffffffu, f.x, s);
-      if (K > 1) f.y += __shfl_xor_sync(0xffffffffu, f.y, s);
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], s);
     }
+    if (warps <= 1) return;
+    float4 *b = buf + turn;
+    turn ^= warps;  // 0 or the second half
+    if (lane == 0) b[warp] = make_float4(v[0], v[K > 1 ? 1 : 0], v[K > 2 ? 2 : 0], 0.f);
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(per) : "memory");
+    // every warp adds the warps' sums, up to 32 of them, in the same order
+    const float4 f = lane < warps ? b[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
     v[0] = f.x;
-    if (K > 1) v[K > 1 ? 1 : 0] = f.y;
+    if constexpr (K > 1) v[1] = f.y;
+    if constexpr (K > 2) v[2] = f.z;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+      if (s < warps)
+#pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], s);
+    // with up to 16 warps the first lane holds the whole sum
+    if (warps <= 16)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
   }
 };
 
-// v -= mean, with columns past the end kept at 0
-template <int NV, bool kVec>
-__device__ __forceinline__ void centre(float (&v)[NV][kChunk], float mean, int D, const Columns<kVec> &col) {
+template <int NV>
+__device__ __forceinline__ float sum_of(const float2 (&v)[NV][kPairs]) {
+  float2 s = both(0.f);
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[k][i] = col(k, i) < D ? v[k][i] - mean : 0.f;
+    for (int i = 0; i < kPairs; ++i) s = add2(s, v[k][i]);
+  return s.x + s.y;
 }
 
 template <int NV>
-__device__ __forceinline__ float sum_of(const float (&v)[NV][kChunk]) {
-  float s = 0.f;
+__device__ __forceinline__ float dot_of(const float2 (&a)[NV][kPairs], const float2 (&b)[NV][kPairs]) {
+  float2 s = both(0.f);
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) s += v[k][i];
-  return s;
+    for (int i = 0; i < kPairs; ++i) s = fma2(a[k][i], b[k][i], s);
+  return s.x + s.y;
 }
 
-template <int NV>
-__device__ __forceinline__ float dot_of(const float (&a)[NV][kChunk], const float (&b)[NV][kChunk]) {
-  float s = 0.f;
+// v -= mean; columns past the end are 0 and stay 0
+template <int NV, int PATH>
+__device__ __forceinline__ void centre(float2 (&v)[NV][kPairs], float mean, int D, const Columns<PATH> &col) {
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) s += a[k][i] * b[k][i];
-  return s;
+    for (int i = 0; i < kPairs; ++i) {
+      v[k][i].x = col(k, 2 * i) < D ? v[k][i].x - mean : 0.f;
+      v[k][i].y = col(k, 2 * i + 1) < D ? v[k][i].y - mean : 0.f;
+    }
 }
 
-// v becomes N(v); returns the inverse divisor
-template <int NV, bool kVec>
-__device__ __forceinline__ float normalise(float (&v)[NV][kChunk], int kind, float eps, float inv_d, int D,
-                                           const Columns<kVec> &col, RowSum &row_sum) {
+// The inverse divisor of a row; a centred row (GE_NORM_LAYER) has its mean taken off v.
+template <int NV, int PATH>
+__device__ __forceinline__ float divisor(float2 (&v)[NV][kPairs], int kind, float eps, float inv_d, int D,
+                                         const Columns<PATH> &col, RowSum &row_sum) {
   if (kind == GE_NORM_LAYER) {
     float m[1] = {sum_of(v)};
     row_sum(m);
@@ -297,22 +412,17 @@ __device__ __forceinline__ float normalise(float (&v)[NV][kChunk], int kind, flo
   }
   float s[1] = {dot_of(v, v)};
   row_sum(s);
-  const float r = 1.f / sqrtf(s[0] * inv_d + eps);
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[k][i] *= r;
-  return r;
+  return rsqrtf(s[0] * inv_d + eps);
 }
 
-// A CTA's share of its shared memory: the rows' sums, then (keep_w) the
+// A thread's row and place in it.  Shared memory of a CTA: the rows' sums, then the
 // factors w_pre and alpha gate w_post of each thread's columns, then the ring.
-template <bool kVec>
+template <int PATH>
 struct Place {
   int per, mine, t;
   __device__ __forceinline__ Place(int row_threads)
       : per(row_threads), mine(threadIdx.x / row_threads), t(threadIdx.x - mine * row_threads) {}
-  __device__ __forceinline__ Columns<kVec> columns() const { return Columns<kVec>{t, per}; }
+  __device__ __forceinline__ Columns<PATH> columns() const { return Columns<PATH>{t, per}; }
   __device__ __forceinline__ RowSum row_sum(uint8_t *smem) const {
     const int warps = per / 32;
     return RowSum{reinterpret_cast<float4 *>(smem) + 2 * mine * warps, per, warps, t >> 5,
@@ -320,103 +430,92 @@ struct Place {
   }
 };
 
-// v *= alpha gate w_post for the rows of gate group g (kept: `at` is the group the kept factors are for)
-template <int NV, bool kVec>
-__device__ __forceinline__ void times_post(const NormParams &p, const Columns<kVec> &col, const Own &own, int64_t g,
-                                           int64_t &at, float (&v)[NV][kChunk]) {
-  if (p.keep_w && at == g) {
-    own.times(v);
-    return;
-  }
-  float f[NV][kChunk], w[NV][kChunk];
-  load_w<NV, kVec>(p, p.gate, p.gate ? g * p.D : 0, col, f);
-  load_w<NV, kVec>(p, p.w_post, 0, col, w);
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      f[k][i] *= p.alpha * w[k][i];
-      v[k][i] *= f[k][i];
+// The gate group of a row: divided out only where the last one's rows end.
+struct Group {
+  int32_t size, g, begin;
+  __device__ __forceinline__ void move(int32_t row) {
+    if (static_cast<uint32_t>(row - begin) >= static_cast<uint32_t>(size)) {
+      g = row / size;
+      begin = g * size;
     }
-  if (p.keep_w) own.put(f);
-  at = g;
-}
-
-template <int NV, bool kVec>
-__device__ __forceinline__ void times_pre(const NormParams &p, const Columns<kVec> &col, const Own &own,
-                                          float (&v)[NV][kChunk]) {
-  if (!p.w_pre) return;
-  if (p.keep_w) {
-    own.times(v);
-    return;
   }
-  float w[NV][kChunk];
-  load_w<NV, kVec>(p, p.w_pre, 0, col, w);
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[k][i] *= w[k][i];
-}
+  __device__ __forceinline__ bool last(int32_t row) const { return row - begin == size - 1; }
+};
 
-template <int DT, int NV, bool kVec>
-__global__ void __launch_bounds__(kMaxThreads) norm_kernel(const __grid_constant__ NormParams p) {
+// kBound: threads that the registers must suffice for
+template <int DT, int NV, int PATH, int kBound>
+__global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__ NormParams p) {
+  using T = typename Elem<DT>::T;
+  constexpr bool kAsk = PATH == P_RING;  // rows are asked for ahead of the one at hand
   extern __shared__ __align__(16) uint8_t smem[];
-  const Place<kVec> pl(p.row_threads);
+  const Place<PATH> pl(p.row_threads);
   const int rows = blockDim.x / pl.per;
-  const Columns<kVec> col = pl.columns();
+  const Columns<PATH> col = pl.columns();
   RowSum row_sum = pl.row_sum(smem);
-  uint4 *words = reinterpret_cast<uint4 *>(smem + kSumBytes) + threadIdx.x;
+  float4 *words = reinterpret_cast<float4 *>(smem + kSumBytes) + threadIdx.x;
   const int n = blockDim.x;
+  // w_pre; alpha gate w_post of the gate group at hand
   const Own own_pre{words, n}, own_post{words + 2 * NV * n, n};
-  const Ring<DT, NV, kVec, 2> ring{words + (p.keep_w ? 4 * NV * n : 0), n, p.ahead, p.D, col};
-  const int64_t step = int64_t(gridDim.x) * rows;
-  int64_t row = int64_t(blockIdx.x) * rows + pl.mine;
+  Ring<DT, NV, PATH, 2> ring(reinterpret_cast<uint4 *>(words + 4 * NV * n), n, p.ahead, p.D, col);
+  const int step = gridDim.x * rows;
+  int64_t first = int64_t(blockIdx.x) * rows;  // the CTA's first row: every thread's loop is as long
+  int64_t row = first + pl.mine;
+  const T *x = static_cast<const T *>(p.x), *b = static_cast<const T *>(p.b);
+  T *y = static_cast<T *>(p.y), *h = static_cast<T *>(p.h);
   griddep_wait();
   griddep_launch_dependents();
-  for (int s = 0; s < p.ahead - 1; ++s) {
-    const int64_t r = row + s * step;
-    ring.issue(s, 0, p.x, r * p.ldx, r < p.T);
-    ring.issue(s, 1, p.b, r * p.ldb, r < p.T);
-    ring.commit();
-  }
-  if (p.keep_w && p.w_pre) {
-    float w[NV][kChunk];
-    load_w<NV, kVec>(p, p.w_pre, 0, col, w);
-    own_pre.put(w);
-  }
-  int64_t at = -1;
-  int slot = 0, next = p.ahead - 1;
-  // rows of a CTA that share warps stay together: they leave the loop at once
-  for (int64_t first = int64_t(blockIdx.x) * rows; first < p.T; first += step, row += step) {
-    const bool on = row < p.T;
-    {
-      const int64_t r = row + (p.ahead - 1) * step;
-      ring.issue(next, 0, p.x, r * p.ldx, r < p.T);
-      ring.issue(next, 1, p.b, r * p.ldb, r < p.T);
-      ring.commit();
-      if (++next == p.ahead) next = 0;
+  int64_t ahead = row;  // the next row to ask for
+  auto fetch = [&](int slot) {
+    if (ahead < p.T) {
+      ring.issue(slot, 0, x + ahead * p.ldx);
+      if (b) ring.issue(slot, 1, b + ahead * p.ldb);
     }
+    ring.commit();
+    ahead += step;
+  };
+  for (int s = 0; s < (kAsk ? p.ahead - 1 : 1); ++s) fetch(s);
+  if (p.w_pre) own_pre.fill<NV>(p, col, 1.f, p.w_pre, 0);
+  int32_t at = -1;  // the group that own_post is for
+  Group group{static_cast<int32_t>(p.rows_per_gate), 0, 0};
+  int slot = 0, next = p.ahead - 1;
+  for (; first < p.T; first += step, row += step) {
+    const bool on = row < p.T;
+    if (kAsk) fetch(next);
+    if (++next == p.ahead) next = 0;
     ring.wait();
-    float y[NV][kChunk];
-    if (p.b) {
-      float b[NV][kChunk];
-      ring.get(slot, 1, p.b, row * p.ldb, on, b);
-      if (p.post != GE_NORM_NONE) normalise(b, p.post, p.eps_post, p.inv_d, p.D, col, row_sum);
-      times_post<NV, kVec>(p, col, own_post, p.gate && on ? row / p.rows_per_gate : 0, at, b);
-      ring.get(slot, 0, p.x, row * p.ldx, on, y);
+    float2 v[NV][kPairs];
+    if (!kAsk || !b) ring.get(slot, 0, x + row * p.ldx, on, v);
+    if (b) {
+      float2 u[NV][kPairs];
+      ring.get(slot, 1, b + row * p.ldb, on, u);
+      if (!kAsk) fetch(0);
+      if (p.gate && on) group.move(static_cast<int32_t>(row));
+      if (at != group.g) {
+        at = group.g;
+        own_post.fill<NV>(p, col, p.alpha, p.w_post, 0);
+        if (p.gate) own_post.fill<NV>(p, col, 1.f, p.gate, int64_t(at) * p.D, true);
+      }
+      const float r = p.post != GE_NORM_NONE
+                          ? divisor(u, p.post, p.eps_post, p.inv_d, p.D, col, row_sum) : 1.f;
+      own_post.times(u);
+      if (kAsk) ring.get(slot, 0, x + row * p.ldx, on, v);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) y[k][i] += b[k][i];
-    } else {
-      ring.get(slot, 0, p.x, row * p.ldx, on, y);
+        for (int i = 0; i < kPairs; ++i) v[k][i] = fma2(u[k][i], both(r), v[k][i]);
+    } else if (!kAsk) {
+      fetch(0);
     }
     if (++slot == p.ahead) slot = 0;
-    if (p.y && on) store_row<DT, NV, kVec>(p.y, row * p.ldy, col, p.D, y);
-    if (p.h) {
-      normalise(y, p.pre, p.eps_pre, p.inv_d, p.D, col, row_sum);
-      times_pre<NV, kVec>(p, col, own_pre, y);
-      if (on) store_row<DT, NV, kVec>(p.h, row * p.ldh, col, p.D, y);
+    if (y && on) store_row<DT, NV, PATH>(y + row * p.ldy, col, p.D, v);
+    if (h) {
+      const float r = divisor(v, p.pre, p.eps_pre, p.inv_d, p.D, col, row_sum);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) v[k][i] = mul2(v[k][i], both(r));
+      if (p.w_pre) own_pre.times(v);
+      if (on) store_row<DT, NV, PATH>(h + row * p.ldh, col, p.D, v);
     }
   }
 }
@@ -437,149 +536,206 @@ __device__ __forceinline__ void unit_rows(const NormParams &p, int u, int64_t &b
 }
 
 // kWhole: a unit holds whole gate groups
-template <int DT, int NV, bool kVec, bool kWhole>
-__global__ void __launch_bounds__(kMaxThreads) norm_grad_kernel(const __grid_constant__ NormParams p) {
+template <int DT, int NV, int PATH, int kBound, bool kWhole>
+__global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_constant__ NormParams p) {
+  using T = typename Elem<DT>::T;
+  constexpr bool kAsk = PATH == P_RING;
   extern __shared__ __align__(16) uint8_t smem[];
-  const Place<kVec> pl(p.row_threads);
-  const Columns<kVec> col = pl.columns();
+  const Place<PATH> pl(p.row_threads);
+  const Columns<PATH> col = pl.columns();
   RowSum row_sum = pl.row_sum(smem);
-  uint4 *words = reinterpret_cast<uint4 *>(smem + kSumBytes) + threadIdx.x;
+  float4 *words = reinterpret_cast<float4 *>(smem + kSumBytes) + threadIdx.x;
   const int n = blockDim.x;
-  const Own own_pre{words, n}, own_post{words + 2 * NV * n, n};
-  const Ring<DT, NV, kVec, 4> ring{words + (p.keep_w ? 4 * NV * n : 0), n, p.ahead, p.D, col};
+  // w_pre; alpha gate w_post of the gate group at hand, or (kWhole) its gate and alpha w_post apart
+  constexpr int kFactors = kWhole ? 3 : 2;
+  const Own own_pre{words, n}, own_post{words + 2 * NV * n, n}, own_w{words + 4 * NV * n, n};
+  Ring<DT, NV, PATH, 4> ring(reinterpret_cast<uint4 *>(words + kFactors * 2 * NV * n), n, p.ahead, p.D, col);
   const int u = blockIdx.x * (n / pl.per) + pl.mine;
   int64_t row, end;
   unit_rows(p, u, row, end);
+  const T *yin = static_cast<const T *>(p.yin), *dh = static_cast<const T *>(p.dh),
+          *dy = static_cast<const T *>(p.dy), *b = static_cast<const T *>(p.b);
+  T *dx = static_cast<T *>(p.dx), *db = static_cast<T *>(p.db);
   griddep_wait();
   griddep_launch_dependents();
-  auto fetch = [&](int slot, int64_t r) {
-    ring.issue(slot, 0, p.yin, r * p.ldy, r < end);
-    ring.issue(slot, 1, p.dh, r * p.ldh, r < end);
-    ring.issue(slot, 2, p.dy, r * p.ldy, r < end);
-    ring.issue(slot, 3, p.b, r * p.ldb, r < end);
+  int64_t ahead = row;  // the next row to ask for
+  auto fetch = [&](int slot) {
+    if (ahead < end) {
+      ring.issue(slot, 0, yin + ahead * p.ldy);
+      ring.issue(slot, 1, dh + ahead * p.ldh);
+      if (dy) ring.issue(slot, 2, dy + ahead * p.ldy);
+      if (b) ring.issue(slot, 3, b + ahead * p.ldb);
+    }
     ring.commit();
+    ++ahead;
   };
-  for (int s = 0; s < p.ahead - 1; ++s) fetch(s, row + s);
-  if (p.keep_w && p.w_pre) {
-    float w[NV][kChunk];
-    load_w<NV, kVec>(p, p.w_pre, 0, col, w);
-    own_pre.put(w);
-  }
-  float acc_pre[NV][kChunk], acc_post[NV][kChunk];
-  float acc_gate[kWhole ? NV : 1][kChunk];  // whole groups: the current group's q
+  for (int s = 0; s < (kAsk ? p.ahead - 1 : 1); ++s) fetch(s);
+  if (p.w_pre) own_pre.fill<NV>(p, col, 1.f, p.w_pre, 0);
+  if (kWhole && b) own_w.fill<NV>(p, col, p.alpha, p.w_post, 0);
+  float2 acc_pre[NV][kPairs], acc_post[NV][kPairs];
+  float2 acc_gate[kWhole ? NV : 1][kPairs];  // whole groups: the current group's q
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      acc_pre[k][i] = acc_post[k][i] = 0.f;
-      if (kWhole) acc_gate[k][i] = 0.f;
+    for (int i = 0; i < kPairs; ++i) {
+      acc_pre[k][i] = acc_post[k][i] = both(0.f);
+      if (kWhole) acc_gate[k][i] = both(0.f);
     }
-  int64_t at = -1;
+  int32_t at = -1;  // the group that own_post is for
+  Group group{static_cast<int32_t>(p.rows_per_gate), 0, 0};
   int slot = 0, next = p.ahead - 1;
-  for (int r = 0; r < p.rows_per_unit; ++r, ++row) {  // every thread: row sums hold barriers
+  const bool layer_b = b && p.post == GE_NORM_LAYER, norm_b = b && p.post != GE_NORM_NONE;
+  // every thread goes round as often: row sums hold barriers.  Past a unit's
+  // last row what is computed is dropped.
+  for (int r = 0; r < p.rows_per_unit; ++r, ++row) {
     const bool on = row < end;
-    fetch(next, row + p.ahead - 1);
+    if (kAsk) fetch(next);
     if (++next == p.ahead) next = 0;
     ring.wait();
-    float y[NV][kChunk], d[NV][kChunk];
-    ring.get(slot, 0, p.yin, row * p.ldy, on, y);
-    ring.get(slot, 1, p.dh, row * p.ldh, on, d);
-    const float ry = normalise(y, p.pre, p.eps_pre, p.inv_d, p.D, col, row_sum);
+    // y becomes what N_pre divides, d = dh w_pre, q = dh y
+    float2 y[NV][kPairs], d[NV][kPairs], q[NV][kPairs];
+    ring.get(slot, 0, yin + row * p.ldy, on, y);
+    ring.get(slot, 1, dh + row * p.ldh, on, d);
+    float mean_d = 0.f;
+    if (p.pre == GE_NORM_LAYER) {
+      float s[2];
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) q[k][i] = d[k][i];
+      if (p.w_pre) own_pre.times(q);
+      s[0] = sum_of(y);
+      s[1] = sum_of(q);
+      row_sum(s);
+      centre(y, s[0] * p.inv_d, p.D, col);
+      mean_d = s[1] * p.inv_d;
+    }
+    float s[2] = {dot_of(y, y), 0.f};
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) acc_pre[k][i] += d[k][i] * y[k][i];
-    times_pre<NV, kVec>(p, col, own_pre, d);
-    float s[2] = {dot_of(d, y), p.pre == GE_NORM_LAYER ? sum_of(d) : 0.f};
+      for (int i = 0; i < kPairs; ++i) q[k][i] = mul2(d[k][i], y[k][i]);
+    if (p.w_pre) {
+      float2 sum = both(0.f);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float4 f = own_pre.base[(2 * k + j) * n];
+          const float2 lo = make_float2(f.x, f.y), hi = make_float2(f.z, f.w);
+          sum = fma2(q[k][2 * j], lo, sum);
+          sum = fma2(q[k][2 * j + 1], hi, sum);
+          d[k][2 * j] = mul2(d[k][2 * j], lo);
+          d[k][2 * j + 1] = mul2(d[k][2 * j + 1], hi);
+        }
+      s[1] = sum.x + sum.y;
+    } else {
+      s[1] = sum_of(q);
+    }
     row_sum(s);
-    s[0] *= p.inv_d;
-    s[1] *= p.inv_d;
-    // d becomes the whole gradient of y
-    {
-      float g[NV][kChunk];
-      ring.get(slot, 2, p.dy, row * p.ldy, on && p.dy, g);
+    const float ry = rsqrtf(s[0] * p.inv_d + p.eps_pre);
+    const float along = -ry * (ry * s[1] * p.inv_d * ry), mean = -ry * mean_d;
+    if (on)
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i)
-          d[k][i] = (col(k, i) < p.D ? ry * (d[k][i] - s[1] - y[k][i] * s[0]) : 0.f) + g[k][i];
-    }
-    if (p.b) ring.get(slot, 3, p.b, row * p.ldb, on, y);  // read before dx is written: it may be in b's place
-    if (++slot == p.ahead) slot = 0;
-    if (on) store_row<DT, NV, kVec>(p.dx, row * p.ldx, col, p.D, d);
-    if (!p.b) continue;
-    float rb = 1.f;
-    if (p.post != GE_NORM_NONE) rb = normalise(y, p.post, p.eps_post, p.inv_d, p.D, col, row_sum);
-    const int64_t g = p.gate && on ? row / p.rows_per_gate : 0;
+        for (int i = 0; i < kPairs; ++i) acc_pre[k][i] = fma2(q[k][i], both(ry), acc_pre[k][i]);
+    // d becomes the whole gradient of y (past the end of a centred row it is
+    // not 0, but the factors it meets there are)
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        if (kWhole) acc_gate[k][i] += d[k][i] * y[k][i];
-        else acc_post[k][i] += d[k][i] * y[k][i];
-      }
-    if (kWhole && on && (row + 1 == end || (row + 1) % p.rows_per_gate == 0)) {
-      // the group's last row: its gate's gradient is complete
-      float w[NV][kChunk];
-      load_w<NV, kVec>(p, p.gate, g * p.D, col, w);
+      for (int i = 0; i < kPairs; ++i)
+        d[k][i] = fma2(d[k][i], both(ry), fma2(y[k][i], both(along), both(mean)));
+    if (dy) {
+      ring.get(slot, 2, dy + row * p.ldy, on, y);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) acc_post[k][i] += w[k][i] * acc_gate[k][i];
-      if (p.dgate) {
-        load_w<NV, kVec>(p, p.w_post, 0, col, w);
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i) w[k][i] *= p.alpha * acc_gate[k][i];
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            if (col(k, i) < p.D) putw(p.wt, p.dgate, g * p.D + col(k, i), w[k][i]);
-      }
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) acc_gate[k][i] = 0.f;
+        for (int i = 0; i < kPairs; ++i) d[k][i] = add2(d[k][i], y[k][i]);
     }
-    times_post<NV, kVec>(p, col, own_post, g, at, d);
-    if (p.post != GE_NORM_NONE) {
-      float s2[2] = {dot_of(d, y), p.post == GE_NORM_LAYER ? sum_of(d) : 0.f};
+    if (b) ring.get(slot, 3, b + row * p.ldb, on, y);  // read before dx is written: it may be in b's place
+    if (++slot == p.ahead) slot = 0;
+    if (!kAsk) fetch(0);
+    if (on) store_row<DT, NV, PATH>(dx + row * p.ldx, col, p.D, d);
+    if (!b) continue;
+    // y is now b, or what N_post divides
+    if (p.gate && on) group.move(static_cast<int32_t>(row));
+    if (at != group.g) {
+      at = group.g;
+      if (!kWhole) own_post.fill<NV>(p, col, p.alpha, p.w_post, 0);
+      if (p.gate) own_post.fill<NV>(p, col, 1.f, p.gate, int64_t(at) * p.D, !kWhole);
+    }
+    if (layer_b) {
+      float m[1] = {sum_of(y)};
+      row_sum(m);
+      centre(y, m[0] * p.inv_d, p.D, col);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) q[k][i] = mul2(d[k][i], y[k][i]);
+    own_post.times(d);
+    if (kWhole) own_w.times(d);
+    float rb = 1.f;
+    if (norm_b) {
+      float s2[3] = {dot_of(y, y), dot_of(d, y), layer_b ? sum_of(d) : 0.f};
       row_sum(s2);
-      s2[0] *= p.inv_d;
-      s2[1] *= p.inv_d;
+      rb = rsqrtf(s2[0] * p.inv_d + p.eps_post);
+      const float along2 = -rb * (rb * s2[1] * p.inv_d * rb), mean2 = -rb * s2[2] * p.inv_d;
+      if (db && on) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i)
+            d[k][i] = fma2(d[k][i], both(rb), fma2(y[k][i], both(along2), both(mean2)));
+      }
+    }
+    if (db && on) store_row<DT, NV, PATH>(db + row * p.ldb, col, p.D, d);
+    if (on)
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) d[k][i] = rb * (d[k][i] - s2[1] - y[k][i] * s2[0]);
+        for (int i = 0; i < kPairs; ++i) {
+          if (kWhole) acc_gate[k][i] = fma2(q[k][i], both(rb), acc_gate[k][i]);
+          else acc_post[k][i] = fma2(q[k][i], both(rb), acc_post[k][i]);
+        }
+    if (kWhole && on && (row + 1 == end || group.last(static_cast<int32_t>(row)))) {
+      // the group's last row: its gate's gradient is complete
+      own_post.get(y);
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) acc_post[k][i] = fma2(y[k][i], acc_gate[k][i], acc_post[k][i]);
+      if (p.dgate) {
+        own_w.times(acc_gate);
+        own_post.put(acc_gate);  // the next group's gate takes this place
+        own_post.store<NV>(p, col, p.dgate, int64_t(group.g) * p.D);
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) acc_gate[k][i] = both(0.f);
     }
-    if (p.db && on) store_row<DT, NV, kVec>(p.db, row * p.ldb, col, p.D, d);
   }
   if (u < p.units) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i)
-        if (col(k, i) < p.D) {
-          p.part_pre[int64_t(u) * p.D + col(k, i)] = acc_pre[k][i];
-          if (p.part_post) p.part_post[int64_t(u) * p.D + col(k, i)] = acc_post[k][i];
-        }
+    store_row<GE_F32, NV, PATH>(p.part_pre + int64_t(u) * p.ld_part, col, p.D, acc_pre);
+    if (p.part_post) store_row<GE_F32, NV, PATH>(p.part_post + int64_t(u) * p.ld_part, col, p.D, acc_post);
   }
 }
 
-template <int NV, bool kVec>
+template <int NV, int PATH, int kBound>
 const void *pick_run(int dt) {
-  return dt == GE_F16    ? reinterpret_cast<const void *>(norm_kernel<GE_F16, NV, kVec>)
-         : dt == GE_BF16 ? reinterpret_cast<const void *>(norm_kernel<GE_BF16, NV, kVec>)
-                         : reinterpret_cast<const void *>(norm_kernel<GE_F32, NV, kVec>);
+  return dt == GE_F16    ? reinterpret_cast<const void *>(norm_kernel<GE_F16, NV, PATH, kBound>)
+         : dt == GE_BF16 ? reinterpret_cast<const void *>(norm_kernel<GE_BF16, NV, PATH, kBound>)
+                         : reinterpret_cast<const void *>(norm_kernel<GE_F32, NV, PATH, kBound>);
 }
 
-template <int NV, bool kVec, bool kWhole>
+template <int NV, int PATH, int kBound, bool kWhole>
 const void *pick_grad(int dt) {
-  return dt == GE_F16    ? reinterpret_cast<const void *>(norm_grad_kernel<GE_F16, NV, kVec, kWhole>)
-         : dt == GE_BF16 ? reinterpret_cast<const void *>(norm_grad_kernel<GE_BF16, NV, kVec, kWhole>)
-                         : reinterpret_cast<const void *>(norm_grad_kernel<GE_F32, NV, kVec, kWhole>);
+  return dt == GE_F16    ? reinterpret_cast<const void *>(norm_grad_kernel<GE_F16, NV, PATH, kBound, kWhole>)
+         : dt == GE_BF16 ? reinterpret_cast<const void *>(norm_grad_kernel<GE_BF16, NV, PATH, kBound, kWhole>)
+                         : reinterpret_cast<const void *>(norm_grad_kernel<GE_F32, NV, PATH, kBound, kWhole>);
 }
 
 }  // namespace ge
