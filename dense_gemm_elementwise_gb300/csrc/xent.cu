@@ -1,18 +1,20 @@
 // xent.cu -- the vocabulary loss and its gradients (gemm_epi_xent_*): plan,
 // launches, and the small kernels around the products of xent_kernel.cuh.
 //
-//   scan     one CTA: which rows take part (their target exists), their order,
-//            targets and weights; ignored rows get loss and lse 0
-//   gather   their hidden states, packed; up to a k-block of zero rows after
-//   X_STATS  logits -> per row and column range: maximum, sum, target's logit
+//   pack     which rows take part (their target exists), in their order: hidden
+//            states, targets and weights side by side, zero rows up to the next
+//            k-block; ignored rows get loss and lse 0
+//   X_KEEP   (X_STATS for fp16) logits -> per row and column range: maximum, sum, target's logit; of
+//            the first piece of the vocabulary also the logits, in 16 bits
 //   finish   joins the ranges: lse, loss, total; what the gradients need per row
 //   per piece of the vocabulary:
-//     X_DLOGIT  dl of the piece (16 bits)
-//     X_OUT     dW rows of the piece = dl^T @ H
-//     X_PART    dH += dl @ W, fp32
+//     convert / X_DLOGIT  dl of the piece, from what was kept / from the product again
+//     X_OUT    dW rows of the piece = dl^T @ H
+//     X_PART   dH += dl @ W, fp32
 //   spread   dH slices added in order, rounded, back to the rows' places
 //
-// Few kernels know how many rows take part; all read it from device memory.
+// A loss alone is X_STATS and finish, after pack where that can save tiles.
+// How many rows take part stays on the device.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,197 +36,240 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr double kLn2 = 0.69314718055994531;
 
-// Device scalars of a run, at the start of the workspace.
-struct Scalars {
-  int32_t rows;       // rows that take part
-  int32_t ticket;     // finish blocks done
-  double weights;     // sum of their weights
-  float out_scale;    // multiplies dl @ W and dl^T @ H
-  float dl_scale;     // power of two in dl
-};
-
-struct ScanParams {
-  const void *target;
-  const float *weight;
-  float *loss, *lse;
-  Scalars *sc;
-  int32_t *index, *place, *gathered;  // row of the r-th taken, its inverse (-1: ignored), targets
-  float *gweight;
-  int64_t V;
-  int32_t T, i32;
-};
-
 __device__ __forceinline__ int64_t target_of(const void *t, int i32, int64_t i) {
   return i32 ? static_cast<const int32_t *>(t)[i] : static_cast<const int64_t *>(t)[i];
 }
 
-// Rows in order: a ballot within each warp, a scan over the CTA's warps, and a
-// running count from chunk to chunk of 1024 rows.
-__global__ void __launch_bounds__(1024) xent_scan_kernel(const __grid_constant__ ScanParams p) {
-  __shared__ int counts[32];
-  __shared__ double sums[32];
+struct PackParams {
+  const void *target;
+  const float *weight;
+  const uint16_t *H;
+  uint16_t *Hc;
+  float *loss, *lse;
+  XentScalars *sc;
+  int32_t *index, *place, *gathered;  // row of the r-th taken, its inverse (-1: ignored), targets
+  float *gweight;
+  int64_t V, ldh, ldc;
+  int32_t T, D, i32, rows_per_cta;
+  // dH's sum over the vocabulary: tiles of `part_m` x `part_n`, k-blocks, CTAs (pairs), slices at most
+  int32_t part_m, part_n_blk, part_kb, part_units, part_slices;
+};
+
+// How many slices dH's k-blocks are split into: the candidates fill one to four
+// waves of CTAs; the least time wins (in k-blocks of a tile, 0.27 us each: the waves'
+// k-blocks and about six for set-up and stores, and each slice's way to memory and back).
+__device__ int split_of(const PackParams &p, int rows) {
+  const int tiles = max(1, (rows + p.part_m - 1) / p.part_m * p.part_n_blk);
+  float best = 0.f;
+  int best_split = p.part_kb;
+  for (int w = 0; w <= 4; ++w) {
+    const int s = w == 0 ? 1 : min(min(p.part_units * w / tiles, p.part_slices), p.part_kb);
+    if (s < 1) continue;
+    const int kbs = (p.part_kb + s - 1) / s, used = (p.part_kb + kbs - 1) / kbs;
+    const int waves = (tiles * used + p.part_units - 1) / p.part_units;
+    const float cost = float(waves) * float(kbs + 6) + float(used) * float(rows) * float(p.D) * (8.f / (6.5e6f * 0.27f));
+    if (w == 0 || cost < best * 0.97f) {
+      best = cost;
+      best_split = kbs;
+    }
+  }
+  return best_split;
+}
+
+// Every CTA packs a run of rows.  It counts the rows that take part before its
+// own from the targets themselves (they are few bytes and in L2 after the
+// first CTA), which costs less than a launch or a chain of CTAs.
+constexpr int kPackThreads = 256;
+__global__ void __launch_bounds__(kPackThreads) xent_pack_kernel(const __grid_constant__ PackParams p) {
+  __shared__ int counts[2][kPackThreads / 32];
+  __shared__ int32_t rows[kPackThreads];
   griddep_wait();
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int base = 0;
-  double w_sum = 0.0;
-  for (int64_t first = 0; first < p.T; first += 1024) {
-    const int64_t i = first + threadIdx.x;
-    const int64_t t = i < p.T ? target_of(p.target, p.i32, i) : -1;
-    const bool take = t >= 0 && t < p.V;
-    const unsigned vote = __ballot_sync(0xffffffffu, take);
-    if (lane == 0) counts[warp] = __popc(vote);
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < 32; ++w) {
-      before += w < warp ? counts[w] : 0;
-      all += counts[w];
-    }
-    __syncthreads();
-    if (take) {
-      const int r = base + before + __popc(vote & ((1u << lane) - 1u));
-      const float w = p.weight ? p.weight[i] : 1.f;
-      p.index[r] = static_cast<int32_t>(i);
-      p.gathered[r] = static_cast<int32_t>(t);
-      p.gweight[r] = w;
-      p.place[i] = r;
-      w_sum += w;
-    } else if (i < p.T) {
-      p.place[i] = -1;
-      if (p.loss) p.loss[i] = 0.f;
-      if (p.lse) p.lse[i] = 0.f;
-    }
-    base += all;
+  const int64_t begin = int64_t(blockIdx.x) * p.rows_per_cta, end = min(begin + p.rows_per_cta, int64_t(p.T));
+  int before = 0, all = 0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x; i < p.T; i += kPackThreads) {
+    const int64_t t = target_of(p.target, p.i32, i);
+    const int take = t >= 0 && t < p.V;
+    all += take;
+    before += i < begin ? take : 0;
   }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) w_sum += __shfl_xor_sync(0xffffffffu, w_sum, s);
-  if (lane == 0) sums[warp] = w_sum;
+  before = __reduce_add_sync(0xffffffffu, before);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) {
+    counts[0][warp] = before;
+    counts[1][warp] = all;
+  }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    double s = 0.0;
-    for (int w = 0; w < 32; ++w) s += sums[w];
-    p.sc->rows = base;
-    p.sc->ticket = 0;
-    p.sc->weights = s;
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < kPackThreads / 32; ++w) {
+    before += counts[0][w];
+    all += counts[1][w];
   }
-}
-
-struct GatherParams {
-  const uint16_t *H;
-  uint16_t *Hc;
-  const int32_t *index;
-  const Scalars *sc;
-  int64_t ldh, ldc;
-  int32_t T, D;
-};
-
-// A warp per row, 16 bytes per lane.
-__global__ void __launch_bounds__(256) xent_gather_kernel(const __grid_constant__ GatherParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int rows = p.sc->rows;
-  const int end = min(p.T, (rows + BK - 1) / BK * BK);
-  for (int r = blockIdx.x * 8 + (threadIdx.x >> 5); r < end; r += gridDim.x * 8) {
-    const uint16_t *src = r < rows ? p.H + int64_t(p.index[r]) * p.ldh : nullptr;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    p.sc->rows = all;
+    p.sc->kb_split = split_of(p, all);
+  }
+  auto copy = [&](const uint16_t *src, int64_t r) {  // a warp copies one row, or zeros
     uint16_t *dst = p.Hc + r * p.ldc;
     for (int c = lane * 8; c < p.D; c += 256) {
       if (c + 8 <= p.D) {
-        *reinterpret_cast<uint4 *>(dst + c) =
-            src ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(dst + c) = src ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
       } else {
         for (int i = c; i < p.D; ++i) dst[i] = src ? src[i] : uint16_t(0);
       }
     }
+  };
+  for (int64_t first = begin; first < end; first += kPackThreads) {
+    const int64_t i = first + threadIdx.x;
+    const int64_t t = i < end ? target_of(p.target, p.i32, i) : -1;
+    const bool take = t >= 0 && t < p.V;
+    const unsigned vote = __ballot_sync(0xffffffffu, take);
+    __syncthreads();
+    if (lane == 0) counts[0][warp] = __popc(vote);
+    __syncthreads();
+    int at = __popc(vote & ((1u << lane) - 1u)), here = 0;
+#pragma unroll
+    for (int w = 0; w < kPackThreads / 32; ++w) {
+      at += w < warp ? counts[0][w] : 0;
+      here += counts[0][w];
+    }
+    if (take) {
+      const int r = before + at;
+      rows[at] = static_cast<int32_t>(i);
+      p.index[r] = static_cast<int32_t>(i);
+      p.gathered[r] = static_cast<int32_t>(t);
+      p.gweight[r] = p.weight ? p.weight[i] : 1.f;
+      p.place[i] = r;
+    } else if (i < end) {
+      p.place[i] = -1;
+      if (p.loss) p.loss[i] = 0.f;
+      if (p.lse) p.lse[i] = 0.f;
+    }
+    __syncthreads();
+    for (int k = warp; k < here; k += kPackThreads / 32) copy(p.H + rows[k] * p.ldh, before + k);
+    before += here;
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+    const int64_t stop = min(int64_t(p.T), (int64_t(all) + BK - 1) / BK * BK);
+    for (int64_t r = all + warp; r < stop; r += kPackThreads / 32) copy(nullptr, r);
   }
 }
 
 struct FinishParams {
   const float2 *stats;       // [slots][T]
   const float *at_target;
-  const int32_t *index;
+  const int32_t *index;      // nullptr: rows were not packed, ...
   const float *gweight;
+  const void *target;        // ... these say which take part
+  const float *weight;
   float *loss, *lse, *total;
   float *lse2;
   float2 *coef;
-  double *block_sum;         // per block
+  double *block_sum;         // per block: of losses, of weights
   float *block_top;
-  Scalars *sc;
-  int32_t T, slots, row_lanes;  // row_lanes rows per block of 1024 threads
+  XentScalars *sc;
+  int64_t V;
+  int32_t T, i32, slots, row_lanes;  // row_lanes rows per block of 1024 threads
   int32_t mean;
   float z, grad_scale, c;
 };
 
+// (maximum, sum of 2^(x - maximum)) of two sets joined
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+  const float top = fmaxf(a.x, b.x), off = top == -INFINITY ? 0.f : top;
+  return make_float2(top, a.y * exp2f(a.x - off) + b.y * exp2f(b.x - off));
+}
+
 // row_lanes consecutive rows per block; the other threads share each row's
-// column ranges: maxima first, then the sums brought to their maximum.  The
-// last block to finish adds the blocks' sums in order.
+// column ranges.  The last block to finish adds the blocks' sums in order.
+// Bound by the latency of its loads when rows are few and by their bytes (8 per
+// row and 64 or 128 columns) when they are many.
 __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant__ FinishParams p) {
-  __shared__ float fbuf[1024];
-  __shared__ double dbuf[32];
+  __shared__ float2 pairs[1024];
+  __shared__ double dbuf[2][32];
+  __shared__ float fbuf[32];
   __shared__ bool last;
   griddep_wait();
   griddep_launch_dependents();
-  const int rows = p.sc->rows;
+  const int rows = p.index ? p.sc->rows : p.T;
   const int per = p.row_lanes, lanes = 1024 / per;
   const int x = threadIdx.x % per, y = threadIdx.x / per;
   const int r = blockIdx.x * per + x;
   const bool on = r < rows;
-  float top = -INFINITY;
-  if (on)
-#pragma unroll 8
-    for (int s = y; s < p.slots; s += lanes) top = fmaxf(top, p.stats[int64_t(s) * p.T + r].x);
-  fbuf[threadIdx.x] = top;
-  __syncthreads();
-  for (int h = lanes / 2; h > 0; h >>= 1) {
-    if (y < h) fbuf[threadIdx.x] = fmaxf(fbuf[threadIdx.x], fbuf[threadIdx.x + h * per]);
-    __syncthreads();
-  }
-  top = fbuf[x];
-  __syncthreads();
-  const float off = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  if (on)
-#pragma unroll 8
-    for (int s = y; s < p.slots; s += lanes) {
-      const float2 v = p.stats[int64_t(s) * p.T + r];
-      sum += v.y * exp2f(v.x - off);
+  float2 all = make_float2(-INFINITY, 0.f);
+  if (on) {
+    for (int s = y; s < p.slots; s += 8 * lanes) {
+      float2 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = s + i * lanes < p.slots ? p.stats[int64_t(s + i * lanes) * p.T + r] : make_float2(-INFINITY, 0.f);
+      float top = all.x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, v[i].x);
+      const float off = top == -INFINITY ? 0.f : top;
+      float sum = all.y * exp2f(all.x - off);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += v[i].y * exp2f(v[i].x - off);
+      all = make_float2(top, sum);
     }
-  fbuf[threadIdx.x] = sum;
+  }
+  pairs[threadIdx.x] = all;
   __syncthreads();
   for (int h = lanes / 2; h > 0; h >>= 1) {
-    if (y < h) fbuf[threadIdx.x] += fbuf[threadIdx.x + h * per];
+    if (y < h) pairs[threadIdx.x] = join(pairs[threadIdx.x], pairs[threadIdx.x + h * per]);
     __syncthreads();
   }
-  double loss = 0.0;
+  double loss = 0.0, weight = 0.0;
   float big = 0.f;
   if (y == 0 && on) {
-    sum = fbuf[x];
-    const double l2 = double(off) + log2(double(sum));
-    const double lse = l2 * kLn2;
-    const float w = p.gweight[r];
-    const double at = p.at_target[r];
-    loss = double(w) * (lse - at + double(p.z) * lse * lse);
-    const int i = p.index[r];
-    if (p.loss) p.loss[i] = static_cast<float>(loss);
-    if (p.lse) p.lse[i] = static_cast<float>(lse);
-    if (p.coef) {
-      const float zf = static_cast<float>(1.0 + 2.0 * double(p.z) * lse);
-      p.lse2[r] = static_cast<float>(l2);
-      p.coef[r] = make_float2(w * zf, w);  // scaled by the last block's choice in xent_scale_kernel
-      const float b = fabsf(w) * fmaxf(1.f, fabsf(zf));
-      big = isfinite(b) ? b : 0.f;
+    all = pairs[x];
+    int64_t i = r;
+    bool take = true;
+    float w = 1.f;
+    if (p.index) {
+      i = p.index[r];
+      w = p.gweight[r];
+    } else {
+      const int64_t t = target_of(p.target, p.i32, i);
+      take = t >= 0 && t < p.V;
+      if (p.weight) w = p.weight[i];
+    }
+    if (take) {
+      const double l2 = double(all.x == -INFINITY ? 0.f : all.x) + double(log2f(all.y));
+      const double lse = l2 * kLn2;
+      loss = double(w) * (lse - double(p.at_target[r]) + double(p.z) * lse * lse);
+      weight = w;
+      if (p.loss) p.loss[i] = static_cast<float>(loss);
+      if (p.lse) p.lse[i] = static_cast<float>(lse);
+      if (p.coef) {
+        const float zf = static_cast<float>(1.0 + 2.0 * double(p.z) * lse);
+        p.lse2[r] = static_cast<float>(l2);
+        p.coef[r] = make_float2(w * zf, w);
+        const float b = fabsf(w) * fmaxf(1.f, fabsf(zf));
+        big = isfinite(b) ? b : 0.f;
+      }
+    } else {
+      if (p.loss) p.loss[i] = 0.f;
+      if (p.lse) p.lse[i] = 0.f;
     }
   }
-  // rows of the block live in its first `per` (at most 32) threads
-  if (threadIdx.x < 32) {
+  auto over_warp = [&]() {
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) {
       loss += __shfl_xor_sync(0xffffffffu, loss, s);
+      weight += __shfl_xor_sync(0xffffffffu, weight, s);
       big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
     }
+  };
+  // rows of the block live in its first `per` (at most 32) threads
+  if (threadIdx.x < 32) {
+    over_warp();
     if (threadIdx.x == 0) {
-      p.block_sum[blockIdx.x] = loss;
+      p.block_sum[2 * blockIdx.x] = loss;
+      p.block_sum[2 * blockIdx.x + 1] = weight;
       p.block_top[blockIdx.x] = big;
       __threadfence();
       last = atomicAdd(&p.sc->ticket, 1) == static_cast<int>(gridDim.x) - 1;
@@ -233,32 +278,31 @@ __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant
   __syncthreads();
   if (!last) return;
   __threadfence();
-  // each thread adds every 1024th block, then the threads' sums are added in order
-  double total = 0.0;
+  // each thread adds every 1024th block, then the warps' sums are added in order
+  loss = weight = 0.0;
   big = 0.f;
   for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += 1024) {
-    total += __ldcg(p.block_sum + b);
+    loss += __ldcg(p.block_sum + 2 * b);
+    weight += __ldcg(p.block_sum + 2 * b + 1);
     big = fmaxf(big, __ldcg(p.block_top + b));
   }
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, s);
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
-  }
+  over_warp();
   if ((threadIdx.x & 31) == 0) {
-    dbuf[threadIdx.x >> 5] = total;
+    dbuf[0][threadIdx.x >> 5] = loss;
+    dbuf[1][threadIdx.x >> 5] = weight;
     fbuf[threadIdx.x >> 5] = big;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
-    total = 0.0;
+    loss = weight = 0.0;
     big = 0.f;
     for (int w = 0; w < 32; ++w) {
-      total += dbuf[w];
+      loss += dbuf[0][w];
+      weight += dbuf[1][w];
       big = fmaxf(big, fbuf[w]);
     }
-    const double norm = p.mean ? p.sc->weights : 1.0;
-    if (p.total) *p.total = norm != 0.0 ? static_cast<float>(total / norm) : 0.f;
+    const double norm = p.mean ? weight : 1.0;
+    if (p.total) *p.total = norm != 0.0 ? static_cast<float>(loss / norm) : 0.f;
     // dl is at most `big`: brought just below 2^14, clear of fp16's largest value
     // (65504) and of its subnormals for every p above 2^-28
     int e = 0;
@@ -269,18 +313,79 @@ __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant
   }
 }
 
-// coef *= dl_scale
-struct ScaleParams {
-  float2 *coef;
-  const Scalars *sc;
+struct ConvertParams {
+  uint16_t *buf;             // [T][pitch]: kept distances in, dl out
+  const float2 *stats;       // [slots][T]
+  const float *at_target, *lse2;
+  const float2 *coef;
+  const int32_t *gathered;
+  const XentScalars *sc;
+  int64_t pitch;
+  int32_t T, N, bn;          // N columns exist of the piece
+  float c2, c;               // logit_scale log2(e), logit_scale
 };
-__global__ void __launch_bounds__(256) xent_scale_kernel(const __grid_constant__ ScaleParams p) {
+
+// Kept distances to dl, in place: a warp per row of 256 columns, 16 bytes per lane, four rows
+// ahead.  Bound by memory: 4 bytes and one exponential per logit.
+constexpr int kConvertRows = 32;  // rows of a CTA (8 warps, 4 rows each)
+__global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant__ ConvertParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const float s = p.sc->dl_scale;
-  for (int r = blockIdx.x * 256 + threadIdx.x; r < p.sc->rows; r += gridDim.x * 256) {
-    const float2 v = p.coef[r];
-    p.coef[r] = make_float2(v.x * s, v.y * s);
+  const int rows = p.sc->rows;
+  const int end = min(p.T, (rows + BK - 1) / BK * BK);  // zeros up to the next k-block
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c0 = blockIdx.x * 256 + lane * 8;
+  const int slot = 2 * (c0 / p.bn) + ((c0 / 64) & 1);
+  const float ds = p.sc->dl_scale;
+  for (int first = blockIdx.y * kConvertRows; first < end; first += gridDim.y * kConvertRows) {
+    uint4 w[4];
+    float shift[4], lse2[4];
+    float2 coef[4];
+    int target[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = first + warp + 8 * i;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
+      shift[i] = lse2[i] = 0.f;
+      coef[i] = make_float2(0.f, 0.f);
+      target[i] = -1;
+      if (r < rows) {
+        w[i] = *reinterpret_cast<const uint4 *>(p.buf + r * p.pitch + c0);
+        const float top = p.stats[int64_t(slot) * p.T + r].x;
+        lse2[i] = p.lse2[r];
+        shift[i] = (top == -INFINITY ? 0.f : top) - lse2[i];
+        coef[i] = p.coef[r];
+        target[i] = p.gathered[r] - c0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = first + warp + 8 * i;
+      if (r >= end) continue;
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      float d[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t code = e & 1 ? u[e / 2] >> 16 : u[e / 2] & 0xffffu;
+        const float q = code == 0xffffu ? 0.f : exp2f(fmaf(float(code), -1.f / (1 << kKeptBits), shift[i]));
+        d[e] = q * (coef[i].x * ds);
+      }
+      if (target[i] >= 0 && target[i] < 8) {
+        // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p
+        const float at = p.at_target[r] * (p.c2 / p.c);
+        const float v = exp2f(at - lse2[i]) * (coef[i].x * ds) - coef[i].y * ds;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (e == target[i]) d[e] = v;
+      }
+      union { uint16_t e[8]; uint4 v; } o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float f = r < rows && c0 + e < p.N ? d[e] : 0.f;
+        o.e[e] = __bfloat16_as_ushort(__float2bfloat16_rn(f));
+      }
+      *reinterpret_cast<uint4 *>(p.buf + r * p.pitch + c0) = o.v;
+    }
   }
 }
 
@@ -288,48 +393,44 @@ struct SpreadParams {
   const float *part;  // [slices][T][Dp]
   uint16_t *dH;
   const int32_t *place;
-  const Scalars *sc;
+  const XentScalars *sc;
   int64_t lddh, Dp;
-  int32_t T, D, slices, bf16;
+  int32_t T, D, kb, bf16;
 };
 
-// A warp per row of dH: its slices added in order; ignored rows are 0.
+// Four columns of a row of dH per thread: its slices added in order; ignored rows are 0.
 __global__ void __launch_bounds__(256) xent_spread_kernel(const __grid_constant__ SpreadParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const float scale = p.sc->out_scale;
-  const int chunks = (p.D + 7) / 8;
-  const int64_t units = int64_t(p.T) * chunks;
+  const int kbs = p.sc->kb_split, slices = (p.kb + kbs - 1) / kbs;
+  const int quads = (p.D + 3) / 4;
+  const int64_t units = int64_t(p.T) * quads;
   for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < units; u += int64_t(gridDim.x) * 256) {
-    const int64_t i = u / chunks;
-    const int c = static_cast<int>(u - i * chunks) * 8;
+    const int64_t i = u / quads;
+    const int c = static_cast<int>(u - i * quads) * 4;
     const int r = p.place[i];
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r >= 0) {
-      for (int s = 0; s < p.slices; ++s) {
-        const float4 *a = reinterpret_cast<const float4 *>(p.part + (int64_t(s) * p.T + r) * p.Dp + c);
-        const float4 lo = a[0], hi = a[1];
-        v[0] += lo.x;
-        v[1] += lo.y;
-        v[2] += lo.z;
-        v[3] += lo.w;
-        v[4] += hi.x;
-        v[5] += hi.y;
-        v[6] += hi.z;
-        v[7] += hi.w;
+      const float *a = p.part + r * p.Dp + c;
+#pragma unroll 8
+      for (int s = 0; s < slices; ++s) {
+        const float4 f = *reinterpret_cast<const float4 *>(a + s * (p.T * p.Dp));
+        v.x += f.x;
+        v.y += f.y;
+        v.z += f.z;
+        v.w += f.w;
       }
+      v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
     }
-    union { uint16_t e[8]; uint4 w; } o;
+    union { uint16_t e[4]; uint2 w; } o;
+    const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float f = r >= 0 ? v[e] * scale : 0.f;
-      o.e[e] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f)) : __half_as_ushort(__float2half_rn(f));
-    }
+    for (int e = 0; e < 4; ++e)
+      o.e[e] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[e])) : __half_as_ushort(__float2half_rn(f[e]));
     uint16_t *dst = p.dH + i * p.lddh + c;
-    if (c + 8 <= p.D) {
-      *reinterpret_cast<uint4 *>(dst) = o.w;
+    if (c + 4 <= p.D) {
+      *reinterpret_cast<uint2 *>(dst) = o.w;
     } else {
       for (int e = 0; e < p.D - c; ++e) dst[e] = o.e[e];
     }
@@ -343,10 +444,10 @@ struct Product {
   uint32_t off_B = 0, off_out = 0, off_bar = 0;
 };
 
-cudaError_t launch(const void *fn, int grid, int threads, int smem, int cluster, void *params, cudaStream_t s) {
+cudaError_t launch(const void *fn, dim3 grid, int threads, int smem, int cluster, void *params, cudaStream_t s) {
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
@@ -377,9 +478,10 @@ struct gemm_epi_xent_plan {
   ge_xent_desc d{};
   int sms = 0, smem = 0, pairs = 0;
   uint32_t *status = nullptr;
-  Product stats, dlogit, out, part;
+  Product stats, keep, dlogit, out, part;
   int64_t piece = 0;    // vocabulary columns of a piece, a multiple of 256
-  int slices = 1, kb_split = 1;
+  int slices = 1;       // of dH's sum over a piece, at most
+  bool pack = true;     // a loss alone packs its rows too
   int row_lanes = 32, finish_grid = 1;
   int64_t ldc = 0, Dp = 0;
 };
@@ -397,7 +499,7 @@ Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {
     return here;
   };
   const size_t T = static_cast<size_t>(pl->T);
-  w.scalars = take(sizeof(Scalars));
+  w.scalars = take(sizeof(XentScalars));
   w.index = take(4 * T);
   w.place = take(4 * T);
   w.gathered = take(4 * T);
@@ -405,10 +507,10 @@ Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {
   w.at_target = take(4 * T);
   w.lse2 = take(4 * T);
   w.coef = take(8 * T);
-  w.block_sum = take(8 * static_cast<size_t>(pl->finish_grid));
+  w.block_sum = take(16 * static_cast<size_t>(pl->finish_grid));
   w.block_top = take(4 * static_cast<size_t>(pl->finish_grid));
   w.stats = take(8 * T * static_cast<size_t>(slots_of(pl)));
-  w.Hc = take(2 * T * static_cast<size_t>(pl->ldc));
+  if (grads || pl->pack) w.Hc = take(2 * T * static_cast<size_t>(pl->ldc));
   if (grads) {
     w.dl = take(2 * T * static_cast<size_t>(pl->piece));
     w.part = take(4 * T * static_cast<size_t>(pl->Dp) * static_cast<size_t>(pl->slices));
@@ -451,6 +553,7 @@ int configure(gemm_epi_xent_plan *pl) {
   const int cg = pl->T <= 128 || (pl->d.max_ctas && pl->d.max_ctas < 2) ? 1 : 2;
   const int cg_out = pl->d.max_ctas && pl->d.max_ctas < 2 ? 1 : 2;
   int st = make_product(pl, &pl->stats, X_STATS, cg, 0);
+  if (st == GE_OK) st = make_product(pl, &pl->keep, X_KEEP, cg, 2);
   if (st == GE_OK) st = make_product(pl, &pl->dlogit, X_DLOGIT, cg, 2);
   if (st == GE_OK) st = make_product(pl, &pl->out, X_OUT, cg_out, 2);
   if (st == GE_OK) st = make_product(pl, &pl->part, X_PART, cg, 2);
@@ -472,45 +575,37 @@ int configure(gemm_epi_xent_plan *pl) {
       pl->pairs = std::min(pl->pairs, clusters);
     cudaGetLastError();
   }
+  // Rows are packed for a loss alone only where that can save a tile of them.
+  pl->pack = pl->T > 128 * cg;
   // pieces of the vocabulary: as wide as the buffer allows, equal, whole tiles
-  const int64_t bound = pl->d.buffer_bytes ? pl->d.buffer_bytes : int64_t(1) << 30;
+  const int64_t bound = pl->d.buffer_bytes ? pl->d.buffer_bytes : int64_t(1) << 29;
   const int64_t widest = std::max<int64_t>(256, bound / (2 * pl->T) / 256 * 256);
   const int64_t pieces = ceil_div(pl->V, widest);
   pl->piece = round_up(ceil_div(pl->V, pieces), 256);
-  // dH: K (the piece) in as many slices as leave the fewest idle CTAs
+  // dH: slices of its sum over a piece, decided on the device by the rows that
+  // take part, within 64 MiB or what two waves of CTAs take
   const int64_t tiles = tiles_of(pl->part, pl->T, pl->D);
   const int64_t kb = ceil_div(std::min(pl->piece, pl->V), BK);
-  const int units = units_of(pl, pl->part);
-  double best = 0;
-  for (int64_t s = 1; s <= std::min<int64_t>(kb, 64); ++s) {
-    const int64_t kbs = ceil_div(kb, s);
-    if (ceil_div(kb, kbs) != s) continue;
-    // in k-blocks of a tile (0.27 us each): waves of tiles, each its k-blocks and about
-    // six k-blocks' time of set-up and stores, and each slice's way to memory and back
-    const double cost = double(ceil_div(tiles * s, units)) * double(kbs + 6) +
-                        double(s) * double(pl->T) * double(pl->D) * 8.0 / (6.5e6 * 0.27);
-    if (s == 1 || cost < best * 0.97) {
-      best = cost;
-      pl->slices = static_cast<int>(s);
-      pl->kb_split = static_cast<int>(kbs);
-    }
-  }
+  const int64_t fit = (int64_t(64) << 20) / (4 * pl->T * pl->Dp);
+  const int64_t want = 2 * int64_t(units_of(pl, pl->part)) / tiles;
+  pl->slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({std::max(fit, want), kb, 64})));
   // finish: few rows are shared by more threads each
   pl->row_lanes = 32;
   while (pl->row_lanes > 1 && pl->row_lanes / 2 >= pl->T) pl->row_lanes /= 2;
   const int64_t fg = ceil_div(pl->T, pl->row_lanes);
   pl->finish_grid = static_cast<int>(fg);
   for (const Product *pr : {&pl->stats, &pl->part})
-    if (tiles_of(*pr, pl->T, std::max(pl->V, pl->D)) * 64 > (int64_t(1) << 30)) return GE_ERR_SHAPE;
+    if (tiles_of(*pr, pl->T, std::max(pl->V, pl->D)) * pl->slices > (int64_t(1) << 30)) return GE_ERR_SHAPE;
   return GE_OK;
 }
 
-XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, const Scalars *sc, int64_t M, int64_t N,
+XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalars *sc, int64_t M, int64_t N,
                      int64_t K) {
   XentParams p;
   std::memset(static_cast<void *>(&p), 0, sizeof(p));
   p.status = pl->status;
   p.timeout_ns = static_cast<uint64_t>(pl->d.timeout_ms ? pl->d.timeout_ms : 1000) * 1000000ull;
+  p.sc = sc;
   p.rows = &sc->rows;
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
@@ -518,8 +613,6 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, const Scal
   p.num_n_blk = static_cast<int32_t>(ceil_div(N, pr.bn));
   const int64_t m_blk = ceil_div(M, 128 * pr.cg);
   p.raster_group = m_blk <= 16 ? 16 : 12;
-  p.splits = 1;
-  p.kb_split = static_cast<int32_t>(ceil_div(K, BK));
   p.stages = pr.stages;
   p.boxes = pr.boxes;
   p.bf16 = pl->d.ab == GE_BF16;
@@ -532,11 +625,10 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, const Scal
   return p;
 }
 
-cudaError_t launch_product(const gemm_epi_xent_plan *pl, const Product &pr, XentParams &p, int64_t splits,
-                           cudaStream_t s) {
-  const int64_t tiles = tiles_of(pr, p.M, p.N) * splits;
+cudaError_t launch_product(const gemm_epi_xent_plan *pl, const Product &pr, XentParams &p, cudaStream_t s) {
+  const int64_t tiles = tiles_of(pr, p.M, p.N) * (pr.mode == X_PART ? pl->slices : 1);
   const int units = static_cast<int>(std::min<int64_t>(units_of(pl, pr), tiles));
-  return launch(pr.fn, units * pr.cg, kXentThreads, pl->smem, pr.cg, &p, s);
+  return launch(pr.fn, dim3(static_cast<unsigned>(units * pr.cg)), kXentThreads, pl->smem, pr.cg, &p, s);
 }
 
 int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const void *target, const float *weight,
@@ -555,7 +647,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   char *ws = static_cast<char *>(workspace);
   const int64_t T = pl->T, V = pl->V, D = pl->D;
   const int ab = pl->d.ab;
-  Scalars *sc = reinterpret_cast<Scalars *>(ws + at.scalars);
+  XentScalars *sc = reinterpret_cast<XentScalars *>(ws + at.scalars);
   int32_t *index = reinterpret_cast<int32_t *>(ws + at.index);
   int32_t *place = reinterpret_cast<int32_t *>(ws + at.place);
   int32_t *gathered = reinterpret_cast<int32_t *>(ws + at.gathered);
@@ -567,33 +659,69 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   void *Hc = ws + at.Hc;
   void *dl = ws + at.dl;
   float *part = reinterpret_cast<float *>(ws + at.part);
-  const int spread_grid = pl->sms * 8;
-  bool ok = true;
-  auto go = [&](cudaError_t e) { ok = ok && e == cudaSuccess; };
+  const uint64_t piece = static_cast<uint64_t>(pl->piece);
+  const bool pack = grads || pl->pack;
+  const int i32 = pl->d.index == GE_INDEX_I32;
+  cudaError_t err = cudaSuccess;
+  auto go = [&](cudaError_t e) { return (err = e) == cudaSuccess; };
 
-  ScanParams sp{target, weight, loss, lse, sc, index, place, gathered, gweight, V, static_cast<int32_t>(T),
-                pl->d.index == GE_INDEX_I32};
-  go(launch(reinterpret_cast<const void *>(xent_scan_kernel), 1, 1024, 0, 1, &sp, s));
-  GatherParams gp{static_cast<const uint16_t *>(H), static_cast<uint16_t *>(Hc), index, sc, pl->d.ldh, pl->ldc,
-                  static_cast<int32_t>(T), static_cast<int32_t>(D)};
-  go(launch(reinterpret_cast<const void *>(xent_gather_kernel),
-            static_cast<int>(std::min<int64_t>(ceil_div(T, 8), spread_grid)), 256, 0, 1, &gp, s));
+  if (pack) {
+    PackParams pp;
+    std::memset(static_cast<void *>(&pp), 0, sizeof(pp));
+    pp.target = target;
+    pp.weight = weight;
+    pp.H = static_cast<const uint16_t *>(H);
+    pp.Hc = static_cast<uint16_t *>(Hc);
+    pp.loss = loss;
+    pp.lse = lse;
+    pp.sc = sc;
+    pp.index = index;
+    pp.place = place;
+    pp.gathered = gathered;
+    pp.gweight = gweight;
+    pp.V = V;
+    pp.ldh = pl->d.ldh;
+    pp.ldc = pl->ldc;
+    pp.T = static_cast<int32_t>(T);
+    pp.D = static_cast<int32_t>(D);
+    pp.i32 = i32;
+    const int ctas = static_cast<int>(std::min<int64_t>(ceil_div(T, 8), 2 * pl->sms));
+    pp.rows_per_cta = static_cast<int32_t>(ceil_div(T, ctas));
+    pp.part_m = 128 * pl->part.cg;
+    pp.part_n_blk = static_cast<int32_t>(ceil_div(D, pl->part.bn));
+    pp.part_kb = static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK));
+    pp.part_units = units_of(pl, pl->part);
+    pp.part_slices = pl->slices;
+    if (!go(launch(reinterpret_cast<const void *>(xent_pack_kernel), ctas, kPackThreads, 0, 1, &pp, s)))
+      return GE_ERR_CUDA;
+  }
 
-  XentParams sl = params_of(pl, pl->stats, sc, T, V, D);
-  ok = ok && encode_rows(&sl.tmA, ab, Hc, D, T, 1, pl->ldc, pl->ldc * T, BK, 128);
-  ok = ok && encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128);
-  if (!ok) return GE_ERR_CUDA;
-  sl.target = gathered;
+  const bool kept = grads && ab == GE_BF16;  // fp16: see kKeptBits
+  const Product &first = kept ? pl->keep : pl->stats;
+  XentParams sl = params_of(pl, first, sc, T, V, D);
+  const int64_t lda = pack ? pl->ldc : pl->d.ldh;
+  if (!encode_rows(&sl.tmA, ab, pack ? Hc : H, D, T, 1, lda, lda * T, BK, 128) ||
+      !encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128))
+    return GE_ERR_CUDA;
+  if (!pack) sl.rows = nullptr;
+  sl.target = pack ? static_cast<const void *>(gathered) : target;
+  sl.target_i64 = !pack && !i32;
   sl.stats = stats;
   sl.at_target = at_target;
-  go(launch_product(pl, pl->stats, sl, 1, s));
+  if (kept) {
+    sl.keep_cols = static_cast<int32_t>(std::min<int64_t>(pl->piece, round_up(V, 256)));
+    if (!encode_rows(&sl.tmOut, ab, dl, piece, T, 1, piece, piece * T, 64, 128)) return GE_ERR_CUDA;
+  }
+  if (!go(launch_product(pl, first, sl, s))) return GE_ERR_CUDA;
 
   FinishParams fp;
   std::memset(static_cast<void *>(&fp), 0, sizeof(fp));
   fp.stats = stats;
   fp.at_target = at_target;
-  fp.index = index;
+  fp.index = pack ? index : nullptr;
   fp.gweight = gweight;
+  fp.target = target;
+  fp.weight = weight;
   fp.loss = loss;
   fp.lse = lse;
   fp.total = total;
@@ -602,65 +730,84 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   fp.block_sum = reinterpret_cast<double *>(ws + at.block_sum);
   fp.block_top = reinterpret_cast<float *>(ws + at.block_top);
   fp.sc = sc;
+  fp.V = V;
   fp.T = static_cast<int32_t>(T);
+  fp.i32 = i32;
   fp.slots = slots_of(pl);
   fp.row_lanes = pl->row_lanes;
   fp.mean = pl->d.reduction == GE_XENT_MEAN;
   fp.z = pl->d.z_loss;
   fp.grad_scale = grad_scale;
   fp.c = pl->d.logit_scale;
-  go(launch(reinterpret_cast<const void *>(xent_finish_kernel), pl->finish_grid, 1024, 0, 1, &fp, s));
-  if (!grads) return ok ? GE_OK : GE_ERR_CUDA;
+  if (!go(launch(reinterpret_cast<const void *>(xent_finish_kernel), pl->finish_grid, 1024, 0, 1, &fp, s)))
+    return GE_ERR_CUDA;
+  if (!grads) return GE_OK;
 
-  ScaleParams cp{coef, sc};
-  go(launch(reinterpret_cast<const void *>(xent_scale_kernel),
-            static_cast<int>(std::min<int64_t>(ceil_div(T, 256), pl->sms)), 256, 0, 1, &cp, s));
-  const uint64_t piece = static_cast<uint64_t>(pl->piece);
   for (int64_t v0 = 0; v0 < V; v0 += pl->piece) {
     const int64_t n = std::min(pl->piece, V - v0);
-    XentParams q = params_of(pl, pl->dlogit, sc, T, n, D);
-    q.tmA = sl.tmA;
-    q.tmB = sl.tmB;
-    ok = ok && encode_rows(&q.tmOut, ab, dl, piece, T, 1, piece, piece * T, 64, 128);
-    q.b_row0 = static_cast<int32_t>(v0);
-    q.target = gathered;
-    q.lse2 = lse2;
-    q.coef = coef;
-    if (!ok) return GE_ERR_CUDA;
-    go(launch_product(pl, pl->dlogit, q, 1, s));
+    if (kept && v0 == 0) {
+      ConvertParams cp;
+      std::memset(static_cast<void *>(&cp), 0, sizeof(cp));
+      cp.buf = static_cast<uint16_t *>(dl);
+      cp.stats = stats;
+      cp.at_target = at_target;
+      cp.lse2 = lse2;
+      cp.coef = coef;
+      cp.gathered = gathered;
+      cp.sc = sc;
+      cp.pitch = pl->piece;
+      cp.T = static_cast<int32_t>(T);
+      cp.N = static_cast<int32_t>(n);
+      cp.bn = first.bn;
+      cp.c2 = sl.c2;
+      cp.c = sl.c;
+      const unsigned cols = static_cast<unsigned>(ceil_div(n, 256));
+      const unsigned rows = static_cast<unsigned>(
+          std::max<int64_t>(1, std::min<int64_t>(ceil_div(T, kConvertRows), ceil_div(16 * pl->sms, cols))));
+      if (!go(launch(reinterpret_cast<const void *>(xent_convert_kernel), dim3(cols, rows), 256, 0, 1, &cp, s)))
+        return GE_ERR_CUDA;
+    } else {
+      XentParams q = params_of(pl, pl->dlogit, sc, T, n, D);
+      q.tmA = sl.tmA;
+      q.tmB = sl.tmB;
+      q.b_row0 = static_cast<int32_t>(v0);
+      q.target = gathered;
+      q.lse2 = lse2;
+      q.coef = coef;
+      if (!encode_rows(&q.tmOut, ab, dl, piece, T, 1, piece, piece * T, 64, 128) ||
+          !go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
+    }
     if (dW) {
       XentParams o = params_of(pl, pl->out, sc, n, D, T);
-      ok = ok && encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, 64, BK);
-      ok = ok && encode_rows(&o.tmB, ab, Hc, D, T, 1, pl->ldc, pl->ldc * T, 64, BK);
       o.tma_cols = static_cast<int32_t>(D / 8 * 8);
       o.out = static_cast<uint16_t *>(dW);
       o.ld_out = pl->d.lddw;
-      if (o.tma_cols)
-        ok = ok && encode_rows(&o.tmOut, ab, dW, o.tma_cols, V, 1, pl->d.lddw, pl->d.lddw * V, 64, 128);
       o.b_row0 = static_cast<int32_t>(v0);
-      if (!ok) return GE_ERR_CUDA;
-      go(launch_product(pl, pl->out, o, 1, s));
+      if (!encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, 64, BK) ||
+          !encode_rows(&o.tmB, ab, Hc, D, T, 1, pl->ldc, pl->ldc * T, 64, BK) ||
+          (o.tma_cols && !encode_rows(&o.tmOut, ab, dW, o.tma_cols, V, 1, pl->d.lddw, pl->d.lddw * V, 64, 128)) ||
+          !go(launch_product(pl, pl->out, o, s)))
+        return GE_ERR_CUDA;
     }
     if (dH) {
       XentParams o = params_of(pl, pl->part, sc, T, D, n);
-      ok = ok && encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, BK, 128);
-      ok = ok && encode_rows(&o.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, 64, BK);
-      ok = ok && encode_rows(&o.tmOut, GE_F32, part, pl->Dp, T, pl->slices, pl->Dp, pl->Dp * T, 32, 128);
       o.b_row0 = static_cast<int32_t>(v0);
-      o.kb_split = pl->kb_split;
-      o.splits = static_cast<int32_t>(ceil_div(ceil_div(n, BK), pl->kb_split));
       o.accumulate = v0 > 0;
-      if (!ok) return GE_ERR_CUDA;
-      go(launch_product(pl, pl->part, o, o.splits, s));
+      if (!encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, BK, 128) ||
+          !encode_rows(&o.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, 64, BK) ||
+          !encode_rows(&o.tmOut, GE_F32, part, pl->Dp, T, pl->slices, pl->Dp, pl->Dp * T, 32, 128) ||
+          !go(launch_product(pl, pl->part, o, s)))
+        return GE_ERR_CUDA;
     }
   }
   if (dH) {
     SpreadParams dp{part, static_cast<uint16_t *>(dH), place, sc, pl->d.lddh, pl->Dp, static_cast<int32_t>(T),
-                    static_cast<int32_t>(D), pl->slices, ab == GE_BF16};
-    go(launch(reinterpret_cast<const void *>(xent_spread_kernel),
-              static_cast<int>(std::min<int64_t>(ceil_div(T * ceil_div(D, 8), 256), spread_grid)), 256, 0, 1, &dp, s));
+                    static_cast<int32_t>(D), static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK)),
+                    ab == GE_BF16};
+    const int grid = static_cast<int>(std::min<int64_t>(ceil_div(T * ceil_div(D, 4), 256), pl->sms * 8));
+    if (!go(launch(reinterpret_cast<const void *>(xent_spread_kernel), grid, 256, 0, 1, &dp, s))) return GE_ERR_CUDA;
   }
-  return ok ? GE_OK : GE_ERR_CUDA;
+  return GE_OK;
 }
 
 }  // namespace

@@ -11,7 +11,24 @@ enum XentMode {
   X_DLOGIT = 1,  // logits again: their gradient, rounded, into the piece buffer
   X_OUT = 2,     // a gradient: scaled, rounded, stored (dW)
   X_PART = 3,    // fp32 partial sums (dH), stored or added to what is there
+  X_KEEP = 4,    // X_STATS, and the logits' distances below their range's maximum, 16 bits each
 };
+
+// Device scalars of a run, at the start of the workspace.
+struct XentScalars {
+  int32_t rows;       // rows that take part
+  int32_t ticket;     // finish blocks done
+  int32_t kb_split;   // k-blocks of a slice of dH's sum over the vocabulary
+  float out_scale;    // multiplies dl @ W and dl^T @ H
+  float dl_scale;     // power of two in dl
+};
+
+// A kept logit is its distance below its range's maximum in log2 units, in
+// fixed point with 11 bits after the point: p comes out off by at most 2^-12 ln 2 =
+// 1.7e-4, a twentieth of bf16's rounding (2^-8), and what is below 2^-32 of the maximum of
+// its own 64 to 128 columns counts as 0.  fp16 rounds too finely for that
+// (2^-11), so its logits are not kept but computed twice.
+constexpr int kKeptBits = 11;
 
 constexpr int kXentBoxes = 2;            // output boxes per epilogue group, at most
 constexpr uint32_t kXentBox = 128 * 128; // one box: 128 rows of 128 bytes
@@ -20,10 +37,10 @@ struct XentParams {
   CUtensorMap tmA, tmB, tmOut;
   uint32_t *status;
   uint64_t timeout_ns;
-  const int32_t *rows;     // rows that take part (device)
+  XentScalars *sc;
+  const int32_t *rows;     // rows that take part (device); nullptr: all M
   int32_t M, N, K;         // sizes at most; the rows replace M (K for X_OUT)
   int32_t num_n_blk, raster_group;
-  int32_t kb_split, splits;  // k-blocks per slice of K and slices (X_PART)
   int32_t stages, boxes;
   int32_t bf16;
   int32_t b_row0;          // first vocabulary row of this piece
@@ -31,7 +48,9 @@ struct XentParams {
   uint32_t off_B, off_out, off_bar;
   float c;                 // logit_scale
   float c2;                // logit_scale * log2(e)
-  const int32_t *target;   // gathered rows: the target, ...
+  const void *target;      // the rows' targets, ...
+  int32_t target_i64;      // ... 8 bytes each, as the caller has them (else 4)
+  int32_t keep_cols;       // X_KEEP: columns that are kept
   float2 *stats;           // [2 * blocks of BN columns][M]: maximum (log2 units), sum
   float *at_target;        // ... the target's logit
   const float *lse2;       // ... log2-sum-exp2 of its logits

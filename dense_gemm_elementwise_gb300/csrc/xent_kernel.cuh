@@ -1,12 +1,14 @@
 // xent_kernel.cuh -- the products of the vocabulary loss on sm_103a.
 //
-// One persistent, warp-specialised kernel in four modes (XentMode):
+// One persistent, warp-specialised kernel in five modes (XentMode):
 //   X_STATS   H @ W^T, K-major operands: logits that never leave the SM.  An
 //             epilogue thread owns one row of the tile and half of its
 //             columns: it takes their maximum, then the sum of
-//             2^(x - maximum), reading the accumulator from TMEM twice (64
-//             loads cost less than rescaling a running sum) and leaves the
+//             2^(x - maximum), reading the accumulator from TMEM twice (that
+//             costs less than rescaling a running sum) and leaves the
 //             pair for the kernel that joins the tiles.
+//   X_KEEP    the same, and each logit's distance below that maximum in 16 bits,
+//             from which dl is made without the product of X_DLOGIT.
 //   X_DLOGIT  the same product: 2^(x - lse) * coef, less the target's 1, rounded
 //             to 16 bits into the piece buffer.
 //   X_OUT     dl^T @ H: dl read M-major, H N-major, the accumulator times one
@@ -95,7 +97,8 @@ template <int CG, int BN, int MODE>
 __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_constant__ XentParams p) {
   using T = TileCfg<CG, BN>;
   constexpr bool kAmn = MODE == X_OUT;                      // A is M-major
-  constexpr bool kBk = MODE == X_STATS || MODE == X_DLOGIT;  // B is K-major
+  constexpr bool kStats = MODE == X_STATS || MODE == X_KEEP;
+  constexpr bool kBk = kStats || MODE == X_DLOGIT;           // B is K-major
   constexpr int kEpi0 = 2;                                   // first epilogue warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -137,20 +140,22 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   griddep_wait();
 
   const Waiter wt{abort_flag, p.status, p.timeout_ns};
-  const int rows = __ldcg(p.rows);
+  const int rows = p.rows ? __ldcg(p.rows) : p.M;
+  if (kStats && blockIdx.x == 0 && threadIdx.x == 0) p.sc->ticket = 0;  // of the kernel that follows
   const int M = MODE == X_OUT ? p.M : min(rows, p.M);
   const int num_m_blk = (M + T::kMmaM - 1) / T::kMmaM;
   // with no rows dW is 0: one k-block is run and its product dropped
   const int num_kb = MODE == X_OUT ? max(1, (min(rows, p.K) + BK - 1) / BK) : (p.K + BK - 1) / BK;
   const int per_slice = num_m_blk * p.num_n_blk;
-  const int num_tiles = MODE == X_PART ? per_slice * p.splits : per_slice;
+  const int kb_split = MODE == X_PART ? __ldcg(&p.sc->kb_split) : num_kb;
+  const int num_tiles = MODE == X_PART ? per_slice * ((num_kb + kb_split - 1) / kb_split) : per_slice;
   const int my_tiles = unit < num_tiles ? (num_tiles - 1 - unit) / n_units + 1 : 0;
   auto tile = [&](int i) {
     XentTile t;
     const int at = unit + i * n_units;
     tile_coords(num_m_blk, p.num_n_blk, p.raster_group, at, t.z, t.mb, t.nb);
-    t.kb0 = MODE == X_PART ? t.z * p.kb_split : 0;
-    t.kb1 = MODE == X_PART ? min(num_kb, t.kb0 + p.kb_split) : num_kb;
+    t.kb0 = MODE == X_PART ? t.z * kb_split : 0;
+    t.kb1 = MODE == X_PART ? min(num_kb, t.kb0 + kb_split) : num_kb;
     return t;
   };
 
@@ -297,12 +302,18 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       int target = -1;
       float lse2 = 0.f, out_scale = 0.f;
       float2 coef = make_float2(0.f, 0.f);
-      if (MODE == X_STATS || MODE == X_DLOGIT) {
-        if (live) target = p.target[m] - p.b_row0 - n0;
-        if (MODE == X_DLOGIT && live) {
-          lse2 = p.lse2[m];
-          coef = p.coef[m];
-        }
+      if ((kStats || MODE == X_DLOGIT) && live) {
+        const int64_t at = p.target_i64 ? static_cast<const int64_t *>(p.target)[m] : static_cast<const int32_t *>(p.target)[m];
+        // no column of this tile for a target that is elsewhere (or does not exist)
+        const int64_t off = at - p.b_row0 - n0;
+        target = off >= 0 && off < BN ? static_cast<int>(off) : -1;
+      }
+      if (MODE == X_DLOGIT && live) {
+        const float ds = p.sc->dl_scale;
+        lse2 = p.lse2[m];
+        coef = p.coef[m];
+        coef.x *= ds;
+        coef.y *= ds;
       }
       if (MODE == X_OUT) out_scale = rows > 0 ? *p.out_scale : 0.f;
       const bool got = wt.wait(bar + kXTmemFull + 8 * abuf, aphase, SITE_EPI_TMEM_FULL);
@@ -320,50 +331,86 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         }
       };
 
-      if constexpr (MODE == X_STATS) {
+      if constexpr (kStats) {
         float v[32];
         auto read = [&](int c0) {
           tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
           tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
           tmem_wait_ld();
+          if (c0 + 32 > limit) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e >= limit) v[e] = p.c2 < 0.f ? INFINITY : -INFINITY;
+          }
         };
+        // 64 columns at a time, in two halves; the groups in turn
         float top = -INFINITY;
-        for (int c0 = grp * 32; c0 < BN; c0 += 64) {
-          read(c0);
-          if (c0 + 32 > limit) {
+        for (int c1 = grp * 64; c1 < BN; c1 += 128)
+#pragma unroll 1
+          for (int c0 = c1; c0 < c1 + 64; c0 += 32) {
+            read(c0);
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e >= limit) v[e] = p.c2 < 0.f ? INFINITY : -INFINITY;
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e] * p.c2);
+            const int at = target - c0;
+            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+              float x = 0.f;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x = at == e ? v[e] : x;
+              if (at >= 0 && at < 32 && target < limit) p.at_target[m] = x * p.c;
+            }
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e] * p.c2);
-          const int at = target - c0;
-          if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-            float x = 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) x = at == e ? v[e] : x;
-            if (at >= 0 && at < 32) p.at_target[m] = x * p.c;
-          }
-        }
         const float off = top == -INFINITY ? 0.f : top;
+        const bool keep = MODE == X_KEEP && n0 < p.keep_cols;
         float sum = 0.f;
-        for (int c0 = grp * 32; c0 < BN; c0 += 64) {
-          read(c0);
-          if (c0 + 64 >= BN) release();
-          if (c0 + 32 > limit) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e >= limit) v[e] = p.c2 < 0.f ? INFINITY : -INFINITY;
+        for (int c1 = grp * 64; c1 < BN; c1 += 128) {
+          uint32_t line = 0;
+          if (keep) {
+            line = boxes + (step & 1) * kXentBox;
+            if (storer) bulk_wait_group_read<1>();
+            group_barrier(bid);  // the box has been read by its last store
+            line += row * 128;
           }
-          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            s0 += ex2(fmaf(v[e], p.c2, -off));
-            s1 += ex2(fmaf(v[e + 1], p.c2, -off));
-            s2 += ex2(fmaf(v[e + 2], p.c2, -off));
-            s3 += ex2(fmaf(v[e + 3], p.c2, -off));
+          for (int h = 0; h < 64; h += 32) {
+            read(c1 + h);
+            if (h == 32 && c1 + 128 >= BN) release();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], p.c2, -off);
+            if (keep) {
+              // the distances, rounded to integers in the low bits of floats of 2^23 and more
+              constexpr float k0 = 8388608.f, kStepsPerOctave = 1 << kKeptBits;
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const float a = fmaxf(fminf(fmaf(v[2 * e], -kStepsPerOctave, k0), k0 + 65535.f), k0);
+                const float b = fmaxf(fminf(fmaf(v[2 * e + 1], -kStepsPerOctave, k0), k0 + 65535.f), k0);
+                w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                st_shared16(line + ((static_cast<uint32_t>(j + h / 8) ^ sw) << 4), w[4 * j], w[4 * j + 1],
+                            w[4 * j + 2], w[4 * j + 3]);
+            }
+            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              s0 += ex2(v[e]);
+              s1 += ex2(v[e + 1]);
+              s2 += ex2(v[e + 2]);
+              s3 += ex2(v[e + 3]);
+            }
+            sum += (s0 + s1) + (s2 + s3);
           }
-          sum += (s0 + s1) + (s2 + s3);
+          if (keep) {
+            fence_proxy_async_smem();
+            group_barrier(bid);
+            if (storer) {
+              tma_store_3d(&p.tmOut, boxes + (step & 1) * kXentBox, n0 + c1,
+                           t.mb * T::kMmaM + static_cast<int>(rank) * BM, 0);
+              bulk_commit_group();
+            }
+            ++step;
+          }
         }
         if (live) p.stats[(2 * int64_t(t.nb) + grp) * p.M + m] = make_float2(top, sum);
       } else {
@@ -464,6 +511,7 @@ const void *pick_xent(int mode) {
     case X_DLOGIT: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_DLOGIT>);
     case X_OUT: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_OUT>);
     case X_PART: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_PART>);
+    case X_KEEP: return reinterpret_cast<const void *>(xent_kernel<CG, BN, X_KEEP>);
     default: return nullptr;
   }
 }

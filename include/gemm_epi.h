@@ -423,8 +423,12 @@ int gemm_epi_plan_info(const gemm_epi_plan *plan, ge_plan_info *info);
  * keeps it clear of fp16's subnormals; dH and dW are summed in fp32 and rounded
  * once.  Results are bit-for-bit repeatable for a given plan and device.
  *
- * The vocabulary is worked through in pieces, so that the 16-bit values kept
- * between two kernels take at most buffer_bytes.
+ * The vocabulary is worked through in pieces, so that the 16-bit values that
+ * pass from one kernel to the next take at most buffer_bytes.  With bf16, the
+ * forward pass leaves each logit of the first piece in that buffer as its
+ * distance below its neighbours' maximum, in 16 bits, and dl is made from it (p off by
+ * up to 1.7e-4 more); other pieces' logits, and fp16's, are computed again.  A
+ * larger buffer so saves up to a quarter of the products.
  */
 typedef enum { GE_XENT_SUM = 0, GE_XENT_MEAN = 1 } ge_xent_reduction;
 typedef enum { GE_INDEX_I64 = 0, GE_INDEX_I32 = 1 } ge_index;
@@ -440,7 +444,7 @@ typedef struct {
   int32_t reserved;     /* 0                                                       */
   int64_t ldh, ldw;     /* row pitches in elements; 0 = D                          */
   int64_t lddh, lddw;
-  int64_t buffer_bytes; /* 0 = 1 GiB; at least 256 columns for all T rows are kept */
+  int64_t buffer_bytes; /* 0 = 512 MiB; at least 256 columns of all T rows   */
 } ge_xent_desc;
 
 typedef struct gemm_epi_xent_plan gemm_epi_xent_plan;
