@@ -28,13 +28,14 @@
 #include "host.h"
 #include "ptx.cuh"
 #include "xent.cuh"
+#include "xent_math.cuh"
 
 using namespace ge;
 
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.69314718055994531;
+constexpr float kLn2Hi = 0.69314718f, kLn2Lo = static_cast<float>(0.69314718055994531 - double(kLn2Hi));
 
 __device__ __forceinline__ int64_t target_of(const void *t, int i32, int64_t i) {
   return i32 ? static_cast<const int32_t *>(t)[i] : static_cast<const int64_t *>(t)[i];
@@ -114,13 +115,11 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack_kernel(const __grid_co
   }
   auto copy = [&](const uint16_t *src, int64_t r) {  // a warp copies one row, or zeros
     uint16_t *dst = p.Hc + r * p.ldc;
-    for (int c = lane * 8; c < p.D; c += 256) {
-      if (c + 8 <= p.D) {
-        *reinterpret_cast<uint4 *>(dst + c) = src ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        for (int i = c; i < p.D; ++i) dst[i] = src ? src[i] : uint16_t(0);
-      }
-    }
+    const int whole = p.D / 8 * 8;
+#pragma unroll 4
+    for (int c = lane * 8; c < whole; c += 256)
+      *reinterpret_cast<uint4 *>(dst + c) = src ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    if (whole + lane < p.D) dst[whole + lane] = src ? src[whole + lane] : uint16_t(0);
   };
   for (int64_t first = begin; first < end; first += kPackThreads) {
     const int64_t i = first + threadIdx.x;
@@ -149,10 +148,11 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack_kernel(const __grid_co
       if (p.lse) p.lse[i] = 0.f;
     }
     __syncthreads();
-    for (int k = warp; k < here; k += kPackThreads / 32) copy(p.H + rows[k] * p.ldh, before + k);
+    // with every row taking part the products read H itself
+    for (int k = warp; k < (all < p.T ? here : 0); k += kPackThreads / 32) copy(p.H + rows[k] * p.ldh, before + k);
     before += here;
   }
-  if (blockIdx.x == gridDim.x - 1) {
+  if (blockIdx.x == gridDim.x - 1 && all < p.T) {
     const int64_t stop = min(int64_t(p.T), (int64_t(all) + BK - 1) / BK * BK);
     for (int64_t r = all + warp; r < stop; r += kPackThreads / 32) copy(nullptr, r);
   }
@@ -168,8 +168,7 @@ struct FinishParams {
   float *loss, *lse, *total;
   float *lse2;
   float2 *coef;
-  double *block_sum;         // per block: of losses, of weights
-  float *block_top;
+  float4 *block_sums;        // per block: losses, weights, the largest factor of dl
   XentScalars *sc;
   int64_t V;
   int32_t T, i32, slots, row_lanes;  // row_lanes rows per block of 1024 threads
@@ -183,24 +182,33 @@ __device__ __forceinline__ float2 join(float2 a, float2 b) {
   return make_float2(top, a.y * exp2f(a.x - off) + b.y * exp2f(b.x - off));
 }
 
+__device__ __forceinline__ float3 add_over_warp(float3 v) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
+    v.z = fmaxf(v.z, __shfl_xor_sync(0xffffffffu, v.z, s));
+  }
+  return v;
+}
+
 // row_lanes consecutive rows per block; the other threads share each row's
-// column ranges.  The last block to finish adds the blocks' sums in order.
-// Bound by the latency of its loads when rows are few and by their bytes (8 per
-// row and 64 or 128 columns) when they are many.
+// column ranges.  The last block to finish adds the blocks' sums, as every sum here
+// in a tree of fixed shape.  Bound by the latency of its loads and barriers when rows are
+// few and by its bytes (8 per row and 64 or 128 columns) when they are many.
 __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant__ FinishParams p) {
   __shared__ float2 pairs[1024];
-  __shared__ double dbuf[2][32];
-  __shared__ float fbuf[32];
+  __shared__ float4 sums[32];
   __shared__ bool last;
   griddep_wait();
   griddep_launch_dependents();
   const int rows = p.index ? p.sc->rows : p.T;
   const int per = p.row_lanes, lanes = 1024 / per;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int x = threadIdx.x % per, y = threadIdx.x / per;
   const int r = blockIdx.x * per + x;
-  const bool on = r < rows;
   float2 all = make_float2(-INFINITY, 0.f);
-  if (on) {
+  if (r < rows) {
     for (int s = y; s < p.slots; s += 8 * lanes) {
       float2 v[8];
 #pragma unroll
@@ -216,100 +224,91 @@ __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant
       all = make_float2(top, sum);
     }
   }
-  pairs[threadIdx.x] = all;
+  // threads of the same row within a warp, then warp x joins row x's 32 warps
+  for (int h = per; h < 32; h <<= 1)
+    all = join(all, make_float2(__shfl_xor_sync(0xffffffffu, all.x, h), __shfl_xor_sync(0xffffffffu, all.y, h)));
+  if (lane < per) pairs[warp * per + lane] = all;
   __syncthreads();
-  for (int h = lanes / 2; h > 0; h >>= 1) {
-    if (y < h) pairs[threadIdx.x] = join(pairs[threadIdx.x], pairs[threadIdx.x + h * per]);
-    __syncthreads();
-  }
-  double loss = 0.0, weight = 0.0;
-  float big = 0.f;
-  if (y == 0 && on) {
-    all = pairs[x];
-    int64_t i = r;
-    bool take = true;
-    float w = 1.f;
-    if (p.index) {
-      i = p.index[r];
-      w = p.gweight[r];
-    } else {
-      const int64_t t = target_of(p.target, p.i32, i);
-      take = t >= 0 && t < p.V;
-      if (p.weight) w = p.weight[i];
-    }
-    if (take) {
-      const double l2 = double(all.x == -INFINITY ? 0.f : all.x) + double(log2f(all.y));
-      const double lse = l2 * kLn2;
-      loss = double(w) * (lse - double(p.at_target[r]) + double(p.z) * lse * lse);
-      weight = w;
-      if (p.loss) p.loss[i] = static_cast<float>(loss);
-      if (p.lse) p.lse[i] = static_cast<float>(lse);
-      if (p.coef) {
-        const float zf = static_cast<float>(1.0 + 2.0 * double(p.z) * lse);
-        p.lse2[r] = static_cast<float>(l2);
-        p.coef[r] = make_float2(w * zf, w);
-        const float b = fabsf(w) * fmaxf(1.f, fabsf(zf));
-        big = isfinite(b) ? b : 0.f;
-      }
-    } else {
-      if (p.loss) p.loss[i] = 0.f;
-      if (p.lse) p.lse[i] = 0.f;
-    }
-  }
-  auto over_warp = [&]() {
+  float3 sum = make_float3(0.f, 0.f, 0.f);
+  if (warp < per) {
+    const int row = blockIdx.x * per + warp;
+    all = pairs[lane * per + warp];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) {
-      loss += __shfl_xor_sync(0xffffffffu, loss, s);
-      weight += __shfl_xor_sync(0xffffffffu, weight, s);
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, s));
+    for (int h = 16; h > 0; h >>= 1)
+      all = join(all, make_float2(__shfl_xor_sync(0xffffffffu, all.x, h), __shfl_xor_sync(0xffffffffu, all.y, h)));
+    if (lane == 0 && row < rows) {
+      int64_t i = row;
+      bool take = true;
+      float w = 1.f;
+      if (p.index) {
+        i = p.index[row];
+        w = p.gweight[row];
+      } else {
+        const int64_t t = target_of(p.target, p.i32, i);
+        take = t >= 0 && t < p.V;
+        if (p.weight) w = p.weight[i];
+      }
+      if (take) {
+        // lse = ln 2 (top + log2 sum), its large part split so that loss loses nothing to it
+        const float top = all.x == -INFINITY ? 0.f : all.x, l2 = log2f(all.y);
+        const float big = top * kLn2Hi;
+        const float rest = fmaf(top, kLn2Hi, -big) + fmaf(top, kLn2Lo, l2 * kLn2Hi);
+        const float lse = big + rest;
+        const float loss = w * (((big - p.at_target[row]) + rest) + p.z * lse * lse);
+        if (p.loss) p.loss[i] = loss;
+        if (p.lse) p.lse[i] = lse;
+        sum = make_float3(loss, w, 0.f);
+        if (p.coef) {
+          const float zf = 1.f + 2.f * p.z * lse;
+          p.lse2[row] = top + l2;
+          p.coef[row] = make_float2(w * zf, w);
+          const float b = fabsf(w) * fmaxf(1.f, fabsf(zf));
+          sum.z = isfinite(b) ? b : 0.f;
+        }
+      } else {
+        if (p.loss) p.loss[i] = 0.f;
+        if (p.lse) p.lse[i] = 0.f;
+      }
     }
-  };
-  // rows of the block live in its first `per` (at most 32) threads
-  if (threadIdx.x < 32) {
-    over_warp();
-    if (threadIdx.x == 0) {
-      p.block_sum[2 * blockIdx.x] = loss;
-      p.block_sum[2 * blockIdx.x + 1] = weight;
-      p.block_top[blockIdx.x] = big;
+  }
+  if (lane == 0) sums[warp] = make_float4(sum.x, sum.y, sum.z, 0.f);
+  __syncthreads();
+  if (warp > 0 && gridDim.x == 1) return;
+  if (warp == 0) {
+    sum = add_over_warp(make_float3(sums[lane].x, sums[lane].y, sums[lane].z));
+    if (lane == 0 && gridDim.x > 1) {
+      p.block_sums[blockIdx.x] = make_float4(sum.x, sum.y, sum.z, 0.f);
       __threadfence();
       last = atomicAdd(&p.sc->ticket, 1) == static_cast<int>(gridDim.x) - 1;
     }
   }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  // each thread adds every 1024th block, then the warps' sums are added in order
-  loss = weight = 0.0;
-  big = 0.f;
-  for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += 1024) {
-    loss += __ldcg(p.block_sum + 2 * b);
-    weight += __ldcg(p.block_sum + 2 * b + 1);
-    big = fmaxf(big, __ldcg(p.block_top + b));
-  }
-  over_warp();
-  if ((threadIdx.x & 31) == 0) {
-    dbuf[0][threadIdx.x >> 5] = loss;
-    dbuf[1][threadIdx.x >> 5] = weight;
-    fbuf[threadIdx.x >> 5] = big;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    loss = weight = 0.0;
-    big = 0.f;
-    for (int w = 0; w < 32; ++w) {
-      loss += dbuf[0][w];
-      weight += dbuf[1][w];
-      big = fmaxf(big, fbuf[w]);
+  if (gridDim.x > 1) {
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    sum = make_float3(0.f, 0.f, 0.f);
+    for (int b = threadIdx.x; b < static_cast<int>(gridDim.x); b += 1024) {
+      const float4 v = __ldcg(p.block_sums + b);
+      sum = make_float3(sum.x + v.x, sum.y + v.y, fmaxf(sum.z, v.z));
     }
-    const double norm = p.mean ? weight : 1.0;
-    if (p.total) *p.total = norm != 0.0 ? static_cast<float>(loss / norm) : 0.f;
-    // dl is at most `big`: brought just below 2^14, clear of fp16's largest value
-    // (65504) and of its subnormals for every p above 2^-28
-    int e = 0;
-    if (big > 0.f) frexpf(big, &e);
-    e = max(-100, min(100, 14 - e));
-    p.sc->dl_scale = ldexpf(1.f, e);
-    p.sc->out_scale = norm != 0.0 ? static_cast<float>(ldexp(double(p.grad_scale) * double(p.c) / norm, -e)) : 0.f;
+    sum = add_over_warp(sum);
+    if (lane == 0) sums[warp] = make_float4(sum.x, sum.y, sum.z, 0.f);
+    __syncthreads();
+    if (warp > 0) return;
+    sum = add_over_warp(make_float3(sums[lane].x, sums[lane].y, sums[lane].z));
+  }
+  if (lane == 0) {
+    const float norm = p.mean ? sum.y : 1.f;
+    if (p.total) *p.total = norm != 0.f ? sum.x / norm : 0.f;
+    if (p.coef) {
+      // dl is at most `big`: brought just below 2^14, clear of fp16's largest value
+      // (65504) and of its subnormals for every p above 2^-28
+      int e = 0;
+      if (sum.z > 0.f) frexpf(sum.z, &e);
+      e = max(-100, min(100, 14 - e));
+      p.sc->dl_scale = ldexpf(1.f, e);
+      p.sc->out_scale = norm != 0.f ? ldexpf(p.grad_scale / norm * p.c, -e) : 0.f;
+    }
   }
 }
 
@@ -363,28 +362,30 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
       const int r = first + warp + 8 * i;
       if (r >= end) continue;
       const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      const float f = coef[i].x * ds;
       float d[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint32_t code = e & 1 ? u[e / 2] >> 16 : u[e / 2] & 0xffffu;
-        const float q = code == 0xffffu ? 0.f : exp2f(fmaf(float(code), -1.f / (1 << kKeptBits), shift[i]));
-        d[e] = q * (coef[i].x * ds);
+        // the code in the low bits of a float of 2^23
+        const float code = __uint_as_float(__byte_perm(u[e / 2], 0x4b000000u, e & 1 ? 0x7432 : 0x7410)) - 8388608.f;
+        const float q = code == 65535.f ? 0.f : ex2(fmaf(code, -1.f / (1 << kKeptBits), shift[i]));
+        d[e] = q * f;
       }
       if (target[i] >= 0 && target[i] < 8) {
         // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p
         const float at = p.at_target[r] * (p.c2 / p.c);
-        const float v = exp2f(at - lse2[i]) * (coef[i].x * ds) - coef[i].y * ds;
+        const float v = ex2(at - lse2[i]) * f - coef[i].y * ds;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (e == target[i]) d[e] = v;
       }
-      union { uint16_t e[8]; uint4 v; } o;
+      if (r >= rows || c0 + 8 > p.N) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float f = r < rows && c0 + e < p.N ? d[e] : 0.f;
-        o.e[e] = __bfloat16_as_ushort(__float2bfloat16_rn(f));
+        for (int e = 0; e < 8; ++e)
+          if (r >= rows || c0 + e >= p.N) d[e] = 0.f;
       }
-      *reinterpret_cast<uint4 *>(p.buf + r * p.pitch + c0) = o.v;
+      *reinterpret_cast<uint4 *>(p.buf + r * p.pitch + c0) =
+          make_uint4(pack16(true, d[0], d[1]), pack16(true, d[2], d[3]), pack16(true, d[4], d[5]), pack16(true, d[6], d[7]));
     }
   }
 }
@@ -467,7 +468,7 @@ cudaError_t launch(const void *fn, dim3 grid, int threads, int smem, int cluster
 }
 
 struct Workspace {
-  size_t scalars, index, place, gathered, gweight, at_target, lse2, coef, block_sum, block_top, stats, Hc, dl, part,
+  size_t scalars, index, place, gathered, gweight, at_target, lse2, coef, block_sums, stats, Hc, dl, part,
       bytes;
 };
 
@@ -507,8 +508,7 @@ Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {
   w.at_target = take(4 * T);
   w.lse2 = take(4 * T);
   w.coef = take(8 * T);
-  w.block_sum = take(16 * static_cast<size_t>(pl->finish_grid));
-  w.block_top = take(4 * static_cast<size_t>(pl->finish_grid));
+  w.block_sums = take(16 * static_cast<size_t>(pl->finish_grid));
   w.stats = take(8 * T * static_cast<size_t>(slots_of(pl)));
   if (grads || pl->pack) w.Hc = take(2 * T * static_cast<size_t>(pl->ldc));
   if (grads) {
@@ -607,6 +607,7 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalar
   p.timeout_ns = static_cast<uint64_t>(pl->d.timeout_ms ? pl->d.timeout_ms : 1000) * 1000000ull;
   p.sc = sc;
   p.rows = &sc->rows;
+  p.all_rows = static_cast<int32_t>(pl->T);
   p.M = static_cast<int32_t>(M);
   p.N = static_cast<int32_t>(N);
   p.K = static_cast<int32_t>(K);
@@ -699,8 +700,9 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   const bool kept = grads && ab == GE_BF16;  // fp16: see kKeptBits
   const Product &first = kept ? pl->keep : pl->stats;
   XentParams sl = params_of(pl, first, sc, T, V, D);
-  const int64_t lda = pack ? pl->ldc : pl->d.ldh;
-  if (!encode_rows(&sl.tmA, ab, pack ? Hc : H, D, T, 1, lda, lda * T, BK, 128) ||
+  if (!encode_rows(&sl.tmA, ab, pack ? Hc : H, D, T, 1, pack ? pl->ldc : pl->d.ldh,
+                   (pack ? pl->ldc : pl->d.ldh) * T, BK, 128) ||
+      !encode_rows(&sl.tmH, ab, H, D, T, 1, pl->d.ldh, pl->d.ldh * T, BK, 128) ||
       !encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128))
     return GE_ERR_CUDA;
   if (!pack) sl.rows = nullptr;
@@ -727,8 +729,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   fp.total = total;
   fp.lse2 = lse2;
   fp.coef = grads ? coef : nullptr;
-  fp.block_sum = reinterpret_cast<double *>(ws + at.block_sum);
-  fp.block_top = reinterpret_cast<float *>(ws + at.block_top);
+  fp.block_sums = reinterpret_cast<float4 *>(ws + at.block_sums);
   fp.sc = sc;
   fp.V = V;
   fp.T = static_cast<int32_t>(T);
@@ -769,6 +770,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
     } else {
       XentParams q = params_of(pl, pl->dlogit, sc, T, n, D);
       q.tmA = sl.tmA;
+      q.tmH = sl.tmH;
       q.tmB = sl.tmB;
       q.b_row0 = static_cast<int32_t>(v0);
       q.target = gathered;
@@ -785,6 +787,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       o.b_row0 = static_cast<int32_t>(v0);
       if (!encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, 64, BK) ||
           !encode_rows(&o.tmB, ab, Hc, D, T, 1, pl->ldc, pl->ldc * T, 64, BK) ||
+          !encode_rows(&o.tmH, ab, H, D, T, 1, pl->d.ldh, pl->d.ldh * T, 64, BK) ||
           (o.tma_cols && !encode_rows(&o.tmOut, ab, dW, o.tma_cols, V, 1, pl->d.lddw, pl->d.lddw * V, 64, 128)) ||
           !go(launch_product(pl, pl->out, o, s)))
         return GE_ERR_CUDA;

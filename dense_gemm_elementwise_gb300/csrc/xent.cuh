@@ -35,10 +35,12 @@ constexpr uint32_t kXentBox = 128 * 128; // one box: 128 rows of 128 bytes
 
 struct XentParams {
   CUtensorMap tmA, tmB, tmOut;
+  CUtensorMap tmH;         // H itself, read in the packed rows' place when every row takes part
   uint32_t *status;
   uint64_t timeout_ns;
   XentScalars *sc;
   const int32_t *rows;     // rows that take part (device); nullptr: all M
+  int32_t all_rows;        // T
   int32_t M, N, K;         // sizes at most; the rows replace M (K for X_OUT)
   int32_t num_n_blk, raster_group;
   int32_t stages, boxes;

@@ -34,14 +34,9 @@
 
 #include "gemm_kernel.cuh"
 #include "xent.cuh"
+#include "xent_math.cuh"
 
 namespace ge {
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void group_barrier(int id) {
   __syncwarp();
@@ -71,13 +66,6 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *m, uint32_t
                    "l"(reinterpret_cast<uint64_t>(m)),
                "r"(src), "r"(x), "r"(y), "r"(z)
                : "memory");
-}
-
-__device__ __forceinline__ uint32_t pack16(bool bf16, float lo, float hi) {
-  uint32_t r;
-  if (bf16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -165,6 +153,9 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       int stage = 0, fills = 0;
       uint32_t phase = 0;
       bool ok = true;
+      // rows of H: packed, or H as it is
+      const bool packed = rows < p.all_rows;
+      const CUtensorMap *mA = kBk && !packed ? &p.tmH : &p.tmA, *mB = MODE == X_OUT && !packed ? &p.tmH : &p.tmB;
       for (int i = 0; ok && i < my_tiles; ++i) {
         const XentTile t = tile(i);
         const int m0 = t.mb * T::kMmaM + static_cast<int>(rank) * BM;
@@ -192,18 +183,18 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             else tma_load_3d(dst, m, fb, x, y, 0);
           };
           if constexpr (kAmn) {
-            load(sa, &p.tmA, m0, kx);
-            load(sa + 8192, &p.tmA, m0 + 64, kx);
+            load(sa, mA, m0, kx);
+            load(sa + 8192, mA, m0 + 64, kx);
           } else {
-            load(sa, &p.tmA, kx, m0);
+            load(sa, mA, kx, m0);
           }
           if constexpr (kBk) {
-            load(sbb, &p.tmB, kx, p.b_row0 + n0);
+            load(sbb, mB, kx, p.b_row0 + n0);
           } else {
             // dH: the k rows of B are the piece's vocabulary rows
             const int ky = MODE == X_PART ? p.b_row0 + kx : kx;
 #pragma unroll
-            for (int j = 0; j < T::kBAtoms; ++j) load(sbb + j * 8192, &p.tmB, n0 + 64 * j, ky);
+            for (int j = 0; j < T::kBAtoms; ++j) load(sbb + j * 8192, mB, n0 + 64 * j, ky);
           }
           ++fills;
           if (++stage == p.stages) {
@@ -365,8 +356,11 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         for (int c1 = grp * 64; c1 < BN; c1 += 128) {
           uint32_t line = 0;
           if (keep) {
-            line = boxes + (step & 1) * kXentBox;
-            if (storer) bulk_wait_group_read<1>();
+            line = boxes + (p.boxes == 2 ? step & 1 : 0) * kXentBox;
+            if (storer) {
+              if (p.boxes == 2) bulk_wait_group_read<1>();
+              else bulk_wait_group_read<0>();
+            }
             group_barrier(bid);  // the box has been read by its last store
             line += row * 128;
           }
@@ -405,7 +399,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             fence_proxy_async_smem();
             group_barrier(bid);
             if (storer) {
-              tma_store_3d(&p.tmOut, boxes + (step & 1) * kXentBox, n0 + c1,
+              tma_store_3d(&p.tmOut, boxes + (p.boxes == 2 ? step & 1 : 0) * kXentBox, n0 + c1,
                            t.mb * T::kMmaM + static_cast<int>(rank) * BM, 0);
               bulk_commit_group();
             }
