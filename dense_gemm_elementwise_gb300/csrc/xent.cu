@@ -515,7 +515,7 @@ Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {
     w.dl = take(2 * T * static_cast<size_t>(pl->piece));
     w.part = take(4 * T * static_cast<size_t>(pl->Dp) * static_cast<size_t>(pl->slices));
   }
-  w.bytes = at;
+  w.bytes = at + 256;  // to start on 256 bytes wherever the workspace does
   return w;
 }
 
@@ -553,10 +553,10 @@ int configure(gemm_epi_xent_plan *pl) {
   const int cg = pl->T <= 128 || (pl->d.max_ctas && pl->d.max_ctas < 2) ? 1 : 2;
   const int cg_out = pl->d.max_ctas && pl->d.max_ctas < 2 ? 1 : 2;
   int st = make_product(pl, &pl->stats, X_STATS, cg, 0);
-  if (st == GE_OK) st = make_product(pl, &pl->keep, X_KEEP, cg, 2);
-  if (st == GE_OK) st = make_product(pl, &pl->dlogit, X_DLOGIT, cg, 2);
-  if (st == GE_OK) st = make_product(pl, &pl->out, X_OUT, cg_out, 2);
-  if (st == GE_OK) st = make_product(pl, &pl->part, X_PART, cg, 2);
+  if (st == GE_OK) st = make_product(pl, &pl->keep, X_KEEP, cg, 0);
+  if (st == GE_OK) st = make_product(pl, &pl->dlogit, X_DLOGIT, cg, 0);
+  if (st == GE_OK) st = make_product(pl, &pl->out, X_OUT, cg_out, 0);
+  if (st == GE_OK) st = make_product(pl, &pl->part, X_PART, cg, kXentBoxes);
   if (st != GE_OK) return st;
   pl->pairs = pl->sms / 2;
   if (cg_out == 2) {
@@ -615,7 +615,6 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalar
   const int64_t m_blk = ceil_div(M, 128 * pr.cg);
   p.raster_group = m_blk <= 16 ? 16 : 12;
   p.stages = pr.stages;
-  p.boxes = pr.boxes;
   p.bf16 = pl->d.ab == GE_BF16;
   p.off_B = pr.off_B;
   p.off_out = pr.off_out;
@@ -645,7 +644,8 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   if (!std::isfinite(grad_scale)) return GE_ERR_INVALID;
   const Workspace at = workspace_of(pl, grads);
   if (!workspace || !is_aligned16(workspace) || workspace_bytes < at.bytes) return GE_ERR_WORKSPACE;
-  char *ws = static_cast<char *>(workspace);
+  // the buffers in it start on 256 bytes
+  char *ws = reinterpret_cast<char *>(round_up(static_cast<int64_t>(reinterpret_cast<uintptr_t>(workspace)), 256));
   const int64_t T = pl->T, V = pl->V, D = pl->D;
   const int ab = pl->d.ab;
   XentScalars *sc = reinterpret_cast<XentScalars *>(ws + at.scalars);
@@ -712,7 +712,8 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   sl.at_target = at_target;
   if (kept) {
     sl.keep_cols = static_cast<int32_t>(std::min<int64_t>(pl->piece, round_up(V, 256)));
-    if (!encode_rows(&sl.tmOut, ab, dl, piece, T, 1, piece, piece * T, 64, 128)) return GE_ERR_CUDA;
+    sl.out = static_cast<uint16_t *>(dl);
+    sl.ld_out = pl->piece;
   }
   if (!go(launch_product(pl, first, sl, s))) return GE_ERR_CUDA;
 
@@ -776,19 +777,19 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       q.target = gathered;
       q.lse2 = lse2;
       q.coef = coef;
-      if (!encode_rows(&q.tmOut, ab, dl, piece, T, 1, piece, piece * T, 64, 128) ||
-          !go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
+      q.out = static_cast<uint16_t *>(dl);
+      q.ld_out = pl->piece;
+      if (!go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
     }
     if (dW) {
       XentParams o = params_of(pl, pl->out, sc, n, D, T);
-      o.tma_cols = static_cast<int32_t>(D / 8 * 8);
       o.out = static_cast<uint16_t *>(dW);
       o.ld_out = pl->d.lddw;
+      o.out32 = pl->d.lddw % 16 == 0 && reinterpret_cast<uintptr_t>(dW) % 32 == 0;
       o.b_row0 = static_cast<int32_t>(v0);
       if (!encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, 64, BK) ||
           !encode_rows(&o.tmB, ab, Hc, D, T, 1, pl->ldc, pl->ldc * T, 64, BK) ||
           !encode_rows(&o.tmH, ab, H, D, T, 1, pl->d.ldh, pl->d.ldh * T, 64, BK) ||
-          (o.tma_cols && !encode_rows(&o.tmOut, ab, dW, o.tma_cols, V, 1, pl->d.lddw, pl->d.lddw * V, 64, 128)) ||
           !go(launch_product(pl, pl->out, o, s)))
         return GE_ERR_CUDA;
     }

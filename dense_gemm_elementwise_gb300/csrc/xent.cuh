@@ -30,7 +30,7 @@ struct XentScalars {
 // (2^-11), so its logits are not kept but computed twice.
 constexpr int kKeptBits = 11;
 
-constexpr int kXentBoxes = 2;            // output boxes per epilogue group, at most
+constexpr int kXentBoxes = 2;            // X_PART: output boxes per epilogue group
 constexpr uint32_t kXentBox = 128 * 128; // one box: 128 rows of 128 bytes
 
 struct XentParams {
@@ -43,7 +43,7 @@ struct XentParams {
   int32_t all_rows;        // T
   int32_t M, N, K;         // sizes at most; the rows replace M (K for X_OUT)
   int32_t num_n_blk, raster_group;
-  int32_t stages, boxes;
+  int32_t stages;
   int32_t bf16;
   int32_t b_row0;          // first vocabulary row of this piece
   int32_t accumulate;      // X_PART: add to the slices
@@ -58,11 +58,9 @@ struct XentParams {
   const float *lse2;       // ... log2-sum-exp2 of its logits
   const float2 *coef;      // ... factors of p and of the target's 1
   const float *out_scale;  // one float
-  // X_OUT: the TMA engine writes whole 16-byte units, so it is given the columns
-  // up to the last whole unit and the threads write the rest of each row
-  int32_t tma_cols;
-  uint16_t *out;
+  uint16_t *out;           // X_KEEP, X_DLOGIT: the piece buffer; X_OUT: dW
   int64_t ld_out;
+  int32_t out32;           // X_OUT: its rows are whole 32-byte units
 };
 
 const void *xent_kernel_cg1(int mode);  // 128 x 128 tiles, one CTA

@@ -20,10 +20,9 @@
 //             of the additions is that of the launches.
 // Warps: 0 loads operands (TMA, an S-stage ring), 1 allocates TMEM and issues
 // tcgen05.mma into one of two accumulators, 2..9 are two epilogue groups of
-// four warps that take the tile's column steps in turn.  The number of rows that
+// four warps that take the tile's column steps in turn, a thread to a row.  The number of rows that
 // take part is read from device memory, so a batch with ignored targets costs
-// what its other rows cost.  Mainloop and roles follow gemm_kernel.cuh; the
-// epilogue groups store through their own boxes.
+// what its other rows cost.  Mainloop and roles follow gemm_kernel.cuh.
 //
 // The products are bound by the tensor pipe when the batch is long and by
 // reading W when it is short.
@@ -71,6 +70,18 @@ __device__ __forceinline__ void tma_reduce_add_3d(const CUtensorMap *m, uint32_t
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
+}
+
+// 16 values of 16 bits to global memory: 32 bytes at once where they are aligned so
+__device__ __forceinline__ void st_global32(uint16_t *p, const uint32_t *w, bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // barrier block
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
     const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
     const int row = q * 32 + lane;            // of the CTA's 128 accumulator rows
     const uint32_t sw = static_cast<uint32_t>(row & 7);
-    const uint32_t boxes = sb + p.off_out + grp * p.boxes * kXentBox;
+    const uint32_t boxes = sb + p.off_out + grp * kXentBoxes * kXentBox;
     int abuf = 0, step = 0;
     uint32_t aphase = 0;
     for (int i = 0; i < my_tiles; ++i) {
@@ -351,23 +362,13 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             }
           }
         const float off = top == -INFINITY ? 0.f : top;
-        const bool keep = MODE == X_KEEP && n0 < p.keep_cols;
+        const bool keep = MODE == X_KEEP && n0 < p.keep_cols && live;
         float sum = 0.f;
         for (int c1 = grp * 64; c1 < BN; c1 += 128) {
-          uint32_t line = 0;
-          if (keep) {
-            line = boxes + (p.boxes == 2 ? step & 1 : 0) * kXentBox;
-            if (storer) {
-              if (p.boxes == 2) bulk_wait_group_read<1>();
-              else bulk_wait_group_read<0>();
-            }
-            group_barrier(bid);  // the box has been read by its last store
-            line += row * 128;
-          }
-#pragma unroll
-          for (int h = 0; h < 64; h += 32) {
-            read(c1 + h);
-            if (h == 32 && c1 + 128 >= BN) release();
+#pragma unroll 1
+          for (int c0 = c1; c0 < c1 + 64; c0 += 32) {
+            read(c0);
+            if (c0 + 96 >= BN && c0 != c1) release();
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], p.c2, -off);
             if (keep) {
@@ -380,10 +381,9 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
                 const float b = fmaxf(fminf(fmaf(v[2 * e + 1], -kStepsPerOctave, k0), k0 + 65535.f), k0);
                 w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
               }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                st_shared16(line + ((static_cast<uint32_t>(j + h / 8) ^ sw) << 4), w[4 * j], w[4 * j + 1],
-                            w[4 * j + 2], w[4 * j + 3]);
+              uint16_t *o = p.out + int64_t(m) * p.ld_out + n0 + c0;
+              st_global32(o, w, true);
+              st_global32(o + 16, w + 8, true);
             }
             float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
@@ -395,96 +395,84 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             }
             sum += (s0 + s1) + (s2 + s3);
           }
-          if (keep) {
-            fence_proxy_async_smem();
-            group_barrier(bid);
-            if (storer) {
-              tma_store_3d(&p.tmOut, boxes + (p.boxes == 2 ? step & 1 : 0) * kXentBox, n0 + c1,
-                           t.mb * T::kMmaM + static_cast<int>(rank) * BM, 0);
-              bulk_commit_group();
-            }
-            ++step;
-          }
         }
         if (live) p.stats[(2 * int64_t(t.nb) + grp) * p.M + m] = make_float2(top, sum);
-      } else {
-        constexpr int kStep = MODE == X_PART ? 32 : 64;  // columns of a box: 128 bytes
-        for (int c0 = grp * kStep; c0 < BN; c0 += 2 * kStep, ++step) {
-          uint32_t box = boxes;
-          if (p.boxes == 2) {
-            box += (step & 1) * kXentBox;
-            if (storer) bulk_wait_group_read<1>();
-          } else {
-            if (storer) bulk_wait_group_read<0>();
-          }
+      } else if constexpr (MODE == X_PART) {
+        // boxes of 128 rows of 32 columns, which the TMA engine stores or adds
+        for (int c0 = grp * 32; c0 < BN; c0 += 64, ++step) {
+          const uint32_t box = boxes + (step & 1) * kXentBox;
+          if (storer) bulk_wait_group_read<kXentBoxes - 1>();
           group_barrier(bid);  // the box has been read by its last store
-          const uint32_t line = box + row * 128;
+          float v[32];
+          tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
+          tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+          tmem_wait_ld();
+          if (c0 + 64 >= BN) release();
 #pragma unroll
-          for (int h = 0; h < kStep; h += 32) {
-            float v[32];
-            tmem_ld16(acc + c0 + h, *reinterpret_cast<float(*)[16]>(v));
-            tmem_ld16(acc + c0 + h + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-            tmem_wait_ld();
-            if (h + 32 == kStep && c0 + 2 * kStep >= BN) release();
-            if constexpr (MODE == X_PART) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)
-                st_shared16(line + ((static_cast<uint32_t>(j) ^ sw) << 4), __float_as_uint(v[4 * j]),
-                            __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
-                            __float_as_uint(v[4 * j + 3]));
-            } else {
-              if constexpr (MODE == X_DLOGIT) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], p.c2, -lse2)) * coef.x;
-                const int at = target - c0 - h;
-                if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (at == e) v[e] -= coef.y;
-                }
-                // rows and columns that do not exist read as 0 in the products to come
-                if (!live || c0 + h + 32 > limit) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!live || c0 + h + e >= limit) v[e] = 0.f;
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = rows > 0 ? v[e] * out_scale : 0.f;
-                const int col = n0 + c0 + h;
-                if (col + 32 > p.tma_cols && col < p.N && live) {
-                  uint16_t *o = p.out + (int64_t(p.b_row0) + m) * p.ld_out;
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (col + e >= p.tma_cols && col + e < p.N)
-                      o[col + e] = static_cast<uint16_t>(pack16(p.bf16, v[e], 0.f));
-                }
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                st_shared16(line + ((static_cast<uint32_t>(j + h / 8) ^ sw) << 4),
-                            pack16(p.bf16, v[8 * j], v[8 * j + 1]), pack16(p.bf16, v[8 * j + 2], v[8 * j + 3]),
-                            pack16(p.bf16, v[8 * j + 4], v[8 * j + 5]), pack16(p.bf16, v[8 * j + 6], v[8 * j + 7]));
-            }
-          }
+          for (int j = 0; j < 8; ++j)
+            st_shared16(box + row * 128 + ((static_cast<uint32_t>(j) ^ sw) << 4), __float_as_uint(v[4 * j]),
+                        __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
           fence_proxy_async_smem();
           group_barrier(bid);
           if (storer) {
-            const int x = n0 + c0;
-            const int y = t.mb * T::kMmaM + static_cast<int>(rank) * BM + (MODE == X_OUT ? p.b_row0 : 0);
-            // nothing is stored outside the tensor's columns: the box would be clipped whole
-            if (MODE == X_DLOGIT || x < (MODE == X_OUT ? p.tma_cols : p.N)) {
-              if (MODE == X_PART && p.accumulate) tma_reduce_add_3d(&p.tmOut, box, x, y, t.z);
-              else tma_store_3d(&p.tmOut, box, x, y, MODE == X_PART ? t.z : 0);
+            const int y = t.mb * T::kMmaM + static_cast<int>(rank) * BM;
+            if (n0 + c0 < p.N) {
+              if (p.accumulate) tma_reduce_add_3d(&p.tmOut, box, n0 + c0, y, t.z);
+              else tma_store_3d(&p.tmOut, box, n0 + c0, y, t.z);
             }
             bulk_commit_group();
+          }
+        }
+      } else {
+        // A thread writes its row's columns itself, 32 bytes at a time: whole sectors,
+        // and nothing that the warps of a group have to wait for.  (Through boxes in shared
+        // memory, with a fence and two barriers for every 64 columns, a tile's epilogue took
+        // about 12000 clocks, longer than 17 k-blocks' products.)
+        for (int c0 = grp * 32; c0 < BN; c0 += 64) {
+          float v[32];
+          tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
+          tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
+          tmem_wait_ld();
+          if (c0 + 64 >= BN) release();
+          if constexpr (MODE == X_DLOGIT) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], p.c2, -lse2)) * coef.x;
+            const int at = target - c0;
+            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (at == e) v[e] -= coef.y;
+            }
+            // rows and columns that do not exist read as 0 in the products to come
+            if (!live || c0 + 32 > limit) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!live || c0 + e >= limit) v[e] = 0.f;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = rows > 0 ? v[e] * out_scale : 0.f;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w[e] = pack16(p.bf16, v[2 * e], v[2 * e + 1]);
+          // dl has zero rows up to the tile's last, as far as the buffer goes
+          if (m >= (MODE == X_DLOGIT ? p.M : M)) continue;
+          uint16_t *o = p.out + (MODE == X_OUT ? int64_t(p.b_row0) + m : int64_t(m)) * p.ld_out + n0 + c0;
+          if (MODE == X_DLOGIT || c0 + 32 <= limit) {
+            st_global32(o, w, MODE == X_DLOGIT || p.out32);
+            st_global32(o + 16, w + 8, MODE == X_DLOGIT || p.out32);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e < limit) o[e] = static_cast<uint16_t>(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
           }
         }
       }
       abuf ^= 1;
       if (abuf == 0) aphase ^= 1u;
     }
-    if (storer) bulk_wait_group<0>();
+    if (MODE == X_PART && storer) bulk_wait_group<0>();
     __syncwarp();
   }
 
