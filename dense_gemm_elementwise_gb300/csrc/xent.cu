@@ -321,6 +321,7 @@ struct ConvertParams {
   const XentScalars *sc;
   int64_t pitch;
   int32_t T, N, bn;          // N columns exist of the piece
+  int32_t band, band_tiles;  // as in the product that kept them
   float c2, c;               // logit_scale log2(e), logit_scale
 };
 
@@ -333,10 +334,13 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
   const int rows = p.sc->rows;
   const int end = min(p.T, (rows + BK - 1) / BK * BK);  // zeros up to the next k-block
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c0 = blockIdx.x * 256 + lane * 8;
-  const int slot = 2 * (c0 / p.bn) + ((c0 / 64) & 1);
+  // last columns first: the product wrote them last, and what is left in L2 for
+  // the next product is what that reads first
+  const int c0 = (gridDim.y - 1 - blockIdx.y) * 256 + lane * 8;
+  const int of_band = p.band ? c0 % p.band : c0;
+  const int slot = 2 * ((p.band ? c0 / p.band * p.band_tiles : 0) + of_band / p.bn) + ((of_band / 64) & 1);
   const float ds = p.sc->dl_scale;
-  for (int first = blockIdx.y * kConvertRows; first < end; first += gridDim.y * kConvertRows) {
+  for (int first = blockIdx.x * kConvertRows; first < end; first += gridDim.x * kConvertRows) {
     uint4 w[4];
     float shift[4], lse2[4];
     float2 coef[4];
@@ -400,40 +404,53 @@ struct SpreadParams {
 };
 
 // Four columns of a row of dH per thread: its slices added in order; ignored rows are 0.
+// kLanes threads share a quad's slices (every kLanes-th each, then the lanes in order),
+// since a long chain of loads is what few rows with many slices would wait for.
+template <int kLanes>
 __global__ void __launch_bounds__(256) xent_spread_kernel(const __grid_constant__ SpreadParams p) {
+  __shared__ float4 sums[kLanes > 1 ? 256 : 1];
   griddep_wait();
   griddep_launch_dependents();
   const float scale = p.sc->out_scale;
   const int kbs = p.sc->kb_split, slices = (p.kb + kbs - 1) / kbs;
-  const int quads = (p.D + 3) / 4;
-  const int64_t units = int64_t(p.T) * quads;
-  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < units; u += int64_t(gridDim.x) * 256) {
-    const int64_t i = u / quads;
-    const int c = static_cast<int>(u - i * quads) * 4;
+  constexpr int kQuads = 256 / kLanes;
+  const int lane = threadIdx.x / kQuads;
+  const int c = (blockIdx.x * kQuads + threadIdx.x % kQuads) * 4;
+  for (int64_t i = blockIdx.y; i < p.T; i += gridDim.y) {
     const int r = p.place[i];
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r >= 0) {
+    if (r >= 0 && c < p.D) {
       const float *a = p.part + r * p.Dp + c;
 #pragma unroll 8
-      for (int s = 0; s < slices; ++s) {
+      for (int s = lane; s < slices; s += kLanes) {
         const float4 f = *reinterpret_cast<const float4 *>(a + s * (p.T * p.Dp));
         v.x += f.x;
         v.y += f.y;
         v.z += f.z;
         v.w += f.w;
       }
-      v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
     }
-    union { uint16_t e[4]; uint2 w; } o;
-    const float f[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (kLanes > 1) {
+      __syncthreads();  // the last row's sums have been read
+      sums[threadIdx.x] = v;
+      __syncthreads();
+      if (lane > 0) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o.e[e] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f[e])) : __half_as_ushort(__float2half_rn(f[e]));
+      for (int l = 1; l < kLanes; ++l) {
+        const float4 f = sums[threadIdx.x + l * kQuads];
+        v = make_float4(v.x + f.x, v.y + f.y, v.z + f.z, v.w + f.w);
+      }
+    }
+    if (c >= p.D) continue;
+    if (r >= 0) v = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    const bool bf16 = p.bf16 != 0;
+    const uint2 o = make_uint2(pack16(bf16, v.x, v.y), pack16(bf16, v.z, v.w));
     uint16_t *dst = p.dH + i * p.lddh + c;
     if (c + 4 <= p.D) {
-      *reinterpret_cast<uint2 *>(dst) = o.w;
+      *reinterpret_cast<uint2 *>(dst) = o;
     } else {
-      for (int e = 0; e < p.D - c; ++e) dst[e] = o.e[e];
+      const uint32_t w[2] = {o.x, o.y};
+      for (int e = 0; e < p.D - c; ++e) dst[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
     }
   }
 }
@@ -485,11 +502,16 @@ struct gemm_epi_xent_plan {
   bool pack = true;     // a loss alone packs its rows too
   int row_lanes = 32, finish_grid = 1;
   int64_t ldc = 0, Dp = 0;
+  int64_t band = 0;     // columns of a CTA's band in the logits' product, 0: tiles
 };
 
 namespace {
 
-int slots_of(const gemm_epi_xent_plan *pl) { return static_cast<int>(2 * ceil_div(pl->V, pl->stats.bn)); }
+// column ranges that leave a maximum and a sum
+int slots_of(const gemm_epi_xent_plan *pl) {
+  if (pl->band) return static_cast<int>(2 * ceil_div(pl->V, pl->band) * ceil_div(pl->band, pl->stats.bn));
+  return static_cast<int>(2 * ceil_div(pl->V, pl->stats.bn));
+}
 
 Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {
   Workspace w{};
@@ -575,6 +597,10 @@ int configure(gemm_epi_xent_plan *pl) {
       pl->pairs = std::min(pl->pairs, clusters);
     cudaGetLastError();
   }
+  // One tile of rows: its time is that of reading W, and every CTA is given as many of W's
+  // rows as the next (to 32) where whole tiles would leave CTAs idle at the end (32000 rows:
+  // 224 to a CTA instead of one or two tiles of 128).
+  pl->band = cg == 1 && pl->T <= 128 ? 32 * ceil_div(ceil_div(pl->V, 32), units_of(pl, pl->stats)) : 0;
   // Rows are packed for a loss alone only where that can save a tile of them.
   pl->pack = pl->T > 128 * cg;
   // pieces of the vocabulary: as wide as the buffer allows, equal, whole tiles
@@ -589,14 +615,20 @@ int configure(gemm_epi_xent_plan *pl) {
   const int64_t fit = (int64_t(64) << 20) / (4 * pl->T * pl->Dp);
   const int64_t want = 2 * int64_t(units_of(pl, pl->part)) / tiles;
   pl->slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({std::max(fit, want), kb, 64})));
-  // finish: few rows are shared by more threads each
-  pl->row_lanes = 32;
-  while (pl->row_lanes > 1 && pl->row_lanes / 2 >= pl->T) pl->row_lanes /= 2;
+  // finish: a block of 1024 threads per row while that is at most two blocks to an SM, then up
+  // to 32 rows to a block (37 rows of 858 ranges: 37 blocks 6 us, 2 blocks 11 us)
+  pl->row_lanes = 1;
+  while (pl->row_lanes < 32 && ceil_div(pl->T, pl->row_lanes) > 2 * int64_t(pl->sms)) pl->row_lanes *= 2;
   const int64_t fg = ceil_div(pl->T, pl->row_lanes);
   pl->finish_grid = static_cast<int>(fg);
   for (const Product *pr : {&pl->stats, &pl->part})
     if (tiles_of(*pr, pl->T, std::max(pl->V, pl->D)) * pl->slices > (int64_t(1) << 30)) return GE_ERR_SHAPE;
   return GE_OK;
+}
+
+// rows of a K-major A tile: all 128, or those of a batch that fills no tile
+int64_t a_rows_of(const gemm_epi_xent_plan *pl, const Product &pr) {
+  return pr.cg == 1 ? std::min<int64_t>(128, round_up(pl->T, 8)) : 128;
 }
 
 XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalars *sc, int64_t M, int64_t N,
@@ -615,6 +647,7 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalar
   const int64_t m_blk = ceil_div(M, 128 * pr.cg);
   p.raster_group = m_blk <= 16 ? 16 : 12;
   p.stages = pr.stages;
+  p.a_rows = static_cast<int32_t>(a_rows_of(pl, pr));
   p.bf16 = pl->d.ab == GE_BF16;
   p.off_B = pr.off_B;
   p.off_out = pr.off_out;
@@ -626,7 +659,7 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalar
 }
 
 cudaError_t launch_product(const gemm_epi_xent_plan *pl, const Product &pr, XentParams &p, cudaStream_t s) {
-  const int64_t tiles = tiles_of(pr, p.M, p.N) * (pr.mode == X_PART ? pl->slices : 1);
+  const int64_t tiles = p.band ? ceil_div(p.N, p.band) : tiles_of(pr, p.M, p.N) * (pr.mode == X_PART ? pl->slices : 1);
   const int units = static_cast<int>(std::min<int64_t>(units_of(pl, pr), tiles));
   return launch(pr.fn, dim3(static_cast<unsigned>(units * pr.cg)), kXentThreads, pl->smem, pr.cg, &p, s);
 }
@@ -701,10 +734,12 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   const Product &first = kept ? pl->keep : pl->stats;
   XentParams sl = params_of(pl, first, sc, T, V, D);
   if (!encode_rows(&sl.tmA, ab, pack ? Hc : H, D, T, 1, pack ? pl->ldc : pl->d.ldh,
-                   (pack ? pl->ldc : pl->d.ldh) * T, BK, 128) ||
-      !encode_rows(&sl.tmH, ab, H, D, T, 1, pl->d.ldh, pl->d.ldh * T, BK, 128) ||
-      !encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128))
+                   (pack ? pl->ldc : pl->d.ldh) * T, BK, sl.a_rows) ||
+      !encode_rows(&sl.tmH, ab, H, D, T, 1, pl->d.ldh, pl->d.ldh * T, BK, sl.a_rows) ||
+      !encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, pl->band ? 32 : 128))
     return GE_ERR_CUDA;
+  sl.band = static_cast<int32_t>(pl->band);
+  sl.band_tiles = static_cast<int32_t>(pl->band ? ceil_div(pl->band, first.bn) : 0);
   if (!pack) sl.rows = nullptr;
   sl.target = pack ? static_cast<const void *>(gathered) : target;
   sl.target_i64 = !pack && !i32;
@@ -761,25 +796,27 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       cp.T = static_cast<int32_t>(T);
       cp.N = static_cast<int32_t>(n);
       cp.bn = first.bn;
+      cp.band = sl.band;
+      cp.band_tiles = sl.band_tiles;
       cp.c2 = sl.c2;
       cp.c = sl.c;
       const unsigned cols = static_cast<unsigned>(ceil_div(n, 256));
       const unsigned rows = static_cast<unsigned>(
           std::max<int64_t>(1, std::min<int64_t>(ceil_div(T, kConvertRows), ceil_div(16 * pl->sms, cols))));
-      if (!go(launch(reinterpret_cast<const void *>(xent_convert_kernel), dim3(cols, rows), 256, 0, 1, &cp, s)))
+      if (!go(launch(reinterpret_cast<const void *>(xent_convert_kernel), dim3(rows, cols), 256, 0, 1, &cp, s)))
         return GE_ERR_CUDA;
     } else {
       XentParams q = params_of(pl, pl->dlogit, sc, T, n, D);
       q.tmA = sl.tmA;
       q.tmH = sl.tmH;
-      q.tmB = sl.tmB;
       q.b_row0 = static_cast<int32_t>(v0);
       q.target = gathered;
       q.lse2 = lse2;
       q.coef = coef;
       q.out = static_cast<uint16_t *>(dl);
       q.ld_out = pl->piece;
-      if (!go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
+      if (!encode_rows(&q.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128) ||
+          !go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
     }
     if (dW) {
       XentParams o = params_of(pl, pl->out, sc, n, D, T);
@@ -797,7 +834,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       XentParams o = params_of(pl, pl->part, sc, T, D, n);
       o.b_row0 = static_cast<int32_t>(v0);
       o.accumulate = v0 > 0;
-      if (!encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, BK, 128) ||
+      if (!encode_rows(&o.tmA, ab, dl, piece, T, 1, piece, piece * T, BK, o.a_rows) ||
           !encode_rows(&o.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, 64, BK) ||
           !encode_rows(&o.tmOut, GE_F32, part, pl->Dp, T, pl->slices, pl->Dp, pl->Dp * T, 32, 128) ||
           !go(launch_product(pl, pl->part, o, s)))
@@ -808,8 +845,13 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
     SpreadParams dp{part, static_cast<uint16_t *>(dH), place, sc, pl->d.lddh, pl->Dp, static_cast<int32_t>(T),
                     static_cast<int32_t>(D), static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK)),
                     ab == GE_BF16};
-    const int grid = static_cast<int>(std::min<int64_t>(ceil_div(T * ceil_div(D, 4), 256), pl->sms * 8));
-    if (!go(launch(reinterpret_cast<const void *>(xent_spread_kernel), grid, 256, 0, 1, &dp, s))) return GE_ERR_CUDA;
+    const bool shared = pl->slices > 8;
+    const int64_t across = ceil_div(D, shared ? 128 : 1024);
+    const dim3 grid(static_cast<unsigned>(across),
+                    static_cast<unsigned>(std::min<int64_t>(T, std::max<int64_t>(1, pl->sms * 16 / across))));
+    const void *fn = shared ? reinterpret_cast<const void *>(xent_spread_kernel<8>)
+                            : reinterpret_cast<const void *>(xent_spread_kernel<1>);
+    if (!go(launch(fn, grid, 256, 0, 1, &dp, s))) return GE_ERR_CUDA;
   }
   return GE_OK;
 }

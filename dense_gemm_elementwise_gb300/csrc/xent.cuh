@@ -44,6 +44,9 @@ struct XentParams {
   int32_t M, N, K;         // sizes at most; the rows replace M (K for X_OUT)
   int32_t num_n_blk, raster_group;
   int32_t stages;
+  int32_t a_rows;          // rows of an A tile that are loaded (K-major A, one CTA)
+  // X_STATS, X_KEEP of a single tile of rows: columns of a CTA's band (0: tiles dealt out) and its tiles
+  int32_t band, band_tiles;
   int32_t bf16;
   int32_t b_row0;          // first vocabulary row of this piece
   int32_t accumulate;      // X_PART: add to the slices

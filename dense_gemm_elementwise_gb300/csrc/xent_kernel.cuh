@@ -3,10 +3,9 @@
 // One persistent, warp-specialised kernel in five modes (XentMode):
 //   X_STATS   H @ W^T, K-major operands: logits that never leave the SM.  An
 //             epilogue thread owns one row of the tile and half of its
-//             columns: it takes their maximum, then the sum of
-//             2^(x - maximum), reading the accumulator from TMEM twice (that
-//             costs less than rescaling a running sum) and leaves the
-//             pair for the kernel that joins the tiles.
+//             columns, which it holds in registers: it takes their maximum, then
+//             the sum of 2^(x - maximum), and leaves the pair for the kernel
+//             that joins the tiles.
 //   X_KEEP    the same, and each logit's distance below that maximum in 16 bits,
 //             from which dl is made without the product of X_DLOGIT.
 //   X_DLOGIT  the same product: 2^(x - lse) * coef, less the target's 1, rounded
@@ -90,6 +89,7 @@ constexpr uint32_t kXFull = 0, kXEmpty = 64, kXTmemFull = 128, kXTmemEmpty = 144
 
 struct XentTile {
   int z, mb, nb, kb0, kb1;
+  int n0, width;  // first column and columns
 };
 
 template <int CG, int BN, int MODE>
@@ -99,6 +99,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   constexpr bool kStats = MODE == X_STATS || MODE == X_KEEP;
   constexpr bool kBk = kStats || MODE == X_DLOGIT;           // B is K-major
   constexpr int kEpi0 = 2;                                   // first epilogue warp
+  // k-blocks that the tensor unit sums before the epilogue adds them up in
+  // registers.  Its sums are cut off, not rounded: left to itself over all of K it gives an
+  // lse that is low by 2.0e-6 of its value at D = 4096 and 4.0e-6 at 8192, in runs of K = 1024 by
+  // 4.8e-7 whatever D is (256: 1.2e-7, but a run's 2000 clocks are then less than its
+  // sums take to be read, and 4096 x 65536 x 2048 takes 771 us instead of 622).
+  constexpr int kRun = kStats ? 16 : 1 << 30;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -148,13 +154,27 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   const int per_slice = num_m_blk * p.num_n_blk;
   const int kb_split = MODE == X_PART ? __ldcg(&p.sc->kb_split) : num_kb;
   const int num_tiles = MODE == X_PART ? per_slice * ((num_kb + kb_split - 1) / kb_split) : per_slice;
-  const int my_tiles = unit < num_tiles ? (num_tiles - 1 - unit) / n_units + 1 : 0;
+  // In bands: unit u takes columns [u band, (u + 1) band) in tiles of up to BN.
+  const bool bands = kStats && CG == 1 && p.band > 0;
+  const int band_cols = bands ? max(0, min(p.band, p.N - unit * p.band)) : 0;
+  const int my_tiles = bands ? (band_cols + BN - 1) / BN * num_m_blk
+                             : unit < num_tiles ? (num_tiles - 1 - unit) / n_units + 1 : 0;
   auto tile = [&](int i) {
     XentTile t;
+    if (bands) {
+      t.z = t.mb = t.kb0 = 0;
+      t.kb1 = num_kb;
+      t.nb = unit * p.band_tiles + i;
+      t.n0 = unit * p.band + i * BN;
+      t.width = min(BN, p.band - i * BN);
+      return t;
+    }
     const int at = unit + i * n_units;
     tile_coords(num_m_blk, p.num_n_blk, p.raster_group, at, t.z, t.mb, t.nb);
     t.kb0 = MODE == X_PART ? t.z * kb_split : 0;
     t.kb1 = MODE == X_PART ? min(num_kb, t.kb0 + kb_split) : num_kb;
+    t.n0 = t.nb * BN;
+    t.width = BN;
     return t;
   };
 
@@ -170,7 +190,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       for (int i = 0; ok && i < my_tiles; ++i) {
         const XentTile t = tile(i);
         const int m0 = t.mb * T::kMmaM + static_cast<int>(rank) * BM;
-        const int n0 = t.nb * BN + static_cast<int>(rank) * T::kBnLocal;
+        const int n0 = t.n0 + static_cast<int>(rank) * T::kBnLocal;
         const int nk = t.kb1 - t.kb0;
         for (int kb = 0; kb < nk; ++kb) {
           if (!wt.wait(bar + kXEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
@@ -181,13 +201,13 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           const int kx = (t.kb0 + ((i & 1) ? nk - 1 - kb : kb)) * BK;
           const uint32_t full = bar + kXFull + 8 * stage;
           const uint32_t sa = sb + stage * T::kABytes, sbb = sb + p.off_B + stage * T::kBBytes;
-          constexpr uint32_t kTx = CG * (T::kABytes + T::kBBytes);
           uint32_t fb = full;
           if constexpr (CG == 2) {
             fb = mapa_shared(full, 0);
-            if (rank == 0) mbar_arrive_expect_tx(full, kTx);
+            if (rank == 0) mbar_arrive_expect_tx(full, CG * (T::kABytes + T::kBBytes));
           } else {
-            mbar_arrive_expect_tx(full, kTx);
+            // few rows: only theirs are loaded; what the others' accumulators then hold is not read
+            mbar_arrive_expect_tx(full, (kAmn ? T::kABytes : p.a_rows * 128) + (bands ? t.width * 128 : T::kBBytes));
           }
           auto load = [&](uint32_t dst, const CUtensorMap *m, int x, int y) {
             if constexpr (CG == 2) tma_load_3d_pair(dst, m, fb, x, y, 0);
@@ -199,7 +219,9 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           } else {
             load(sa, mA, kx, m0);
           }
-          if constexpr (kBk) {
+          if (bands) {
+            for (int j = 0; j < t.width; j += 32) load(sbb + j * 128, mB, kx, n0 + j);
+          } else if constexpr (kBk) {
             load(sbb, mB, kx, p.b_row0 + n0);
           } else {
             // dH: the k rows of B are the piece's vocabulary rows
@@ -235,7 +257,6 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer --
     if (lane == 0 && rank == 0) {
-      const uint32_t id = make_idesc_f16(p.bf16 != 0, T::kMmaM, BN, kAmn, !kBk);
       constexpr uint32_t kAk16 = (kAmn ? 2048u : 32u) >> 4, kBk16 = (kBk ? 32u : 2048u) >> 4;
       const uint64_t a_desc0 = smem_desc_sw128(sb, kAmn ? 8192u : 16u, 1024u);
       const uint64_t b_desc0 = smem_desc_sw128(sb + p.off_B, kBk ? 16u : 8192u, 1024u);
@@ -244,33 +265,37 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       bool ok = true;
       for (int i = 0; ok && i < my_tiles; ++i) {
         const XentTile t = tile(i);
-        if (!wt.wait<CG == 2>(bar + kXTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * BN);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wt.wait(bar + kXFull + 8 * stage, phase, SITE_MMA_FULL)) {
+        const uint32_t id = make_idesc_f16(p.bf16 != 0, T::kMmaM, t.width, kAmn, !kBk);
+        for (int first = t.kb0; ok && first < t.kb1; first += kRun) {
+          if (!wt.wait<CG == 2>(bar + kXTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (T::kABytes >> 4));
-          const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage * (T::kBBytes >> 4));
+          const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * BN);
+          const int end = min(t.kb1, first + kRun);
+          for (int kb = first; kb < end; ++kb) {
+            if (!wt.wait(bar + kXFull + 8 * stage, phase, SITE_MMA_FULL)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (T::kABytes >> 4));
+            const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage * (T::kBBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < BK / UMMA_K; ++k)
-            umma_f16<CG>(d, ad + kAk16 * k, bd + kBk16 * k, id, (kb > t.kb0 || k != 0) ? 1u : 0u);
-          umma_commit<CG>(bar + kXEmpty + 8 * stage);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
+            for (int k = 0; k < BK / UMMA_K; ++k)
+              umma_f16<CG>(d, ad + kAk16 * k, bd + kBk16 * k, id, (kb > first || k != 0) ? 1u : 0u);
+            umma_commit<CG>(bar + kXEmpty + 8 * stage);
+            if (++stage == p.stages) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
+          if (!ok) break;
+          umma_commit<CG>(bar + kXTmemFull + 8 * abuf);
+          abuf ^= 1;
+          if (abuf == 0) aphase ^= 1u;
         }
-        if (!ok) break;
-        umma_commit<CG>(bar + kXTmemFull + 8 * abuf);
-        abuf ^= 1;
-        if (abuf == 0) aphase ^= 1u;
       }
       if (ok) {
         for (int i = 0; i < 2; ++i) {
@@ -298,7 +323,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
     for (int i = 0; i < my_tiles; ++i) {
       const XentTile t = tile(i);
       const int m = t.mb * T::kMmaM + static_cast<int>(rank) * BM + row;
-      const int n0 = t.nb * BN;
+      const int n0 = t.n0;
       const bool live = m < M;
       // what the row needs, on its way while the tile's product finishes
       int target = -1;
@@ -308,7 +333,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         const int64_t at = p.target_i64 ? static_cast<const int64_t *>(p.target)[m] : static_cast<const int32_t *>(p.target)[m];
         // no column of this tile for a target that is elsewhere (or does not exist)
         const int64_t off = at - p.b_row0 - n0;
-        target = off >= 0 && off < BN ? static_cast<int>(off) : -1;
+        target = off >= 0 && off < t.width ? static_cast<int>(off) : -1;
       }
       if (MODE == X_DLOGIT && live) {
         const float ds = p.sc->dl_scale;
@@ -318,11 +343,15 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         coef.y *= ds;
       }
       if (MODE == X_OUT) out_scale = rows > 0 ? *p.out_scale : 0.f;
-      const bool got = wt.wait(bar + kXTmemFull + 8 * abuf, aphase, SITE_EPI_TMEM_FULL);
-      if (!group_agrees(bid, got)) break;
-      tc_fence_after();
-      const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN);
       const int limit = p.N - n0;  // columns of the tile that exist
+      // the accumulator is complete: no where the wait ran out
+      auto ready = [&]() {
+        const bool got = wt.wait(bar + kXTmemFull + 8 * abuf, aphase, SITE_EPI_TMEM_FULL);
+        if (!group_agrees(bid, got)) return false;
+        tc_fence_after();
+        return true;
+      };
+      // it has been read: the next one
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
@@ -331,73 +360,92 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           if constexpr (CG == 2) mbar_arrive_remote(mapa_shared(tb, 0));
           else mbar_arrive(tb);
         }
+        abuf ^= 1;
+        if (abuf == 0) aphase ^= 1u;
       };
 
       if constexpr (kStats) {
-        float v[32];
-        auto read = [&](int c0) {
-          tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
-          tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
-          tmem_wait_ld();
-          if (c0 + 32 > limit) {
+        // this group's columns, 64 of every 128, in registers
+        constexpr int kParts = BN / 64;  // of 32 columns: grp * 64 + 128 (j / 2) + 32 (j % 2)
+        float v[kParts][32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e >= limit) v[e] = p.c2 < 0.f ? INFINITY : -INFINITY;
-          }
-        };
-        // 64 columns at a time, in two halves; the groups in turn
-        float top = -INFINITY;
-        for (int c1 = grp * 64; c1 < BN; c1 += 128)
-#pragma unroll 1
-          for (int c0 = c1; c0 < c1 + 64; c0 += 32) {
-            read(c0);
+        for (int j = 0; j < kParts; ++j)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[e] * p.c2);
-            const int at = target - c0;
-            if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-              float x = 0.f;
+          for (int e = 0; e < 32; ++e) v[j][e] = 0.f;
+        bool ok = true;
+        for (int first = t.kb0; first < t.kb1; first += kRun) {
+          if (!(ok = ready())) break;
+          const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN + grp * 64);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x = at == e ? v[e] : x;
-              if (at >= 0 && at < 32 && target < limit) p.at_target[m] = x * p.c;
+          for (int j = 0; j < kParts; ++j) {
+            const int c0 = 128 * (j / 2) + 32 * (j % 2);
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              float x[16];
+              tmem_ld16(acc + c0 + h, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[j][h + e] += x[e];
             }
           }
+          release();
+        }
+        if (!ok) break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < kParts; ++j) {
+          const int c0 = grp * 64 + 128 * (j / 2) + 32 * (j % 2);
+          const int at = target - c0;
+          if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+            float x = 0.f;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x = at == e ? v[j][e] : x;
+            if (at >= 0 && at < 32 && target < limit) p.at_target[m] = x * p.c;
+          }
+          const int end = min(limit, t.width) - c0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            v[j][e] *= p.c2;
+            if (end < 32 && e >= end) v[j][e] = -INFINITY;
+            top = fmaxf(top, v[j][e]);
+          }
+        }
         const float off = top == -INFINITY ? 0.f : top;
         const bool keep = MODE == X_KEEP && n0 < p.keep_cols && live;
         float sum = 0.f;
-        for (int c1 = grp * 64; c1 < BN; c1 += 128) {
-#pragma unroll 1
-          for (int c0 = c1; c0 < c1 + 64; c0 += 32) {
-            read(c0);
-            if (c0 + 96 >= BN && c0 != c1) release();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = fmaf(v[e], p.c2, -off);
-            if (keep) {
-              // the distances, rounded to integers in the low bits of floats of 2^23 and more
-              constexpr float k0 = 8388608.f, kStepsPerOctave = 1 << kKeptBits;
-              uint32_t w[16];
+        for (int j = 0; j < kParts; ++j) {
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const float a = fmaxf(fminf(fmaf(v[2 * e], -kStepsPerOctave, k0), k0 + 65535.f), k0);
-                const float b = fmaxf(fminf(fmaf(v[2 * e + 1], -kStepsPerOctave, k0), k0 + 65535.f), k0);
-                w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
-              }
-              uint16_t *o = p.out + int64_t(m) * p.ld_out + n0 + c0;
-              st_global32(o, w, true);
-              st_global32(o + 16, w + 8, true);
+          for (int e = 0; e < 32; ++e) v[j][e] -= off;
+          const int c0 = grp * 64 + 128 * (j / 2) + 32 * (j % 2);
+          if (keep && c0 < t.width) {
+            // the distances, rounded to integers in the low bits of floats of 2^23 and more
+            constexpr float k0 = 8388608.f, kStepsPerOctave = 1 << kKeptBits;
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float a = fminf(fmaf(v[j][2 * e], -kStepsPerOctave, k0), k0 + 65535.f);
+              const float b = fminf(fmaf(v[j][2 * e + 1], -kStepsPerOctave, k0), k0 + 65535.f);
+              w[e] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
             }
-            float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              s0 += ex2(v[e]);
-              s1 += ex2(v[e + 1]);
-              s2 += ex2(v[e + 2]);
-              s3 += ex2(v[e + 3]);
-            }
-            sum += (s0 + s1) + (s2 + s3);
+            uint16_t *o = p.out + int64_t(m) * p.ld_out + n0 + c0;
+            st_global32(o, w, true);
+            st_global32(o + 16, w + 8, true);
           }
+          float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            s0 += ex2(v[j][e]);
+            s1 += ex2(v[j][e + 1]);
+            s2 += ex2(v[j][e + 2]);
+            s3 += ex2(v[j][e + 3]);
+          }
+          sum += (s0 + s1) + (s2 + s3);
         }
         if (live) p.stats[(2 * int64_t(t.nb) + grp) * p.M + m] = make_float2(top, sum);
       } else if constexpr (MODE == X_PART) {
+        if (!ready()) break;
+        const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN);
         // boxes of 128 rows of 32 columns, which the TMA engine stores or adds
         for (int c0 = grp * 32; c0 < BN; c0 += 64, ++step) {
           const uint32_t box = boxes + (step & 1) * kXentBox;
@@ -428,6 +476,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         // and nothing that the warps of a group have to wait for.  (Through boxes in shared
         // memory, with a fence and two barriers for every 64 columns, a tile's epilogue took
         // about 12000 clocks, longer than 17 k-blocks' products.)
+        if (!ready()) break;
+        const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN);
         for (int c0 = grp * 32; c0 < BN; c0 += 64) {
           float v[32];
           tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
@@ -469,9 +519,11 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           }
         }
       }
-      abuf ^= 1;
-      if (abuf == 0) aphase ^= 1u;
     }
+    // ranges of a band that have no columns
+    if (bands && row < M)
+      for (int i = my_tiles; i < p.band_tiles; ++i)
+        p.stats[(2 * (int64_t(unit) * p.band_tiles + i) + grp) * p.M + row] = make_float2(-INFINITY, 0.f);
     if (MODE == X_PART && storer) bulk_wait_group<0>();
     __syncwarp();
   }
