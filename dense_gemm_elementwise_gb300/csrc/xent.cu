@@ -372,8 +372,7 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
       for (int e = 0; e < 8; ++e) {
         // the code in the low bits of a float of 2^23
         const float code = __uint_as_float(__byte_perm(u[e / 2], 0x4b000000u, e & 1 ? 0x7432 : 0x7410)) - 8388608.f;
-        const float q = code == 65535.f ? 0.f : ex2(fmaf(code, -1.f / (1 << kKeptBits), shift[i]));
-        d[e] = q * f;
+        d[e] = ex2(fmaf(code, -1.f / (1 << kKeptBits), shift[i])) * f;
       }
       if (target[i] >= 0 && target[i] < 8) {
         // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   // lse that is low by 2.0e-6 of its value at D = 4096 and 4.0e-6 at 8192, in runs of K = 1024 by
   // 4.8e-7 whatever D is (256: 1.2e-7, but a run's 2000 clocks are then less than its
   // sums take to be read, and 4096 x 65536 x 2048 takes 771 us instead of 622).
-  constexpr int kRun = kStats ? 16 : 1 << 30;
+  constexpr int kMostRun = 16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -154,6 +154,9 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   const int per_slice = num_m_blk * p.num_n_blk;
   const int kb_split = MODE == X_PART ? __ldcg(&p.sc->kb_split) : num_kb;
   const int num_tiles = MODE == X_PART ? per_slice * ((num_kb + kb_split - 1) / kb_split) : per_slice;
+  // (Runs of equal length: a short last one would be waited for.)
+  const int runs = kStats ? (num_kb + kMostRun - 1) / kMostRun : 1;
+  const int run = kStats ? (num_kb + runs - 1) / runs : num_kb;
   // In bands: unit u takes columns [u band, (u + 1) band) in tiles of up to BN.
   const bool bands = kStats && CG == 1 && p.band > 0;
   const int band_cols = bands ? max(0, min(p.band, p.N - unit * p.band)) : 0;
@@ -266,14 +269,14 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       for (int i = 0; ok && i < my_tiles; ++i) {
         const XentTile t = tile(i);
         const uint32_t id = make_idesc_f16(p.bf16 != 0, T::kMmaM, t.width, kAmn, !kBk);
-        for (int first = t.kb0; ok && first < t.kb1; first += kRun) {
+        for (int first = t.kb0; ok && first < t.kb1; first += run) {
           if (!wt.wait<CG == 2>(bar + kXTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * BN);
-          const int end = min(t.kb1, first + kRun);
+          const int end = min(t.kb1, first + run);
           for (int kb = first; kb < end; ++kb) {
             if (!wt.wait(bar + kXFull + 8 * stage, phase, SITE_MMA_FULL)) {
               ok = false;
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[j][e] = 0.f;
         bool ok = true;
-        for (int first = t.kb0; first < t.kb1; first += kRun) {
+        for (int first = t.kb0; first < t.kb1; first += run) {
           if (!(ok = ready())) break;
           const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN + grp * 64);
 #pragma unroll
