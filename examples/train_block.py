@@ -79,7 +79,7 @@ class Model:
         B.gemm_epi_xent_plan_destroy(self.head)
 
 
-def train(steps, tokens, width, vocabulary, rate=20.0, seed=0):
+def train(steps, tokens, width, vocabulary, rate=1.0, seed=0):
     """Losses of `steps` steps on one batch: token i is to predict a fixed permutation of itself; a tenth are ignored."""
     m = Model(tokens, width, vocabulary, seed=seed)
     dev = m.embed.device

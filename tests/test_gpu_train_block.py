@@ -36,7 +36,8 @@ def test_gradients_of_the_whole_step():
     logits = (unit(y) * p["w_pre"]) @ p["W"].T
     want = torch.nn.functional.cross_entropy(logits, target, ignore_index=-100)
     want.backward()
-    assert abs(float(total) - float(want)) <= 2.0 ** -8 * float(want)
+    want = want.item()
+    assert abs(float(total) - want) <= 2.0 ** -8 * want
     for k, v in p.items():
         off = float((m.grad[k].double() - v.grad).norm() / v.grad.norm())
         assert off <= 6 * 2.0 ** -8, (k, off)
