@@ -41,6 +41,36 @@ __device__ __forceinline__ int64_t target_of(const void *t, int i32, int64_t i) 
   return i32 ? static_cast<const int32_t *>(t)[i] : static_cast<const int64_t *>(t)[i];
 }
 
+// dH's sum over the vocabulary: tiles of m x n, k-blocks, CTAs (pairs), slices at most
+struct SplitParams {
+  int32_t m, n, n_blk, kb, units, slices;
+};
+
+// dH has few tiles for its long sum.  Whole waves of them are left whole; the k-blocks of those
+// left over are split so that the slices fill one to four waves of CTAs in the
+// least time (in k-blocks of a tile, 0.27 us each: the waves' k-blocks and about six for
+// set-up and stores, and the slices' way to memory and back).
+__device__ void choose_split(const SplitParams &p, int rows, XentScalars *sc) {
+  const int tiles = max(1, (rows + p.m - 1) / p.m) * p.n_blk;
+  const int full = tiles / p.units * p.units, rest = tiles - full;
+  float best = 0.f;
+  int best_kbs = p.kb;
+  for (int w = 0; w <= 4 && rest > 0; ++w) {
+    const int s = max(1, w == 0 ? 1 : min(min(p.units * w / rest, p.slices), p.kb));
+    const int kbs = (p.kb + s - 1) / s, used = (p.kb + kbs - 1) / kbs;
+    const int waves = (rest * used + p.units - 1) / p.units;
+    const float cost = float(waves) * float(kbs + 6) +
+                       float(used) * float(rest) * float(p.m * p.n) * (8.f / (6.5e6f * 0.27f));
+    if (w == 0 || cost < best * 0.9f) {
+      best = cost;
+      best_kbs = kbs;
+    }
+  }
+  sc->rows = rows;
+  sc->full = full;
+  sc->kb_split = best_kbs;
+}
+
 struct PackParams {
   const void *target;
   const float *weight;
@@ -52,30 +82,8 @@ struct PackParams {
   float *gweight;
   int64_t V, ldh, ldc;
   int32_t T, D, i32, rows_per_cta;
-  // dH's sum over the vocabulary: tiles of `part_m` x `part_n`, k-blocks, CTAs (pairs), slices at most
-  int32_t part_m, part_n_blk, part_kb, part_units, part_slices;
+  SplitParams split;
 };
-
-// How many slices dH's k-blocks are split into: the candidates fill one to four
-// waves of CTAs; the least time wins (in k-blocks of a tile, 0.27 us each: the waves'
-// k-blocks and about six for set-up and stores, and each slice's way to memory and back).
-__device__ int split_of(const PackParams &p, int rows) {
-  const int tiles = max(1, (rows + p.part_m - 1) / p.part_m * p.part_n_blk);
-  float best = 0.f;
-  int best_split = p.part_kb;
-  for (int w = 0; w <= 4; ++w) {
-    const int s = w == 0 ? 1 : min(min(p.part_units * w / tiles, p.part_slices), p.part_kb);
-    if (s < 1) continue;
-    const int kbs = (p.part_kb + s - 1) / s, used = (p.part_kb + kbs - 1) / kbs;
-    const int waves = (tiles * used + p.part_units - 1) / p.part_units;
-    const float cost = float(waves) * float(kbs + 6) + float(used) * float(rows) * float(p.D) * (8.f / (6.5e6f * 0.27f));
-    if (w == 0 || cost < best * 0.97f) {
-      best = cost;
-      best_split = kbs;
-    }
-  }
-  return best_split;
-}
 
 // Every CTA packs a run of rows.  It counts the rows that take part before its
 // own from the targets themselves (they are few bytes and in L2 after the
@@ -109,10 +117,7 @@ __global__ void __launch_bounds__(kPackThreads) xent_pack_kernel(const __grid_co
     before += counts[0][w];
     all += counts[1][w];
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    p.sc->rows = all;
-    p.sc->kb_split = split_of(p, all);
-  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) choose_split(p.split, all, p.sc);
   auto copy = [&](const uint16_t *src, int64_t r) {  // a warp copies one row, or zeros
     uint16_t *dst = p.Hc + r * p.ldc;
     const int whole = p.D / 8 * 8;
@@ -170,8 +175,15 @@ struct FinishParams {
   float2 *coef;
   float4 *block_sums;        // per block: losses, weights, the largest factor of dl
   XentScalars *sc;
+  // rows that were not packed and whose gradients follow: a block per row, which leaves what
+  // packing would (the row itself or zeros, its target or -1, its place)
+  const uint16_t *H;
+  uint16_t *Hc;
+  int32_t *gathered, *place;
+  int64_t ldh, ldc;
+  SplitParams split;
   int64_t V;
-  int32_t T, i32, slots, row_lanes;  // row_lanes rows per block of 1024 threads
+  int32_t T, D, i32, slots, row_lanes;  // row_lanes rows per block of 1024 threads
   int32_t mean;
   float z, grad_scale, c;
 };
@@ -268,6 +280,27 @@ __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant
       } else {
         if (p.loss) p.loss[i] = 0.f;
         if (p.lse) p.lse[i] = 0.f;
+        if (p.coef) {
+          p.lse2[row] = 0.f;
+          p.coef[row] = make_float2(0.f, 0.f);
+        }
+      }
+      if (p.Hc) {
+        p.gathered[row] = take ? static_cast<int32_t>(target_of(p.target, p.i32, i)) : -1;
+        p.place[row] = take ? row : -1;
+      }
+    }
+  }
+  if (p.Hc) {
+    const int64_t t = target_of(p.target, p.i32, blockIdx.x);
+    const bool take = t >= 0 && t < p.V;
+    const uint16_t *src = p.H + blockIdx.x * p.ldh;
+    uint16_t *dst = p.Hc + blockIdx.x * p.ldc;
+    for (int c = threadIdx.x * 8; c < p.D; c += 8192) {
+      if (c + 8 <= p.D) {
+        *reinterpret_cast<uint4 *>(dst + c) = take ? *reinterpret_cast<const uint4 *>(src + c) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        for (int e = c; e < p.D; ++e) dst[e] = take ? src[e] : uint16_t(0);
       }
     }
   }
@@ -300,6 +333,7 @@ __global__ void __launch_bounds__(1024) xent_finish_kernel(const __grid_constant
   if (lane == 0) {
     const float norm = p.mean ? sum.y : 1.f;
     if (p.total) *p.total = norm != 0.f ? sum.x / norm : 0.f;
+    if (p.Hc) choose_split(p.split, p.T, p.sc);
     if (p.coef) {
       // dl is at most `big`: brought just below 2^14, clear of fp16's largest value
       // (65504) and of its subnormals for every p above 2^-28
@@ -358,13 +392,15 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
         lse2[i] = p.lse2[r];
         shift[i] = (top == -INFINITY ? 0.f : top) - lse2[i];
         coef[i] = p.coef[r];
-        target[i] = p.gathered[r] - c0;
+        target[i] = p.gathered[r];
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = first + warp + 8 * i;
       if (r >= end) continue;
+      const bool live = target[i] >= 0;
+      target[i] -= c0;
       const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       const float f = coef[i].x * ds;
       float d[8];
@@ -374,7 +410,7 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
         const float code = __uint_as_float(__byte_perm(u[e / 2], 0x4b000000u, e & 1 ? 0x7432 : 0x7410)) - 8388608.f;
         d[e] = ex2(fmaf(code, -1.f / (1 << kKeptBits), shift[i])) * f;
       }
-      if (target[i] >= 0 && target[i] < 8) {
+      if (live && target[i] >= 0 && target[i] < 8) {
         // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p
         const float at = p.at_target[r] * (p.c2 / p.c);
         const float v = ex2(at - lse2[i]) * f - coef[i].y * ds;
@@ -382,10 +418,10 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
         for (int e = 0; e < 8; ++e)
           if (e == target[i]) d[e] = v;
       }
-      if (r >= rows || c0 + 8 > p.N) {
+      if (!live || c0 + 8 > p.N) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (r >= rows || c0 + e >= p.N) d[e] = 0.f;
+          if (!live || c0 + e >= p.N) d[e] = 0.f;
       }
       *reinterpret_cast<uint4 *>(p.buf + r * p.pitch + c0) =
           make_uint4(pack16(true, d[0], d[1]), pack16(true, d[2], d[3]), pack16(true, d[4], d[5]), pack16(true, d[6], d[7]));
@@ -399,7 +435,9 @@ struct SpreadParams {
   const int32_t *place;
   const XentScalars *sc;
   int64_t lddh, Dp;
-  int32_t T, D, kb, bf16;
+  int32_t T, D, bf16;
+  SplitParams split;
+  int32_t raster_group;
 };
 
 // Four columns of a row of dH per thread: its slices added in order; ignored rows are 0.
@@ -411,7 +449,8 @@ __global__ void __launch_bounds__(256) xent_spread_kernel(const __grid_constant_
   griddep_wait();
   griddep_launch_dependents();
   const float scale = p.sc->out_scale;
-  const int kbs = p.sc->kb_split, slices = (p.kb + kbs - 1) / kbs;
+  const int kbs = p.sc->kb_split, full = p.sc->full;
+  const int m_blk = (p.sc->rows + p.split.m - 1) / p.split.m;
   constexpr int kQuads = 256 / kLanes;
   const int lane = threadIdx.x / kQuads;
   const int c = (blockIdx.x * kQuads + threadIdx.x % kQuads) * 4;
@@ -419,6 +458,10 @@ __global__ void __launch_bounds__(256) xent_spread_kernel(const __grid_constant_
     const int r = p.place[i];
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r >= 0 && c < p.D) {
+      // the element's tile in the order of the product's tiles, and so its slices
+      const int mb = r / p.split.m, group = mb / p.raster_group, first_m = group * p.raster_group;
+      const int tile = first_m * p.split.n_blk + c / p.split.n * min(m_blk - first_m, p.raster_group) + mb - first_m;
+      const int slices = tile < full ? 1 : (p.split.kb + kbs - 1) / kbs;
       const float *a = p.part + r * p.Dp + c;
 #pragma unroll 8
       for (int s = lane; s < slices; s += kLanes) {
@@ -608,12 +651,13 @@ int configure(gemm_epi_xent_plan *pl) {
   const int64_t pieces = ceil_div(pl->V, widest);
   pl->piece = round_up(ceil_div(pl->V, pieces), 256);
   // dH: slices of its sum over a piece, decided on the device by the rows that
-  // take part, within 64 MiB or what two waves of CTAs take
+  // take part, within 64 MiB or what four waves of CTAs take of the tiles left over
   const int64_t tiles = tiles_of(pl->part, pl->T, pl->D);
   const int64_t kb = ceil_div(std::min(pl->piece, pl->V), BK);
   const int64_t fit = (int64_t(64) << 20) / (4 * pl->T * pl->Dp);
-  const int64_t want = 2 * int64_t(units_of(pl, pl->part)) / tiles;
-  pl->slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({std::max(fit, want), kb, 64})));
+  const int64_t units = units_of(pl, pl->part), left = tiles % units;
+  const int64_t want = left ? 4 * units / left : 1;
+  pl->slices = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({std::max(fit, std::min<int64_t>(want, 8)), kb, 64})));
   // finish: a block of 1024 threads per row while that is at most two blocks to an SM, then up
   // to 32 rows to a block (37 rows of 858 ranges: 37 blocks 6 us, 2 blocks 11 us)
   pl->row_lanes = 1;
@@ -660,6 +704,9 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalar
 cudaError_t launch_product(const gemm_epi_xent_plan *pl, const Product &pr, XentParams &p, cudaStream_t s) {
   const int64_t tiles = p.band ? ceil_div(p.N, p.band) : tiles_of(pr, p.M, p.N) * (pr.mode == X_PART ? pl->slices : 1);
   const int units = static_cast<int>(std::min<int64_t>(units_of(pl, pr), tiles));
+  // dW: a last wave that would leave half of the CTAs idle runs as half tiles
+  const int64_t last = tiles % units_of(pl, pr);
+  p.num_full = static_cast<int32_t>(last > 0 && 2 * last <= units_of(pl, pr) && tiles > last ? tiles - last : tiles);
   return launch(pr.fn, dim3(static_cast<unsigned>(units * pr.cg)), kXentThreads, pl->smem, pr.cg, &p, s);
 }
 
@@ -693,8 +740,11 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   void *dl = ws + at.dl;
   float *part = reinterpret_cast<float *>(ws + at.part);
   const uint64_t piece = static_cast<uint64_t>(pl->piece);
-  const bool pack = grads || pl->pack;
+  const bool pack = pl->pack;
   const int i32 = pl->d.index == GE_INDEX_I32;
+  const SplitParams split = {128 * pl->part.cg, pl->part.bn, static_cast<int32_t>(ceil_div(D, pl->part.bn)),
+                             static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK)), units_of(pl, pl->part),
+                             pl->slices};
   cudaError_t err = cudaSuccess;
   auto go = [&](cudaError_t e) { return (err = e) == cudaSuccess; };
 
@@ -720,11 +770,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
     pp.i32 = i32;
     const int ctas = static_cast<int>(std::min<int64_t>(ceil_div(T, 8), 2 * pl->sms));
     pp.rows_per_cta = static_cast<int32_t>(ceil_div(T, ctas));
-    pp.part_m = 128 * pl->part.cg;
-    pp.part_n_blk = static_cast<int32_t>(ceil_div(D, pl->part.bn));
-    pp.part_kb = static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK));
-    pp.part_units = units_of(pl, pl->part);
-    pp.part_slices = pl->slices;
+    pp.split = split;
     if (!go(launch(reinterpret_cast<const void *>(xent_pack_kernel), ctas, kPackThreads, 0, 1, &pp, s)))
       return GE_ERR_CUDA;
   }
@@ -771,6 +817,16 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   fp.i32 = i32;
   fp.slots = slots_of(pl);
   fp.row_lanes = pl->row_lanes;
+  if (grads && !pack) {
+    fp.H = static_cast<const uint16_t *>(H);
+    fp.Hc = static_cast<uint16_t *>(Hc);
+    fp.gathered = gathered;
+    fp.place = place;
+    fp.ldh = pl->d.ldh;
+    fp.ldc = pl->ldc;
+    fp.split = split;
+  }
+  fp.D = static_cast<int32_t>(D);
   fp.mean = pl->d.reduction == GE_XENT_MEAN;
   fp.z = pl->d.z_loss;
   fp.grad_scale = grad_scale;
@@ -819,6 +875,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
     }
     if (dW) {
       XentParams o = params_of(pl, pl->out, sc, n, D, T);
+      if (!pack) o.all_rows = static_cast<int32_t>(T) + 1;  // rows that take no part are zeros in Hc alone
       o.out = static_cast<uint16_t *>(dW);
       o.ld_out = pl->d.lddw;
       o.out32 = pl->d.lddw % 16 == 0 && reinterpret_cast<uintptr_t>(dW) % 32 == 0;
@@ -842,8 +899,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   }
   if (dH) {
     SpreadParams dp{part, static_cast<uint16_t *>(dH), place, sc, pl->d.lddh, pl->Dp, static_cast<int32_t>(T),
-                    static_cast<int32_t>(D), static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK)),
-                    ab == GE_BF16};
+                    static_cast<int32_t>(D), ab == GE_BF16, split, params_of(pl, pl->part, sc, T, D, 1).raster_group};
     const bool shared = pl->slices > 8;
     const int64_t across = ceil_div(D, shared ? 128 : 1024);
     const dim3 grid(static_cast<unsigned>(across),

@@ -18,7 +18,8 @@ enum XentMode {
 struct XentScalars {
   int32_t rows;       // rows that take part
   int32_t ticket;     // finish blocks done
-  int32_t kb_split;   // k-blocks of a slice of dH's sum over the vocabulary
+  int32_t full;       // dH: tiles [0, full) sum a whole piece, ...
+  int32_t kb_split;   // ... the others slices of this many k-blocks
   float out_scale;    // multiplies dl @ W and dl^T @ H
   float dl_scale;     // power of two in dl
 };
@@ -43,6 +44,7 @@ struct XentParams {
   int32_t all_rows;        // T
   int32_t M, N, K;         // sizes at most; the rows replace M (K for X_OUT)
   int32_t num_n_blk, raster_group;
+  int32_t num_full;        // X_OUT: tiles [0, num_full) are whole, each later pair the column halves of one
   int32_t stages;
   int32_t a_rows;          // rows of an A tile that are loaded (K-major A, one CTA)
   // X_STATS, X_KEEP of a single tile of rows: columns of a CTA's band (0: tiles dealt out) and its tiles
@@ -53,7 +55,7 @@ struct XentParams {
   uint32_t off_B, off_out, off_bar;
   float c;                 // logit_scale
   float c2;                // logit_scale * log2(e)
-  const void *target;      // the rows' targets, ...
+  const void *target;      // the rows' targets (X_DLOGIT: below 0 for a row that takes no part), ...
   int32_t target_i64;      // ... 8 bytes each, as the caller has them (else 4)
   int32_t keep_cols;       // X_KEEP: columns that are kept
   float2 *stats;           // [2 * blocks of BN columns][M]: maximum (log2 units), sum

@@ -102,9 +102,9 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   // k-blocks that the tensor unit sums before the epilogue adds them up in
   // registers.  Its sums are cut off, not rounded: left to itself over all of K it gives an
   // lse that is low by 2.0e-6 of its value at D = 4096 and 4.0e-6 at 8192, in runs of K = 1024 by
-  // 4.8e-7 whatever D is (256: 1.2e-7, but a run's 2000 clocks are then less than its
-  // sums take to be read, and 4096 x 65536 x 2048 takes 771 us instead of 622).
-  constexpr int kMostRun = 16;
+  // 4.8e-7, of 1536 by 7.2e-7 whatever D is (256: 1.2e-7, but a run's 2000 clocks are then
+  // less than its sums take to be read, and 4096 x 65536 x 2048 takes 771 us instead of 622).
+  constexpr int kMostRun = 24;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -152,8 +152,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   // with no rows dW is 0: one k-block is run and its product dropped
   const int num_kb = MODE == X_OUT ? max(1, (min(rows, p.K) + BK - 1) / BK) : (p.K + BK - 1) / BK;
   const int per_slice = num_m_blk * p.num_n_blk;
+  // dH's last tiles, too few for a wave of CTAs, are split along K; dW's along N
   const int kb_split = MODE == X_PART ? __ldcg(&p.sc->kb_split) : num_kb;
-  const int num_tiles = MODE == X_PART ? per_slice * ((num_kb + kb_split - 1) / kb_split) : per_slice;
+  const int num_full = MODE == X_PART ? min(per_slice, __ldcg(&p.sc->full))
+                       : MODE == X_OUT && CG == 2 ? min(per_slice, p.num_full) : per_slice;
+  const int rest = per_slice - num_full;
+  const int num_tiles = num_full + rest * (MODE == X_PART ? (num_kb + kb_split - 1) / kb_split : 2);
   // (Runs of equal length: a short last one would be waited for.)
   const int runs = kStats ? (num_kb + kMostRun - 1) / kMostRun : 1;
   const int run = kStats ? (num_kb + runs - 1) / runs : num_kb;
@@ -172,12 +176,25 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       t.width = min(BN, p.band - i * BN);
       return t;
     }
-    const int at = unit + i * n_units;
-    tile_coords(num_m_blk, p.num_n_blk, p.raster_group, at, t.z, t.mb, t.nb);
-    t.kb0 = MODE == X_PART ? t.z * kb_split : 0;
-    t.kb1 = MODE == X_PART ? min(num_kb, t.kb0 + kb_split) : num_kb;
-    t.n0 = t.nb * BN;
-    t.width = BN;
+    int at = unit + i * n_units, half = -1;
+    const bool split = at >= num_full;
+    t.z = 0;
+    if (split) {
+      const int j = at - num_full;
+      if (MODE == X_PART) {
+        t.z = j / rest;
+        at = num_full + j - t.z * rest;
+      } else {
+        half = j & 1;
+        at = num_full + (j >> 1);
+      }
+    }
+    int batch;
+    tile_coords(num_m_blk, p.num_n_blk, p.raster_group, at, batch, t.mb, t.nb);
+    t.kb0 = MODE == X_PART && split ? t.z * kb_split : 0;
+    t.kb1 = MODE == X_PART && split ? min(num_kb, t.kb0 + kb_split) : num_kb;
+    t.n0 = t.nb * BN + (half > 0 ? BN / 2 : 0);
+    t.width = half < 0 ? BN : BN / 2;
     return t;
   };
 
@@ -193,7 +210,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       for (int i = 0; ok && i < my_tiles; ++i) {
         const XentTile t = tile(i);
         const int m0 = t.mb * T::kMmaM + static_cast<int>(rank) * BM;
-        const int n0 = t.n0 + static_cast<int>(rank) * T::kBnLocal;
+        const int n0 = t.n0 + static_cast<int>(rank) * (t.width / CG);
         const int nk = t.kb1 - t.kb0;
         for (int kb = 0; kb < nk; ++kb) {
           if (!wt.wait(bar + kXEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
@@ -207,7 +224,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           uint32_t fb = full;
           if constexpr (CG == 2) {
             fb = mapa_shared(full, 0);
-            if (rank == 0) mbar_arrive_expect_tx(full, CG * (T::kABytes + T::kBBytes));
+            if (rank == 0) mbar_arrive_expect_tx(full, CG * T::kABytes + t.width * 128);
           } else {
             // few rows: only theirs are loaded; what the others' accumulators then hold is not read
             mbar_arrive_expect_tx(full, (kAmn ? T::kABytes : p.a_rows * 128) + (bands ? t.width * 128 : T::kBBytes));
@@ -230,7 +247,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             // dH: the k rows of B are the piece's vocabulary rows
             const int ky = MODE == X_PART ? p.b_row0 + kx : kx;
 #pragma unroll
-            for (int j = 0; j < T::kBAtoms; ++j) load(sbb + j * 8192, mB, n0 + 64 * j, ky);
+            for (int j = 0; j < T::kBAtoms; ++j)
+              if (64 * j < t.width / CG) load(sbb + j * 8192, mB, n0 + 64 * j, ky);
           }
           ++fills;
           if (++stage == p.stages) {
@@ -327,7 +345,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       const XentTile t = tile(i);
       const int m = t.mb * T::kMmaM + static_cast<int>(rank) * BM + row;
       const int n0 = t.n0;
-      const bool live = m < M;
+      bool live = m < M;
       // what the row needs, on its way while the tile's product finishes
       int target = -1;
       float lse2 = 0.f, out_scale = 0.f;
@@ -335,6 +353,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       if ((kStats || MODE == X_DLOGIT) && live) {
         const int64_t at = p.target_i64 ? static_cast<const int64_t *>(p.target)[m] : static_cast<const int32_t *>(p.target)[m];
         // no column of this tile for a target that is elsewhere (or does not exist)
+        if (MODE == X_DLOGIT && at < 0) live = false;
         const int64_t off = at - p.b_row0 - n0;
         target = off >= 0 && off < t.width ? static_cast<int>(off) : -1;
       }
@@ -371,33 +390,37 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         // this group's columns, 64 of every 128, in registers
         constexpr int kParts = BN / 64;  // of 32 columns: grp * 64 + 128 (j / 2) + 32 (j % 2)
         float v[kParts][32];
-#pragma unroll
-        for (int j = 0; j < kParts; ++j)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) v[j][e] = 0.f;
-        bool ok = true;
-        for (int first = t.kb0; first < t.kb1; first += run) {
-          if (!(ok = ready())) break;
+        auto part = [&](int j) { return 128 * (j / 2) + 32 * (j % 2); };
+        bool ok = ready();
+        if (!ok) break;
+        {  // the first run: all loads on their way at once
           const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN + grp * 64);
 #pragma unroll
           for (int j = 0; j < kParts; ++j) {
-            const int c0 = 128 * (j / 2) + 32 * (j % 2);
+            tmem_ld16(acc + part(j), *reinterpret_cast<float(*)[16]>(v[j]));
+            tmem_ld16(acc + part(j) + 16, *reinterpret_cast<float(*)[16]>(v[j] + 16));
+          }
+          tmem_wait_ld();
+          release();
+        }
+        for (int first = t.kb0 + run; first < t.kb1; first += run) {
+          if (!(ok = ready())) break;
+          const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN + grp * 64);
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-              float x[16];
-              tmem_ld16(acc + c0 + h, x);
-              tmem_wait_ld();
+          for (int j = 0; j < 2 * kParts; ++j) {
+            float x[16];
+            tmem_ld16(acc + part(j / 2) + 16 * (j % 2), x);
+            tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) v[j][h + e] += x[e];
-            }
+            for (int e = 0; e < 16; ++e) v[j / 2][16 * (j % 2) + e] += x[e];
           }
           release();
         }
         if (!ok) break;
-        float top = -INFINITY;
+        const bool upside = p.c2 >= 0.f;  // the largest logit is the largest product, or the least
 #pragma unroll
         for (int j = 0; j < kParts; ++j) {
-          const int c0 = grp * 64 + 128 * (j / 2) + 32 * (j % 2);
+          const int c0 = grp * 64 + part(j);
           const int at = target - c0;
           if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
             float x = 0.f;
@@ -406,21 +429,33 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             if (at >= 0 && at < 32 && target < limit) p.at_target[m] = x * p.c;
           }
           const int end = min(limit, t.width) - c0;
+          if (end < 32) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            v[j][e] *= p.c2;
-            if (end < 32 && e >= end) v[j][e] = -INFINITY;
-            top = fmaxf(top, v[j][e]);
+            for (int e = 0; e < 32; ++e)
+              if (e >= end) v[j][e] = upside ? -INFINITY : INFINITY;
           }
         }
+        float top = upside ? -INFINITY : INFINITY;
+        if (upside) {
+#pragma unroll
+          for (int j = 0; j < kParts; ++j)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, v[j][e]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kParts; ++j)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fminf(top, v[j][e]);
+        }
+        top *= p.c2;
         const float off = top == -INFINITY ? 0.f : top;
         const bool keep = MODE == X_KEEP && n0 < p.keep_cols && live;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kParts; ++j) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[j][e] -= off;
-          const int c0 = grp * 64 + 128 * (j / 2) + 32 * (j % 2);
+          for (int e = 0; e < 32; ++e) v[j][e] = fmaf(v[j][e], p.c2, -off);
+          const int c0 = grp * 64 + part(j);
           if (keep && c0 < t.width) {
             // the distances, rounded to integers in the low bits of floats of 2^23 and more
             constexpr float k0 = 8388608.f, kStepsPerOctave = 1 << kKeptBits;
@@ -481,12 +516,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         // about 12000 clocks, longer than 17 k-blocks' products.)
         if (!ready()) break;
         const uint32_t acc = tq + static_cast<uint32_t>(abuf * BN);
-        for (int c0 = grp * 32; c0 < BN; c0 += 64) {
+        for (int c0 = grp * 32; c0 < t.width; c0 += 64) {
           float v[32];
           tmem_ld16(acc + c0, *reinterpret_cast<float(*)[16]>(v));
           tmem_ld16(acc + c0 + 16, *reinterpret_cast<float(*)[16]>(v + 16));
           tmem_wait_ld();
-          if (c0 + 64 >= BN) release();
+          if (c0 + 64 >= t.width) release();
           if constexpr (MODE == X_DLOGIT) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], p.c2, -lse2)) * coef.x;
