@@ -781,7 +781,8 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   if (!encode_rows(&sl.tmA, ab, pack ? Hc : H, D, T, 1, pack ? pl->ldc : pl->d.ldh,
                    (pack ? pl->ldc : pl->d.ldh) * T, BK, sl.a_rows) ||
       !encode_rows(&sl.tmH, ab, H, D, T, 1, pl->d.ldh, pl->d.ldh * T, BK, sl.a_rows) ||
-      !encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, pl->band ? 32 : 128))
+      !encode_rows(&sl.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128) ||
+      (pl->band && !encode_rows(&sl.tmB32, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 32)))
     return GE_ERR_CUDA;
   sl.band = static_cast<int32_t>(pl->band);
   sl.band_tiles = static_cast<int32_t>(pl->band ? ceil_div(pl->band, first.bn) : 0);
@@ -870,8 +871,8 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       q.coef = coef;
       q.out = static_cast<uint16_t *>(dl);
       q.ld_out = pl->piece;
-      if (!encode_rows(&q.tmB, ab, W, D, V, 1, pl->d.ldw, pl->d.ldw * V, BK, 128) ||
-          !go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
+      q.tmB = sl.tmB;
+      if (!go(launch_product(pl, pl->dlogit, q, s))) return GE_ERR_CUDA;
     }
     if (dW) {
       XentParams o = params_of(pl, pl->out, sc, n, D, T);

@@ -36,6 +36,7 @@ constexpr uint32_t kXentBox = 128 * 128; // one box: 128 rows of 128 bytes
 
 struct XentParams {
   CUtensorMap tmA, tmB, tmOut;
+  CUtensorMap tmB32;       // bands: B in boxes of 32 rows
   CUtensorMap tmH;         // H itself, read in the packed rows' place when every row takes part
   uint32_t *status;
   uint64_t timeout_ns;
