@@ -192,22 +192,25 @@ void set_shape(NormParams *p, const RowShape &r) {
   p->ahead = r.ahead;
 }
 
-// Units of the gradient pass: as many as the GPU holds at once, rounded so that
-// a unit stays inside a gate group or holds whole ones.
+// Units of the gradient pass: CTAs, as many as the GPU holds at once, rounded so that
+// a unit stays inside a gate group or each of its lanes holds whole ones.
 void share_rows(gemm_epi_norm_plan *pl) {
   NormParams &p = pl->p;
   const RowShape &r = pl->bwd;
   const int64_t lanes = r.threads / r.row_threads;
-  int64_t want = ceil_div(pl->T, std::min<int64_t>(pl->T, int64_t(r.grid) * lanes));  // rows per unit
   const int64_t rpg = pl->d.rows_per_gate ? std::min<int64_t>(pl->d.rows_per_gate, pl->T) : pl->T;
   const int64_t groups = ceil_div(pl->T, rpg);
-  if (rpg <= want && pl->d.rows_per_gate) {
-    p.rows_per_unit = static_cast<int32_t>(want / rpg * rpg);
+  int64_t want = ceil_div(pl->T, r.grid);  // rows per unit
+  const int64_t lane = ceil_div(want, lanes);
+  if (rpg <= lane && pl->d.rows_per_gate) {
+    p.rows_per_lane = static_cast<int32_t>(lane / rpg * rpg);
+    p.rows_per_unit = static_cast<int32_t>(p.rows_per_lane * lanes);
     p.units_per_group = 0;
     p.units = static_cast<int32_t>(ceil_div(pl->T, p.rows_per_unit));
   } else {
     p.units_per_group = static_cast<int32_t>(ceil_div(rpg, want));
-    p.rows_per_unit = static_cast<int32_t>(ceil_div(rpg, p.units_per_group));
+    p.rows_per_lane = static_cast<int32_t>(ceil_div(ceil_div(rpg, p.units_per_group), lanes));
+    p.rows_per_unit = static_cast<int32_t>(p.rows_per_lane * lanes);
     p.units_per_group = static_cast<int32_t>(ceil_div(rpg, p.rows_per_unit));
     p.units = static_cast<int32_t>(groups * p.units_per_group);
   }
@@ -367,9 +370,7 @@ int gemm_epi_norm_grad(gemm_epi_norm_plan *pl, const void *dy, const void *dh, c
   p.part_pre = static_cast<float *>(workspace);
   p.part_post = b ? p.part_pre + static_cast<size_t>(p.units) * static_cast<size_t>(p.ld_part) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int lanes = pl->bwd.threads / pl->bwd.row_threads;
-  const int grid = static_cast<int>(ceil_div(p.units, lanes));
-  if (launch(pl->bwd.fn, dim3(grid), dim3(pl->bwd.threads), pl->bwd.smem, &p, s) != cudaSuccess) return GE_ERR_CUDA;
+  if (launch(pl->bwd.fn, dim3(static_cast<unsigned>(p.units)), dim3(pl->bwd.threads), pl->bwd.smem, &p, s) != cudaSuccess) return GE_ERR_CUDA;
   const bool gates = dgate && p.units_per_group;
   if (!dw_pre && !dw_post && !gates) return GE_OK;
   SumParams q;

@@ -32,7 +32,8 @@ struct NormParams {
   int32_t ahead;         // rows of the ring
   int32_t w_vec;         // gate's rows and the vectors are whole 16-byte units
   // units of the gradient pass
-  int32_t units, rows_per_unit, units_per_group;  // units_per_group 0: a unit holds whole groups
+  int32_t units, rows_per_unit, rows_per_lane;
+  int32_t units_per_group;  // 0: a lane holds whole groups
 };
 
 // nv chunks per thread; threads of a CTA; vec: rows are whole 16-byte units (nv 1 and 2

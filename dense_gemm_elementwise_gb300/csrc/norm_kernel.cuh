@@ -178,41 +178,44 @@ struct Own {
         v[k][2 * j + 1] = mul2(v[k][2 * j + 1], make_float2(f.z, f.w));
       }
   }
-  // scale * a[off + column] (times what is there, with `into`), 0 past the end; a
-  // vector that is NULL counts as 1.
-  // Not inlined: it runs once for many rows, and its instructions would crowd
-  // out the others'; one chunk at a time, to leave the callers their registers.
+  // scale * a[off + column] * b[column], 0 past the end; a vector that is NULL
+  // counts as 1.  Not inlined: it runs once for many rows, and its
+  // instructions would crowd out the others'; one chunk at a time, to leave the
+  // callers their registers.
   template <int NV, int PATH>
   __device__ __noinline__ void fill(const NormParams &p, const Columns<PATH> &col, float scale, const void *a,
-                                    int64_t off, bool into = false) const {
+                                    int64_t off, const void *b) const {
 #pragma unroll 1
     for (int k = 0; k < NV; ++k) {
-      float f[kChunk];
-      if (!a) {
+      // the loads of both vectors are on their way before the first is used
+      float f[kChunk], g[kChunk];
+      if (p.wt == GE_F32) read<GE_F32>(p, col, k, a, off, f), read<GE_F32>(p, col, k, b, 0, g);
+      else if (p.wt == GE_F16) read<GE_F16>(p, col, k, a, off, f), read<GE_F16>(p, col, k, b, 0, g);
+      else read<GE_BF16>(p, col, k, a, off, f), read<GE_BF16>(p, col, k, b, 0, g);
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) f[i] = 1.f;
-      } else if (PATH != P_STRIDED && p.w_vec && p.wt != GE_F32 && col(k, 0) < p.D) {
-        const uint4 w = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a) + off + col(k, 0));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 v = p.wt == GE_F16 ? Elem<GE_F16>::get2(u[i]) : Elem<GE_BF16>::get2(u[i]);
-          f[2 * i] = v.x;
-          f[2 * i + 1] = v.y;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) f[i] = getw(p.wt, a, off + min(col(k, i), p.D - 1));
-      }
+      for (int i = 0; i < kChunk; ++i) f[i] *= g[i];
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) f[i] = col(k, i) < p.D ? scale * f[i] : 0.f;
-      float4 &lo = base[2 * k * threads], &hi = base[(2 * k + 1) * threads];
-      if (into) {
-        f[0] *= lo.x, f[1] *= lo.y, f[2] *= lo.z, f[3] *= lo.w;
-        f[4] *= hi.x, f[5] *= hi.y, f[6] *= hi.z, f[7] *= hi.w;
-      }
-      lo = make_float4(f[0], f[1], f[2], f[3]);
-      hi = make_float4(f[4], f[5], f[6], f[7]);
+      base[2 * k * threads] = make_float4(f[0], f[1], f[2], f[3]);
+      base[(2 * k + 1) * threads] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+  }
+  template <int WT, int PATH>
+  static __device__ __forceinline__ void read(const NormParams &p, const Columns<PATH> &col, int k, const void *v,
+                                              int64_t off, float (&f)[kChunk]) {
+    using T = typename Elem<WT>::T;
+    const T *q = static_cast<const T *>(v) + off;
+    if (!v) {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) f[i] = 1.f;
+    } else if (PATH != P_STRIDED && WT != GE_F32 && p.w_vec && col(k, 0) < p.D) {
+      union { uint4 w; T e[kChunk]; } u;
+      u.w = *reinterpret_cast<const uint4 *>(q + col(k, 0));
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) f[i] = Elem<WT>::get(u.e[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) f[i] = Elem<WT>::get(q[min(col(k, i), p.D - 1)]);
     }
   }
   // what is kept, to a row of the weights' type
@@ -231,8 +234,9 @@ struct Own {
 
 // Rows on their way from memory: NA tensors of them.  P_RING: `ahead` rows, by cp.async
 // into the thread's own words of shared memory.  P_STRIDED: the next row's
-// elements in registers, asked for once the current row's have been taken.
-template <int DT, int NV, int PATH, int NA>
+// elements in registers, asked for once the current row's have been taken (kEarly; CTAs of over 512
+// threads have no registers for that and read a row when it is wanted).
+template <int DT, int NV, int PATH, int NA, bool kEarly>
 struct Ring {
   using T = typename Elem<DT>::T;
   static constexpr int kWords = kChunk * sizeof(T) / 16;  // of one tensor's chunk
@@ -240,7 +244,8 @@ struct Ring {
   uint4 *base;
   int threads, ahead, D;
   Columns<PATH> col;
-  T raw[PATH == P_STRIDED ? NA : 1][PATH == P_STRIDED ? NV : 1][kChunk];
+  static constexpr bool kRaw = PATH == P_STRIDED && kEarly;
+  T raw[kRaw ? NA : 1][kRaw ? NV : 1][kChunk];
 
   __device__ __forceinline__ Ring(uint4 *base_, int threads_, int ahead_, int D_, const Columns<PATH> &col_)
       : base(base_), threads(threads_), ahead(ahead_), D(D_), col(col_) {}
@@ -261,7 +266,7 @@ struct Ring {
                        "r"(left)
                        : "memory");
         }
-    } else if constexpr (PATH == P_STRIDED) {
+    } else if constexpr (kRaw) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -293,7 +298,7 @@ struct Ring {
       v[3] = Elem<DT>::get2(w[0].w);
     }
   }
-  // row, on: where P_DIRECT finds it, and whether it is there
+  // row, on: where a row that is read now is, and whether it is there (else `row` is some row that is)
   __device__ __forceinline__ void get(int slot, int a, const T *row, bool on, float2 (&v)[NV][kPairs]) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -316,10 +321,16 @@ struct Ring {
           }
         }
       } else {
+        T e[kChunk];
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          if constexpr (kRaw) e[i] = raw[a][k][i];
+          else e[i] = row[on ? min(col(k, i), D - 1) : 0];
+        }
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
-          v[k][i].x = col(k, 2 * i) < D ? Elem<DT>::get(raw[a][k][2 * i]) : 0.f;
-          v[k][i].y = col(k, 2 * i + 1) < D ? Elem<DT>::get(raw[a][k][2 * i + 1]) : 0.f;
+          v[k][i].x = col(k, 2 * i) < D ? Elem<DT>::get(e[2 * i]) : 0.f;
+          v[k][i].y = col(k, 2 * i + 1) < D ? Elem<DT>::get(e[2 * i + 1]) : 0.f;
         }
       }
     }
@@ -456,7 +467,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
   const int n = blockDim.x;
   // w_pre; alpha gate w_post of the gate group at hand
   const Own own_pre{words, n}, own_post{words + 2 * NV * n, n};
-  Ring<DT, NV, PATH, 2> ring(reinterpret_cast<uint4 *>(words + 4 * NV * n), n, p.ahead, p.D, col);
+  Ring<DT, NV, PATH, 2, kBound <= kVecThreads> ring(reinterpret_cast<uint4 *>(words + 4 * NV * n), n, p.ahead, p.D, col);
   const int step = gridDim.x * rows;
   int64_t first = int64_t(blockIdx.x) * rows;  // the CTA's first row: every thread's loop is as long
   int64_t row = first + pl.mine;
@@ -474,7 +485,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
     ahead += step;
   };
   for (int s = 0; s < (kAsk ? p.ahead - 1 : 1); ++s) fetch(s);
-  if (p.w_pre) own_pre.fill<NV>(p, col, 1.f, p.w_pre, 0);
+  if (p.w_pre) own_pre.fill<NV>(p, col, 1.f, p.w_pre, 0, nullptr);
   int32_t at = -1;  // the group that own_post is for
   Group group{static_cast<int32_t>(p.rows_per_gate), 0, 0};
   int slot = 0, next = p.ahead - 1;
@@ -482,23 +493,28 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
     const bool on = row < p.T;
     if (kAsk) fetch(next);
     if (++next == p.ahead) next = 0;
-    ring.wait();
-    float2 v[NV][kPairs];
-    if (!kAsk || !b) ring.get(slot, 0, x + row * p.ldx, on, v);
-    if (b) {
-      float2 u[NV][kPairs];
-      ring.get(slot, 1, b + row * p.ldb, on, u);
-      if (!kAsk) fetch(0);
+    // the factors of the row's gate group: while the row is on its way, but not while it is in
+    // registers, which the call would have to save
+    auto factors = [&]() {
       if (p.gate && on) group.move(static_cast<int32_t>(row));
       if (at != group.g) {
         at = group.g;
-        own_post.fill<NV>(p, col, p.alpha, p.w_post, 0);
-        if (p.gate) own_post.fill<NV>(p, col, 1.f, p.gate, int64_t(at) * p.D, true);
+        own_post.fill<NV>(p, col, p.alpha, p.gate, int64_t(at) * p.D, p.w_post);
       }
+    };
+    if (PATH != P_STRIDED && b) factors();
+    ring.wait();
+    float2 v[NV][kPairs];
+    if (!kAsk || !b) ring.get(slot, 0, x + (on ? row : 0) * p.ldx, on, v);
+    if (b) {
+      float2 u[NV][kPairs];
+      ring.get(slot, 1, b + (on ? row : 0) * p.ldb, on, u);
+      if (!kAsk) fetch(0);
+      if (PATH == P_STRIDED) factors();
       const float r = p.post != GE_NORM_NONE
                           ? divisor(u, p.post, p.eps_post, p.inv_d, p.D, col, row_sum) : 1.f;
       own_post.times(u);
-      if (kAsk) ring.get(slot, 0, x + row * p.ldx, on, v);
+      if (kAsk) ring.get(slot, 0, x + (on ? row : 0) * p.ldx, on, v);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -520,19 +536,20 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
   }
 }
 
-// The rows of unit u.
-__device__ __forceinline__ void unit_rows(const NormParams &p, int u, int64_t &begin, int64_t &end) {
-  begin = end = p.T;
-  if (u >= p.units) return;
+// The rows of lane `lane` of unit u: a unit is a CTA, its lanes take runs of rows_per_lane rows.
+__device__ __forceinline__ void unit_rows(const NormParams &p, int u, int lane, int64_t &begin, int64_t &end) {
+  int64_t stop;
   if (p.units_per_group) {
     const int64_t g = u / p.units_per_group, s = u - g * p.units_per_group;
     begin = g * p.rows_per_gate + s * p.rows_per_unit;
-    end = min(min(begin + p.rows_per_unit, (g + 1) * p.rows_per_gate), int64_t(p.T));
-    begin = min(begin, end);
+    stop = min(min(begin + p.rows_per_unit, (g + 1) * p.rows_per_gate), int64_t(p.T));
   } else {
     begin = int64_t(u) * p.rows_per_unit;
-    end = min(begin + p.rows_per_unit, int64_t(p.T));
+    stop = min(begin + p.rows_per_unit, int64_t(p.T));
   }
+  begin += int64_t(lane) * p.rows_per_lane;
+  end = min(begin + p.rows_per_lane, stop);
+  begin = min(begin, end);
 }
 
 // kWhole: a unit holds whole gate groups
@@ -549,10 +566,9 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
   // w_pre; alpha gate w_post of the gate group at hand, or (kWhole) its gate and alpha w_post apart
   constexpr int kFactors = kWhole ? 3 : 2;
   const Own own_pre{words, n}, own_post{words + 2 * NV * n, n}, own_w{words + 4 * NV * n, n};
-  Ring<DT, NV, PATH, 4> ring(reinterpret_cast<uint4 *>(words + kFactors * 2 * NV * n), n, p.ahead, p.D, col);
-  const int u = blockIdx.x * (n / pl.per) + pl.mine;
+  Ring<DT, NV, PATH, 4, kBound <= kVecThreads> ring(reinterpret_cast<uint4 *>(words + kFactors * 2 * NV * n), n, p.ahead, p.D, col);
   int64_t row, end;
-  unit_rows(p, u, row, end);
+  unit_rows(p, blockIdx.x, pl.mine, row, end);
   const T *yin = static_cast<const T *>(p.yin), *dh = static_cast<const T *>(p.dh),
           *dy = static_cast<const T *>(p.dy), *b = static_cast<const T *>(p.b);
   T *dx = static_cast<T *>(p.dx), *db = static_cast<T *>(p.db);
@@ -570,8 +586,8 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
     ++ahead;
   };
   for (int s = 0; s < (kAsk ? p.ahead - 1 : 1); ++s) fetch(s);
-  if (p.w_pre) own_pre.fill<NV>(p, col, 1.f, p.w_pre, 0);
-  if (kWhole && b) own_w.fill<NV>(p, col, p.alpha, p.w_post, 0);
+  if (p.w_pre) own_pre.fill<NV>(p, col, 1.f, p.w_pre, 0, nullptr);
+  if (kWhole && b) own_w.fill<NV>(p, col, p.alpha, p.w_post, 0, nullptr);
   float2 acc_pre[NV][kPairs], acc_post[NV][kPairs];
   float2 acc_gate[kWhole ? NV : 1][kPairs];  // whole groups: the current group's q
 #pragma unroll
@@ -587,15 +603,23 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
   const bool layer_b = b && p.post == GE_NORM_LAYER, norm_b = b && p.post != GE_NORM_NONE;
   // every thread goes round as often: row sums hold barriers.  Past a unit's
   // last row what is computed is dropped.
-  for (int r = 0; r < p.rows_per_unit; ++r, ++row) {
+  for (int r = 0; r < p.rows_per_lane; ++r, ++row) {
     const bool on = row < end;
     if (kAsk) fetch(next);
     if (++next == p.ahead) next = 0;
+    auto factors = [&]() {  // of the row's gate group, as in the forward pass
+      if (p.gate && on) group.move(static_cast<int32_t>(row));
+      if (at != group.g) {
+        at = group.g;
+        own_post.fill<NV>(p, col, kWhole ? 1.f : p.alpha, p.gate, int64_t(at) * p.D, kWhole ? nullptr : p.w_post);
+      }
+    };
+    if (PATH != P_STRIDED && b) factors();
     ring.wait();
     // y becomes what N_pre divides, d = dh w_pre, q = dh y
     float2 y[NV][kPairs], d[NV][kPairs], q[NV][kPairs];
-    ring.get(slot, 0, yin + row * p.ldy, on, y);
-    ring.get(slot, 1, dh + row * p.ldh, on, d);
+    ring.get(slot, 0, yin + (on ? row : 0) * p.ldy, on, y);
+    ring.get(slot, 1, dh + (on ? row : 0) * p.ldh, on, d);
     float mean_d = 0.f;
     if (p.pre == GE_NORM_LAYER) {
       float s[2];
@@ -648,24 +672,19 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
       for (int i = 0; i < kPairs; ++i)
         d[k][i] = fma2(d[k][i], both(ry), fma2(y[k][i], both(along), both(mean)));
     if (dy) {
-      ring.get(slot, 2, dy + row * p.ldy, on, y);
+      ring.get(slot, 2, dy + (on ? row : 0) * p.ldy, on, y);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) d[k][i] = add2(d[k][i], y[k][i]);
     }
-    if (b) ring.get(slot, 3, b + row * p.ldb, on, y);  // read before dx is written: it may be in b's place
+    if (b) ring.get(slot, 3, b + (on ? row : 0) * p.ldb, on, y);  // read before dx is written: it may be in b's place
     if (++slot == p.ahead) slot = 0;
     if (!kAsk) fetch(0);
     if (on) store_row<DT, NV, PATH>(dx + row * p.ldx, col, p.D, d);
     if (!b) continue;
     // y is now b, or what N_post divides
-    if (p.gate && on) group.move(static_cast<int32_t>(row));
-    if (at != group.g) {
-      at = group.g;
-      if (!kWhole) own_post.fill<NV>(p, col, p.alpha, p.w_post, 0);
-      if (p.gate) own_post.fill<NV>(p, col, 1.f, p.gate, int64_t(at) * p.D, !kWhole);
-    }
+    if (PATH == P_STRIDED) factors();
     if (layer_b) {
       float m[1] = {sum_of(y)};
       row_sum(m);
@@ -718,9 +737,29 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
         for (int i = 0; i < kPairs; ++i) acc_gate[k][i] = both(0.f);
     }
   }
-  if (u < p.units) {
-    store_row<GE_F32, NV, PATH>(p.part_pre + int64_t(u) * p.ld_part, col, p.D, acc_pre);
-    if (p.part_post) store_row<GE_F32, NV, PATH>(p.part_post + int64_t(u) * p.ld_part, col, p.D, acc_post);
+  // the lanes' sums in order, through the words that held w_pre's factors
+  const int lanes = n / pl.per;
+  auto over_lanes = [&](float2 (&v)[NV][kPairs]) {
+    if (lanes == 1) return;
+    own_pre.put(v);
+    __syncthreads();
+    if (pl.mine == 0)
+      for (int l = 1; l < lanes; ++l) {
+        float2 w[NV][kPairs];
+        Own{own_pre.base + l * pl.per, n}.get(w);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) v[k][i] = add2(v[k][i], w[k][i]);
+      }
+    __syncthreads();
+  };
+  if (lanes > 1) __syncthreads();
+  over_lanes(acc_pre);
+  if (p.part_post) over_lanes(acc_post);
+  if (pl.mine == 0) {
+    store_row<GE_F32, NV, PATH>(p.part_pre + int64_t(blockIdx.x) * p.ld_part, col, p.D, acc_pre);
+    if (p.part_post) store_row<GE_F32, NV, PATH>(p.part_post + int64_t(blockIdx.x) * p.ld_part, col, p.D, acc_post);
   }
 }
 
