@@ -94,7 +94,7 @@ class ge_xent_desc(ctypes.Structure):
     _fields_ = [("ab", ctypes.c_int32), ("index", ctypes.c_int32), ("reduction", ctypes.c_int32),
                 ("timeout_ms", ctypes.c_int32), ("max_ctas", ctypes.c_int32),
                 ("logit_scale", ctypes.c_float), ("z_loss", ctypes.c_float),
-                ("reserved", ctypes.c_int32), ("ldh", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("debug_flags", ctypes.c_uint32), ("ldh", ctypes.c_int64), ("ldw", ctypes.c_int64),
                 ("lddh", ctypes.c_int64), ("lddw", ctypes.c_int64),
                 ("buffer_bytes", ctypes.c_int64)]
 
@@ -355,12 +355,12 @@ def prepare_run(plan, A, B, aux, scalars, outs, stream=None):
 # ------------------------------------------------------- vocabulary loss --
 
 def make_xent_desc(ab, index="i64", ldh=0, ldw=0, lddh=0, lddw=0, logit_scale=1.0, z_loss=0.0,
-                   reduction="mean", buffer_bytes=0, timeout_ms=0, max_ctas=0):
+                   reduction="mean", buffer_bytes=0, timeout_ms=0, max_ctas=0, debug_flags=0):
     d = ge_xent_desc()
     d.ab = DTYPE[ab] if isinstance(ab, str) else ab
     d.index = INDEX[index] if isinstance(index, str) else index
     d.reduction = REDUCTION[reduction] if isinstance(reduction, str) else reduction
-    d.timeout_ms, d.max_ctas = timeout_ms, max_ctas
+    d.timeout_ms, d.max_ctas, d.debug_flags = timeout_ms, max_ctas, debug_flags
     d.logit_scale, d.z_loss = logit_scale, z_loss
     d.ldh, d.ldw, d.lddh, d.lddw = ldh, ldw, lddh, lddw
     d.buffer_bytes = buffer_bytes

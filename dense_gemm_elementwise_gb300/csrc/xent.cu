@@ -690,6 +690,7 @@ XentParams params_of(const gemm_epi_xent_plan *pl, const Product &pr, XentScalar
   const int64_t m_blk = ceil_div(M, 128 * pr.cg);
   p.raster_group = m_blk <= 16 ? 16 : 12;
   p.stages = pr.stages;
+  p.debug_flags = pl->d.debug_flags;
   p.a_rows = static_cast<int32_t>(a_rows_of(pl, pr));
   p.bf16 = pl->d.ab == GE_BF16;
   p.off_B = pr.off_B;
@@ -923,7 +924,7 @@ int gemm_epi_xent_plan_create(gemm_epi_xent_plan **plan, int64_t T, int64_t V, i
   if (desc->ab != GE_F16 && desc->ab != GE_BF16) return GE_ERR_UNSUPPORTED;
   if (desc->index != GE_INDEX_I64 && desc->index != GE_INDEX_I32) return GE_ERR_UNSUPPORTED;
   if ((desc->reduction != GE_XENT_SUM && desc->reduction != GE_XENT_MEAN) || desc->timeout_ms < 0 ||
-      desc->max_ctas < 0 || desc->reserved != 0 || desc->buffer_bytes < 0 || !std::isfinite(desc->logit_scale) ||
+      desc->max_ctas < 0 || (desc->debug_flags & ~GE_DEBUG_SKIP_FIRST_LOAD) != 0 || desc->buffer_bytes < 0 || !std::isfinite(desc->logit_scale) ||
       !std::isfinite(desc->z_loss))
     return GE_ERR_INVALID;
   const int64_t most = (int64_t(1) << 31) - 1;

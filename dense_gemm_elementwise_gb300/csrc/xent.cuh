@@ -47,6 +47,7 @@ struct XentParams {
   int32_t num_n_blk, raster_group;
   int32_t num_full;        // X_OUT: tiles [0, num_full) are whole, each later pair the column halves of one
   int32_t stages;
+  uint32_t debug_flags;
   int32_t a_rows;          // rows of an A tile that are loaded (K-major A, one CTA)
   // X_STATS, X_KEEP of a single tile of rows: columns of a CTA's band (0: tiles dealt out) and its tiles
   int32_t band, band_tiles;

@@ -203,9 +203,16 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer --
     if (lane == 0) {
-      int stage = 0, fills = 0;
+      int stage = 0, fills = 0, skipped = -1;
       uint32_t phase = 0;
-      bool ok = true;
+      bool ok = true, skip = (p.debug_flags & GE_DEBUG_SKIP_FIRST_LOAD) != 0u;
+      auto next_stage = [&]() {
+        ++fills;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
       // rows of H: packed, or H as it is
       const bool packed = rows < p.all_rows;
       const CUtensorMap *mA = kBk && !packed ? &p.tmH : &p.tmA, *mB = MODE == X_OUT && !packed ? &p.tmH : &p.tmB;
@@ -223,32 +230,32 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             int at[kTogether], kq[kTogether];
 #pragma unroll
             for (int q = 0; q < kTogether; ++q) {
-              if (q >= some || !ok) break;
+              at[q] = kq[q] = -1;
+              if (q >= some || !ok) continue;
               ok = wt.wait(bar + kXEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY);
-              if (!ok) break;
-              at[q] = stage;
-              kq[q] = (i & 1) ? nk - 1 - kb - q : kb + q;
-              const uint32_t full = bar + kXFull + 8 * stage;
-              mbar_arrive_expect_tx(full, p.a_rows * 128 + t.width * 128);
-              tma_load_3d(sb + stage * T::kABytes, mA, full, kq[q] * BK, m0, 0);
-              ++fills;
-              if (++stage == p.stages) {
-                stage = 0;
-                phase ^= 1u;
+              if (!ok) continue;
+              if (skip) {
+                skip = false;
+                skipped = fills;
+              } else {
+                at[q] = stage;
+                kq[q] = (i & 1) ? nk - 1 - kb - q : kb + q;
+                const uint32_t full = bar + kXFull + 8 * stage;
+                mbar_arrive_expect_tx(full, p.a_rows * 128 + t.width * 128);
+                tma_load_3d(sb + stage * T::kABytes, mA, full, kq[q] * BK, m0, 0);
               }
+              next_stage();
             }
-            // (a wait that ran out: what was begun above is completed all the same)
-            const int begun = ok ? some : 0;
             if (t.width == BN) {
 #pragma unroll
               for (int q = 0; q < kTogether; ++q)
-                if (q < begun)
+                if (at[q] >= 0)
                   tma_load_3d(sb + p.off_B + at[q] * T::kBBytes, mB, bar + kXFull + 8 * at[q], kq[q] * BK, n0, 0);
             } else {
               for (int j = 0; j < t.width; j += 32)
 #pragma unroll
                 for (int q = 0; q < kTogether; ++q)
-                  if (q < begun)
+                  if (at[q] >= 0)
                     tma_load_3d(sb + p.off_B + at[q] * T::kBBytes + j * 128, &p.tmB32, bar + kXFull + 8 * at[q],
                                 kq[q] * BK, n0 + j, 0);
             }
@@ -259,6 +266,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
           if (!wt.wait(bar + kXEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
             ok = false;
             break;
+          }
+          if (skip) {
+            skip = false;
+            skipped = fills;
+            next_stage();
+            continue;
           }
           // odd tiles walk K backwards: a wave starts on what the last one left in L2
           const int kx = (t.kb0 + ((i & 1) ? nk - 1 - kb : kb)) * BK;
@@ -291,11 +304,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             for (int j = 0; j < T::kBAtoms; ++j)
               if (64 * j < t.width / CG) load(sbb + j * 8192, mB, n0 + 64 * j, ky);
           }
-          ++fills;
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          next_stage();
         }
       }
       if (ok) {
@@ -312,7 +321,8 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
       }
       if (!ok && rank == 0) {
         for (int f = max(fills - p.stages, 0); f < fills; ++f)
-          wt.drain(bar + kXFull + 8 * (f % p.stages), static_cast<uint32_t>(f / p.stages) & 1u);
+          if (f != skipped)
+            wt.drain(bar + kXFull + 8 * (f % p.stages), static_cast<uint32_t>(f / p.stages) & 1u);
       }
     }
   } else if (warp == 1) {

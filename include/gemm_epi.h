@@ -441,7 +441,7 @@ typedef struct {
   int32_t max_ctas;     /* 0 = one CTA per SM, else a cap on the products' grids   */
   float logit_scale;    /* 0 = 1                                                   */
   float z_loss;         /* weight of lse^2; 0 = none                               */
-  int32_t reserved;     /* 0                                                       */
+  uint32_t debug_flags; /* 0; GE_DEBUG_SKIP_FIRST_LOAD for tests only              */
   int64_t ldh, ldw;     /* row pitches in elements; 0 = D                          */
   int64_t lddh, lddw;
   int64_t buffer_bytes; /* 0 = 512 MiB; at least 256 columns of all T rows   */

@@ -319,6 +319,21 @@ def test_long_rows_of_offsets_past_32_bits():
     B.gemm_epi_xent_plan_destroy(plan)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [20, 300])
+def test_a_load_that_never_comes_is_reported(T):
+    """The first k-block of every product is left out: its wait runs out after 20 ms and the run ends by itself."""
+    c = Case(T, 600, 128, seed=12)
+    plan, desc = c.plan, B.make_xent_desc("bf16", timeout_ms=20, debug_flags=B.GE_DEBUG_SKIP_FIRST_LOAD)
+    c.plan = B.gemm_epi_xent_plan_create(T, 600, 128, desc)
+    c.step()
+    torch.cuda.synchronize()
+    assert B.gemm_epi_last_error() == B.GE_ERR_TIMEOUT
+    B.gemm_epi_xent_plan_destroy(c.plan)
+    c.plan = plan
+    c.check(c.step())
+
+
 def test_gradient_formula_against_differences():
     gen = torch.Generator().manual_seed(2)
     T, V, D = 5, 11, 7
@@ -349,7 +364,8 @@ def _create(T=4, V=8, D=8, **kw):
     (dict(ab="f32"), "UNSUPPORTED"), (dict(index=2), "UNSUPPORTED"), (dict(T=0), "SHAPE"), (dict(V=0), "SHAPE"), (dict(D=-1), "SHAPE"),
     (dict(T=1 << 31), "SHAPE"), (dict(ldh=7), "SHAPE"), (dict(D=9), "MISALIGNED"), (dict(ldw=12), "MISALIGNED"),
     (dict(reduction=2), "INVALID"), (dict(timeout_ms=-1), "INVALID"), (dict(logit_scale=float("nan")), "INVALID"),
-    (dict(z_loss=float("inf")), "INVALID"), (dict(buffer_bytes=-1), "INVALID"), (dict(max_ctas=-2), "INVALID")], ids=str)
+    (dict(z_loss=float("inf")), "INVALID"), (dict(buffer_bytes=-1), "INVALID"), (dict(max_ctas=-2), "INVALID"),
+    (dict(debug_flags=2), "INVALID")], ids=str)
 def test_plan_refusals(kw, status):
     with pytest.raises(B.GemmEpiError) as e:
         _create(**kw)
