@@ -541,7 +541,7 @@ struct gemm_epi_xent_plan {
   Product stats, keep, dlogit, out, part;
   int64_t piece = 0;    // vocabulary columns of a piece, a multiple of 256
   int slices = 1;       // of dH's sum over a piece, at most
-  bool pack = true;     // a loss alone packs its rows too
+  bool pack_loss = true, pack_step = true;  // rows that take part are packed first
   int row_lanes = 32, finish_grid = 1;
   int64_t ldc = 0, Dp = 0;
   int64_t band = 0;     // columns of a CTA's band in the logits' product, 0: tiles
@@ -574,7 +574,7 @@ Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {
   w.coef = take(8 * T);
   w.block_sums = take(16 * static_cast<size_t>(pl->finish_grid));
   w.stats = take(8 * T * static_cast<size_t>(slots_of(pl)));
-  if (grads || pl->pack) w.Hc = take(2 * T * static_cast<size_t>(pl->ldc));
+  if (grads || pl->pack_loss) w.Hc = take(2 * T * static_cast<size_t>(pl->ldc));
   if (grads) {
     w.dl = take(2 * T * static_cast<size_t>(pl->piece));
     w.part = take(4 * T * static_cast<size_t>(pl->Dp) * static_cast<size_t>(pl->slices));
@@ -613,17 +613,28 @@ int units_of(const gemm_epi_xent_plan *pl, const Product &pr) {
 int64_t tiles_of(const Product &pr, int64_t M, int64_t N) { return ceil_div(M, 128 * pr.cg) * ceil_div(N, pr.bn); }
 
 int configure(gemm_epi_xent_plan *pl) {
-  // A batch of at most 128 rows fills one 128-row tile; longer ones use CTA pairs.
-  const int cg = pl->T <= 128 || (pl->d.max_ctas && pl->d.max_ctas < 2) ? 1 : 2;
-  const int cg_out = pl->d.max_ctas && pl->d.max_ctas < 2 ? 1 : 2;
+  // Tiles: 256 x 256 on CTA pairs, or 128 x 128 on single CTAs where a batch fills no more
+  // rows than that or the whole product is at most one tile for every SM, which
+  // is then bound by its start and its end (256 x 8000 x 1024: a loss 17.2 us against
+  // 18.8 on pairs, a step 57.3 against 60.1).
+  const int sms = pl->d.max_ctas ? std::min(pl->d.max_ctas, pl->sms) : pl->sms;
+  auto single = [&](int64_t M, int64_t N) { return ceil_div(M, 128) * ceil_div(N, 128) <= sms; };
+  const int cg = sms < 2 || pl->T <= 128 || single(pl->T, pl->V) ? 1 : 2;
+  // The gradients' products too, up to 10^10 operations (about 6 us of the GPU): 200 x 4000 x 512
+  // in 37.6 us against 43.6, 1500 x 1000 x 2048 in 64.3 against 66.1.
+  const bool light = 2.0 * double(pl->T) * double(pl->V) * double(pl->D) <= 1e10;
+  const int cg_out = sms < 2 || (light && single(pl->V, pl->D)) ? 1 : 2;
+  const int cg_part = sms < 2 || pl->T <= 128 || (light && single(pl->T, pl->D)) ? 1 : 2;
   int st = make_product(pl, &pl->stats, X_STATS, cg, 0);
   if (st == GE_OK) st = make_product(pl, &pl->keep, X_KEEP, cg, 0);
   if (st == GE_OK) st = make_product(pl, &pl->dlogit, X_DLOGIT, cg, 0);
   if (st == GE_OK) st = make_product(pl, &pl->out, X_OUT, cg_out, 0);
-  if (st == GE_OK) st = make_product(pl, &pl->part, X_PART, cg, kXentBoxes);
+  if (st == GE_OK) st = make_product(pl, &pl->part, X_PART, cg_part, kXentBoxes);
   if (st != GE_OK) return st;
   pl->pairs = pl->sms / 2;
-  if (cg_out == 2) {
+  if (cudaFuncSetAttribute(xent_kernel_cg2(X_OUT), cudaFuncAttributeMaxDynamicSharedMemorySize, pl->smem) != cudaSuccess)
+    return GE_ERR_CUDA;
+  if (sms >= 2) {
     int clusters = 0;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -635,7 +646,7 @@ int configure(gemm_epi_xent_plan *pl) {
     cfg.dynamicSmemBytes = static_cast<size_t>(pl->smem);
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&clusters, pl->out.fn, &cfg) == cudaSuccess && clusters > 0)
+    if (cudaOccupancyMaxActiveClusters(&clusters, xent_kernel_cg2(X_OUT), &cfg) == cudaSuccess && clusters > 0)
       pl->pairs = std::min(pl->pairs, clusters);
     cudaGetLastError();
   }
@@ -643,8 +654,12 @@ int configure(gemm_epi_xent_plan *pl) {
   // rows as the next (to 32) where whole tiles would leave CTAs idle at the end (32000 rows:
   // 224 to a CTA instead of one or two tiles of 128).
   pl->band = cg == 1 && pl->T <= 128 ? 32 * ceil_div(ceil_div(pl->V, 32), units_of(pl, pl->stats)) : 0;
-  // Rows are packed for a loss alone only where that can save a tile of them.
-  pl->pack = pl->T > 128 * cg;
+  // Packing costs a launch (4 to 5 us) and saves the products of ignored rows: it is left
+  // out where a batch fills one tile anyway and where the logits' product takes less than
+  // about 20 us.  (A step without it needs a block of finish for every row.)
+  const bool small = pl->T <= 128 || 2.0 * double(pl->T) * double(pl->V) * double(pl->D) < 3e10;
+  pl->pack_loss = !small;
+  pl->pack_step = !small || pl->T > 2 * pl->sms;
   // pieces of the vocabulary: as wide as the buffer allows, equal, whole tiles
   const int64_t bound = pl->d.buffer_bytes ? pl->d.buffer_bytes : int64_t(1) << 29;
   const int64_t widest = std::max<int64_t>(256, bound / (2 * pl->T) / 256 * 256);
@@ -741,7 +756,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
   void *dl = ws + at.dl;
   float *part = reinterpret_cast<float *>(ws + at.part);
   const uint64_t piece = static_cast<uint64_t>(pl->piece);
-  const bool pack = pl->pack;
+  const bool pack = grads ? pl->pack_step : pl->pack_loss;
   const int i32 = pl->d.index == GE_INDEX_I32;
   const SplitParams split = {128 * pl->part.cg, pl->part.bn, static_cast<int32_t>(ceil_div(D, pl->part.bn)),
                              static_cast<int32_t>(ceil_div(std::min(pl->piece, V), BK)), units_of(pl, pl->part),
