@@ -359,9 +359,10 @@ struct ConvertParams {
   float c2, c;               // logit_scale log2(e), logit_scale
 };
 
-// Kept distances to dl, in place: a warp per row of 256 columns, 16 bytes per lane, four rows
-// ahead.  Bound by memory: 4 bytes and one exponential per logit.
-constexpr int kConvertRows = 32;  // rows of a CTA (8 warps, 4 rows each)
+// Kept distances to dl, in place: a warp per row of 512 columns, two times 16 bytes per
+// lane, two rows ahead.  Bound by memory: 4 bytes and one exponential per logit.
+constexpr int kConvertRows = 16;   // rows of a CTA (8 warps, 2 rows each)
+constexpr int kConvertCols = 512;
 __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant__ ConvertParams p) {
   griddep_wait();
   griddep_launch_dependents();
@@ -370,61 +371,78 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // last columns first: the product wrote them last, and what is left in L2 for
   // the next product is what that reads first
-  const int c0 = (gridDim.y - 1 - blockIdx.y) * 256 + lane * 8;
-  const int of_band = p.band ? c0 % p.band : c0;
-  const int slot = 2 * ((p.band ? c0 / p.band * p.band_tiles : 0) + of_band / p.bn) + ((of_band / 64) & 1);
-  const float ds = p.sc->dl_scale;
-  for (int first = blockIdx.x * kConvertRows; first < end; first += gridDim.x * kConvertRows) {
-    uint4 w[4];
-    float shift[4], lse2[4];
-    float2 coef[4];
-    int target[4];
+  const int c0 = (gridDim.y - 1 - blockIdx.y) * kConvertCols + lane * 8;
+  int64_t slot[2];
+  bool there[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = first + warp + 8 * i;
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
-      shift[i] = lse2[i] = 0.f;
-      coef[i] = make_float2(0.f, 0.f);
+  for (int h = 0; h < 2; ++h) {
+    const int c = c0 + 256 * h, of_band = p.band ? c % p.band : c;
+    slot[h] = int64_t(2 * ((p.band ? c / p.band * p.band_tiles : 0) + of_band / p.bn) + ((of_band / 64) & 1)) * p.T;
+    there[h] = c < (p.N + 255) / 256 * 256;
+  }
+  const float ds = p.sc->dl_scale;
+  for (int first = blockIdx.x * kConvertRows + warp; first < end; first += gridDim.x * kConvertRows) {
+    uint4 w[2][2];
+    float top[2][2], lse2[2];
+    float2 coef[2];
+    int target[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = first + 8 * i;
       target[i] = -1;
+      lse2[i] = 0.f;
+      coef[i] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        w[i][h] = make_uint4(0u, 0u, 0u, 0u);
+        top[i][h] = 0.f;
+      }
       if (r < rows) {
-        w[i] = *reinterpret_cast<const uint4 *>(p.buf + r * p.pitch + c0);
-        const float top = p.stats[int64_t(slot) * p.T + r].x;
+        const uint16_t *row = p.buf + r * p.pitch + c0;
+        w[i][0] = *reinterpret_cast<const uint4 *>(row);
+        if (there[1]) w[i][1] = *reinterpret_cast<const uint4 *>(row + 256);
+        top[i][0] = p.stats[slot[0] + r].x;
+        if (there[1]) top[i][1] = p.stats[slot[1] + r].x;
         lse2[i] = p.lse2[r];
-        shift[i] = (top == -INFINITY ? 0.f : top) - lse2[i];
         coef[i] = p.coef[r];
         target[i] = p.gathered[r];
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = first + warp + 8 * i;
+    for (int i = 0; i < 2; ++i) {
+      const int r = first + 8 * i;
       if (r >= end) continue;
       const bool live = target[i] >= 0;
-      target[i] -= c0;
-      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       const float f = coef[i].x * ds;
-      float d[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        // the code in the low bits of a float of 2^23
-        const float code = __uint_as_float(__byte_perm(u[e / 2], 0x4b000000u, e & 1 ? 0x7432 : 0x7410)) - 8388608.f;
-        d[e] = ex2(fmaf(code, -1.f / (1 << kKeptBits), shift[i])) * f;
-      }
-      if (live && target[i] >= 0 && target[i] < 8) {
-        // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p
-        const float at = p.at_target[r] * (p.c2 / p.c);
-        const float v = ex2(at - lse2[i]) * f - coef[i].y * ds;
+      for (int h = 0; h < 2; ++h) {
+        if (!there[h]) continue;
+        const int c = c0 + 256 * h, at = target[i] - c;
+        const uint32_t u[4] = {w[i][h].x, w[i][h].y, w[i][h].z, w[i][h].w};
+        const float shift = (top[i][h] == -INFINITY ? 0.f : top[i][h]) - lse2[i];
+        float d[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e == target[i]) d[e] = v;
-      }
-      if (!live || c0 + 8 > p.N) {
+        for (int e = 0; e < 8; ++e) {
+          // the code in the low bits of a float of 2^23
+          const float code = __uint_as_float(__byte_perm(u[e / 2], 0x4b000000u, e & 1 ? 0x7432 : 0x7410)) - 8388608.f;
+          d[e] = ex2(fmaf(code, -1.f / (1 << kKeptBits), shift)) * f;
+        }
+        if (live && at >= 0 && at < 8) {
+          // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p
+          const float v = ex2(p.at_target[r] * (p.c2 / p.c) - lse2[i]) * f - coef[i].y * ds;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!live || c0 + e >= p.N) d[e] = 0.f;
+          for (int e = 0; e < 8; ++e)
+            if (e == at) d[e] = v;
+        }
+        if (!live || c + 8 > p.N) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (!live || c + e >= p.N) d[e] = 0.f;
+        }
+        *reinterpret_cast<uint4 *>(p.buf + r * p.pitch + c) =
+            make_uint4(pack16(true, d[0], d[1]), pack16(true, d[2], d[3]), pack16(true, d[4], d[5]),
+                       pack16(true, d[6], d[7]));
       }
-      *reinterpret_cast<uint4 *>(p.buf + r * p.pitch + c0) =
-          make_uint4(pack16(true, d[0], d[1]), pack16(true, d[2], d[3]), pack16(true, d[4], d[5]), pack16(true, d[6], d[7]));
     }
   }
 }
@@ -872,7 +890,7 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       cp.band_tiles = sl.band_tiles;
       cp.c2 = sl.c2;
       cp.c = sl.c;
-      const unsigned cols = static_cast<unsigned>(ceil_div(n, 256));
+      const unsigned cols = static_cast<unsigned>(ceil_div(n, kConvertCols));
       const unsigned rows = static_cast<unsigned>(
           std::max<int64_t>(1, std::min<int64_t>(ceil_div(T, kConvertRows), ceil_div(16 * pl->sms, cols))));
       if (!go(launch(reinterpret_cast<const void *>(xent_convert_kernel), dim3(rows, cols), 256, 0, 1, &cp, s)))
