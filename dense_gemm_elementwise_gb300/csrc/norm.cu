@@ -90,7 +90,11 @@ __global__ void __launch_bounds__(kSumQuads *kSumLanes) norm_sum_kernel(const __
 
 enum NormPass { PASS_RUN = 0, PASS_GRAD = 1, PASS_GRAD_WHOLE = 2 };
 
-const void *pick_kernel(int dt, int nv, int threads, bool vec, int pass) {
+const void *pick_kernel(int dt, int nv, int threads, bool vec, bool even, int pass) {
+  if (!vec && even)
+    return pass == PASS_RUN    ? norm_kernel_run_pairs(dt, nv, threads)
+           : pass == PASS_GRAD ? norm_kernel_grad_pairs(dt, nv, threads)
+                               : norm_kernel_grad_whole_pairs(dt, nv, threads);
   return pass == PASS_RUN    ? norm_kernel_run(dt, nv, threads, vec)
          : pass == PASS_GRAD ? norm_kernel_grad(dt, nv, threads, vec)
                              : norm_kernel_grad_whole(dt, nv, threads, vec);
@@ -127,7 +131,7 @@ struct gemm_epi_norm_plan {
   int64_t T = 0, D = 0;
   ge_norm_desc d{};
   int sms = 0;
-  bool vec = false;
+  bool vec = false, even = false;
   RowShape fwd, bwd;
   NormParams p{};
 };
@@ -160,7 +164,7 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
   if (r.row_threads < 32) cta_rows = round_up(cta_rows, 32 / r.row_threads);
   r.threads = r.row_threads * static_cast<int>(cta_rows);
   const int rows = r.threads / r.row_threads;
-  r.fn = pick_kernel(pl->d.x, r.nv, r.threads, vec, pass);
+  r.fn = pick_kernel(pl->d.x, r.nv, r.threads, vec, pl->even, pass);
   // shared memory: sums, factors in fp32, and as many rows of the ring as let two CTAs
   // (three of the forward pass) share an SM, one at least: 512 threads' fp32 rows and
   // factors take 224 KiB
@@ -259,7 +263,11 @@ int gemm_epi_norm_plan_create(gemm_epi_norm_plan **plan, int64_t T, int64_t D, c
   pl->d = d;
   const int64_t es = size_of(d.x);
   pl->vec = true;
-  for (int64_t ld : {d.ldx, d.ldb, d.ldy, d.ldh}) pl->vec = pl->vec && (ld * es) % 16 == 0;
+  pl->even = D % 2 == 0;
+  for (int64_t ld : {d.ldx, d.ldb, d.ldy, d.ldh}) {
+    pl->vec = pl->vec && (ld * es) % 16 == 0;
+    pl->even = pl->even && ld % 2 == 0;
+  }
   int dev = 0, smem = 0;
   int st = current_device(&dev, &pl->sms, &smem);
   if (st == GE_OK) st = shape_of(pl, PASS_RUN, smem, &pl->fwd);

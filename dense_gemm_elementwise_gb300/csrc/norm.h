@@ -41,5 +41,9 @@ struct NormParams {
 const void *norm_kernel_run(int dt, int nv, int threads, bool vec);
 const void *norm_kernel_grad(int dt, int nv, int threads, bool vec);
 const void *norm_kernel_grad_whole(int dt, int nv, int threads, bool vec);  // units hold whole gate groups
+// rows of other units whose width and pitch are even
+const void *norm_kernel_run_pairs(int dt, int nv, int threads);
+const void *norm_kernel_grad_pairs(int dt, int nv, int threads);
+const void *norm_kernel_grad_whole_pairs(int dt, int nv, int threads);
 
 }  // namespace ge

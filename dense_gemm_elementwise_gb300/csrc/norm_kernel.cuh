@@ -27,6 +27,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "gemm_epi.h"
 #include "norm.h"
 #include "ptx.cuh"
@@ -94,13 +96,16 @@ constexpr int kPairs = kChunk / 2;
 //   P_STRIDED  other rows: every row_threads-th column, so that the threads of a
 //              warp read neighbouring elements (8 in a run would have each load
 //              touch four times the cache lines)
-enum Path { P_RING = 0, P_DIRECT = 1, P_STRIDED = 2 };
+//   P_PAIRS    the same, two columns at a time, where rows and widths are even
+enum Path { P_RING = 0, P_DIRECT = 1, P_STRIDED = 2, P_PAIRS = 3 };
 
 template <int PATH>
 struct Columns {
   int t, per;
   __device__ __forceinline__ int operator()(int k, int i) const {
-    return PATH == P_STRIDED ? (k * kChunk + i) * per + t : (t + k * per) * kChunk + i;
+    return PATH == P_PAIRS     ? 2 * ((k * kPairs + i / 2) * per + t) + (i & 1)
+           : PATH == P_STRIDED ? (k * kChunk + i) * per + t
+                               : (t + k * per) * kChunk + i;
   }
 };
 
@@ -111,7 +116,14 @@ __device__ __forceinline__ void store_row(typename Elem<DT>::T *row, const Colum
   using E = Elem<DT>;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    if (PATH != P_STRIDED && col(k, 0) + kChunk <= D) {
+    if constexpr (PATH == P_PAIRS) {
+#pragma unroll
+      for (int j = 0; j < kPairs; ++j) {
+        if (col(k, 2 * j) >= D) continue;  // D is even
+        if constexpr (DT == GE_F32) *reinterpret_cast<float2 *>(row + col(k, 2 * j)) = v[k][j];
+        else *reinterpret_cast<uint32_t *>(row + col(k, 2 * j)) = E::put2(v[k][j]);
+      }
+    } else if (PATH < P_STRIDED && col(k, 0) + kChunk <= D) {
       uint4 *q = reinterpret_cast<uint4 *>(row + col(k, 0));
       if constexpr (DT == GE_F32) {
 #pragma unroll
@@ -208,7 +220,7 @@ struct Own {
     if (!v) {
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) f[i] = 1.f;
-    } else if (PATH != P_STRIDED && WT != GE_F32 && p.w_vec && col(k, 0) < p.D) {
+    } else if (PATH < P_STRIDED && WT != GE_F32 && p.w_vec && col(k, 0) < p.D) {
       union { uint4 w; T e[kChunk]; } u;
       u.w = *reinterpret_cast<const uint4 *>(q + col(k, 0));
 #pragma unroll
@@ -244,7 +256,7 @@ struct Ring {
   uint4 *base;
   int threads, ahead, D;
   Columns<PATH> col;
-  static constexpr bool kRaw = PATH == P_STRIDED && kEarly;
+  static constexpr bool kRaw = PATH >= P_STRIDED && kEarly;
   T raw[kRaw ? NA : 1][kRaw ? NV : 1][kChunk];
 
   __device__ __forceinline__ Ring(uint4 *base_, int threads_, int ahead_, int D_, const Columns<PATH> &col_)
@@ -270,7 +282,19 @@ struct Ring {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) raw[a][k][i] = row[min(col(k, i), D - 1)];
+        for (int i = 0; i < (PATH == P_PAIRS ? kPairs : kChunk); ++i) take(row, k, i, raw[a][k]);
+    }
+  }
+  // element i of chunk k, or its pair i, from a row at least D long
+  __device__ __forceinline__ void take(const T *row, int k, int i, T (&e)[kChunk]) const {
+    if constexpr (PATH == P_PAIRS) {
+      using Two = typename std::conditional<sizeof(T) == 4, uint2, uint32_t>::type;
+      union { Two w; T e[2]; } u;
+      u.w = *reinterpret_cast<const Two *>(row + min(col(k, 2 * i), D - 2));
+      e[2 * i] = u.e[0];
+      e[2 * i + 1] = u.e[1];
+    } else {
+      e[i] = row[min(col(k, i), D - 1)];
     }
   }
   __device__ __forceinline__ void commit() const {
@@ -322,10 +346,12 @@ struct Ring {
         }
       } else {
         T e[kChunk];
+        if constexpr (kRaw) {
 #pragma unroll
-        for (int i = 0; i < kChunk; ++i) {
-          if constexpr (kRaw) e[i] = raw[a][k][i];
-          else e[i] = row[on ? min(col(k, i), D - 1) : 0];
+          for (int i = 0; i < kChunk; ++i) e[i] = raw[a][k][i];
+        } else {
+#pragma unroll
+          for (int i = 0; i < (PATH == P_PAIRS ? kPairs : kChunk); ++i) take(row, k, i, e);
         }
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
@@ -502,7 +528,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
         own_post.fill<NV>(p, col, p.alpha, p.gate, int64_t(at) * p.D, p.w_post);
       }
     };
-    if (PATH != P_STRIDED && b) factors();
+    if (PATH < P_STRIDED && b) factors();
     ring.wait();
     float2 v[NV][kPairs];
     if (!kAsk || !b) ring.get(slot, 0, x + (on ? row : 0) * p.ldx, on, v);
@@ -510,7 +536,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
       float2 u[NV][kPairs];
       ring.get(slot, 1, b + (on ? row : 0) * p.ldb, on, u);
       if (!kAsk) fetch(0);
-      if (PATH == P_STRIDED) factors();
+      if (PATH >= P_STRIDED) factors();
       const float r = p.post != GE_NORM_NONE
                           ? divisor(u, p.post, p.eps_post, p.inv_d, p.D, col, row_sum) : 1.f;
       own_post.times(u);
@@ -614,7 +640,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
         own_post.fill<NV>(p, col, kWhole ? 1.f : p.alpha, p.gate, int64_t(at) * p.D, kWhole ? nullptr : p.w_post);
       }
     };
-    if (PATH != P_STRIDED && b) factors();
+    if (PATH < P_STRIDED && b) factors();
     ring.wait();
     // y becomes what N_pre divides, d = dh w_pre, q = dh y
     float2 y[NV][kPairs], d[NV][kPairs], q[NV][kPairs];
@@ -684,7 +710,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
     if (on) store_row<DT, NV, PATH>(dx + row * p.ldx, col, p.D, d);
     if (!b) continue;
     // y is now b, or what N_post divides
-    if (PATH == P_STRIDED) factors();
+    if (PATH >= P_STRIDED) factors();
     if (layer_b) {
       float m[1] = {sum_of(y)};
       row_sum(m);
