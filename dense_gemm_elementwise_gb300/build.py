@@ -19,7 +19,8 @@ LIBDIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIBDIR, "libgemm_epi.so")
 UNITS = ["plan", "unfused", "jit", "k_cg1_n64", "k_cg1_n128", "k_cg1_n256", "k_cg2_n128", "k_cg2_n256",
          "norm", "k_norm_run", "k_norm_grad", "k_norm_grad_whole",
-         "k_norm_run_pairs", "k_norm_grad_pairs", "k_norm_grad_whole_pairs", "xent", "k_xent_cg1", "k_xent_cg2"]
+         "k_norm_run_small", "k_norm_grad_small", "k_norm_grad_whole_small", "k_norm_run_odd", "k_norm_grad_odd",
+         "k_norm_grad_whole_odd", "xent", "k_xent_cg1", "k_xent_cg2"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

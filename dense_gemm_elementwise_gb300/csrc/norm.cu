@@ -90,14 +90,18 @@ __global__ void __launch_bounds__(kSumQuads *kSumLanes) norm_sum_kernel(const __
 
 enum NormPass { PASS_RUN = 0, PASS_GRAD = 1, PASS_GRAD_WHOLE = 2 };
 
-const void *pick_kernel(int dt, int nv, int threads, bool vec, bool even, int pass) {
-  if (!vec && even)
-    return pass == PASS_RUN    ? norm_kernel_run_pairs(dt, nv, threads)
-           : pass == PASS_GRAD ? norm_kernel_grad_pairs(dt, nv, threads)
-                               : norm_kernel_grad_whole_pairs(dt, nv, threads);
-  return pass == PASS_RUN    ? norm_kernel_run(dt, nv, threads, vec)
-         : pass == PASS_GRAD ? norm_kernel_grad(dt, nv, threads, vec)
-                             : norm_kernel_grad_whole(dt, nv, threads, vec);
+const void *pick_kernel(int dt, int nv, int threads, int rows, bool even, int pass) {
+  if (rows == ROWS_16)
+    return pass == PASS_RUN    ? norm_kernel_run(dt, nv)
+           : pass == PASS_GRAD ? norm_kernel_grad(dt, nv)
+                               : norm_kernel_grad_whole(dt, nv);
+  if (rows == ROWS_SMALL)
+    return pass == PASS_RUN    ? norm_kernel_run_small(dt, nv, threads, even)
+           : pass == PASS_GRAD ? norm_kernel_grad_small(dt, nv, threads, even)
+                               : norm_kernel_grad_whole_small(dt, nv, threads, even);
+  return pass == PASS_RUN    ? norm_kernel_run_odd(dt, nv, threads)
+         : pass == PASS_GRAD ? norm_kernel_grad_odd(dt, nv, threads)
+                             : norm_kernel_grad_whole_odd(dt, nv, threads);
 }
 
 bool valid_type(int t) { return t == GE_F16 || t == GE_BF16 || t == GE_F32; }
@@ -145,12 +149,17 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
   // Rows of whole 16-byte units: two chunks per thread spread the cost of the row's sums (shuffles, a
   // barrier) over 16 columns, but rows too few to fill the GPU, and rows of
   // up to a warp's chunks, take one; what 512 threads cannot hold so takes four.
-  // Rows of other units: one up to 1024 threads, since each element has a register
+  // Rows moved 4 or 8 bytes at a time: two in CTAs of over 512 columns' chunks only (with two,
+  // the gradients of 8000 x 2050 fp32 take 193 us, not 107), and above 1024 chunks CTAs of up to
+  // 1024 threads (500 x 12346 bf16 30 us and 86, with four chunks 33 and 97).
+  // Odd rows of 16-bit elements: one up to 1024 threads, since each element has a register
   // of its own on its way.
-  const bool vec = pl->vec;
+  const int rows_by = pl->vec ? ROWS_16 : pl->even || pl->d.x == GE_F32 ? ROWS_SMALL : ROWS_ODD;
   const int64_t few = 4 * int64_t(pl->sms);
-  if (vec) r.nv = chunks <= 32 || (pl->T <= few && chunks <= kVecThreads) ? 1 : (chunks <= 2 * kVecThreads ? 2 : 4);
-  else r.nv = chunks <= kMaxThreads ? 1 : 2;
+  if (rows_by == ROWS_16)
+    r.nv = chunks <= 32 || (pl->T <= few && chunks <= kVecThreads) ? 1 : (chunks <= 2 * kVecThreads ? 2 : 4);
+  else
+    r.nv = chunks <= (rows_by == ROWS_SMALL ? kVecThreads : kMaxThreads) ? 1 : 2;
   const int want = static_cast<int>(ceil_div(chunks, r.nv));
   r.row_threads = static_cast<int>(round_up(want, 32));
   if (want < 32) {  // rows share warps
@@ -164,7 +173,7 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
   if (r.row_threads < 32) cta_rows = round_up(cta_rows, 32 / r.row_threads);
   r.threads = r.row_threads * static_cast<int>(cta_rows);
   const int rows = r.threads / r.row_threads;
-  r.fn = pick_kernel(pl->d.x, r.nv, r.threads, vec, pl->even, pass);
+  r.fn = pick_kernel(pl->d.x, r.nv, r.threads, rows_by, pl->even, pass);
   // shared memory: sums, factors in fp32, and as many rows of the ring as let two CTAs
   // (three of the forward pass) share an SM, one at least: 512 threads' fp32 rows and
   // factors take 224 KiB
@@ -172,7 +181,7 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
   const int per_row = r.threads * r.nv * tensors * static_cast<int>(size_of(pl->d.x)) * kChunk;
   r.ahead = 1;
   r.smem = fixed;
-  if (vec && r.nv < 4) {
+  if ((rows_by == ROWS_16 && r.nv < 4) || (rows_by == ROWS_SMALL && r.threads <= kVecThreads)) {
     const int room = max_smem / std::max(1, std::min(pass == PASS_RUN ? 3 : 2, 768 / r.threads));
     while (r.ahead < kMaxAhead && fixed + (r.ahead + 1) * per_row <= room) ++r.ahead;
     r.smem = fixed + r.ahead * per_row;

@@ -6,8 +6,8 @@
 namespace ge {
 
 constexpr int kChunk = 8;        // columns a thread holds per chunk
-constexpr int kVecThreads = 512;   // threads of a CTA whose rows are whole 16-byte units, at most
-constexpr int kMaxThreads = 1024;  // ... of other rows
+constexpr int kVecThreads = 512;   // threads of a CTA, at most
+constexpr int kMaxThreads = 1024;  // ... with other rows than of whole 16-byte units
 // The forward pass is held to the registers of a CTA of 768 (85), so that three CTAs of 256 share
 // an SM: 8192 x 4096 bf16 in 47.0 us against 48.9 with two.  The gradients keep 128
 // (222 us against 306 for 16384 x 4096, whose sums then spill).
@@ -36,14 +36,20 @@ struct NormParams {
   int32_t units_per_group;  // 0: a lane holds whole groups
 };
 
-// nv chunks per thread; threads of a CTA; vec: rows are whole 16-byte units (nv 1 and 2
-// with a ring, 4 without; else 1 or 2)
-const void *norm_kernel_run(int dt, int nv, int threads, bool vec);
-const void *norm_kernel_grad(int dt, int nv, int threads, bool vec);
-const void *norm_kernel_grad_whole(int dt, int nv, int threads, bool vec);  // units hold whole gate groups
-// rows of other units whose width and pitch are even
-const void *norm_kernel_run_pairs(int dt, int nv, int threads);
-const void *norm_kernel_grad_pairs(int dt, int nv, int threads);
-const void *norm_kernel_grad_whole_pairs(int dt, int nv, int threads);
+// Kernels, by how rows are moved; nv chunks per thread (1 or 2; whole units also 4), `threads` of a CTA.
+enum NormRows {
+  ROWS_16 = 0,     // whole 16-byte units (nv 1, 2, 4)
+  ROWS_SMALL = 1,  // even rows, or odd rows of fp32 (`even` says which): 4 or 8 bytes at a time
+  ROWS_ODD = 2,    // odd rows of 16-bit elements, one by one
+};
+const void *norm_kernel_run(int dt, int nv);
+const void *norm_kernel_grad(int dt, int nv);
+const void *norm_kernel_grad_whole(int dt, int nv);  // units hold whole gate groups
+const void *norm_kernel_run_small(int dt, int nv, int threads, bool even);
+const void *norm_kernel_grad_small(int dt, int nv, int threads, bool even);
+const void *norm_kernel_grad_whole_small(int dt, int nv, int threads, bool even);
+const void *norm_kernel_run_odd(int dt, int nv, int threads);
+const void *norm_kernel_grad_odd(int dt, int nv, int threads);
+const void *norm_kernel_grad_whole_odd(int dt, int nv, int threads);
 
 }  // namespace ge

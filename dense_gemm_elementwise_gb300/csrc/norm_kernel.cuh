@@ -95,8 +95,9 @@ constexpr int kPairs = kChunk / 2;
 //              (each thread then has 8 or 16 loads in flight)
 //   P_STRIDED  other rows: every row_threads-th column, so that the threads of a
 //              warp read neighbouring elements (8 in a run would have each load
-//              touch four times the cache lines)
-//   P_PAIRS    the same, two columns at a time, where rows and widths are even
+//              touch four times the cache lines); fp32 through the ring
+//   P_PAIRS    the same, two columns at a time and through the ring, where rows
+//              and widths are even
 enum Path { P_RING = 0, P_DIRECT = 1, P_STRIDED = 2, P_PAIRS = 3 };
 
 template <int PATH>
@@ -244,27 +245,55 @@ struct Own {
   }
 };
 
-// Rows on their way from memory: NA tensors of them.  P_RING: `ahead` rows, by cp.async
-// into the thread's own words of shared memory.  P_STRIDED: the next row's
-// elements in registers, asked for once the current row's have been taken (kEarly; CTAs of over 512
-// threads have no registers for that and read a row when it is wanted).
-template <int DT, int NV, int PATH, int NA, bool kEarly>
+// Whether rows come through a ring in shared memory: copies of 16 bytes, or of one
+// or two elements of 4 or 8 bytes in all (with two columns per load into registers instead,
+// 13390 x 4594 bf16 took 268 us and its gradients 514, against 179 and 440).
+// kBound: threads that the registers must suffice for; 1024 threads' rows do not
+// fit in shared memory.
+template <int DT, int PATH, int kBound>
+constexpr bool kBySmall = (PATH == P_PAIRS || (PATH == P_STRIDED && DT == GE_F32)) && kBound < kMaxThreads;
+template <int DT, int PATH, int kBound>
+constexpr bool kByRing = PATH == P_RING || kBySmall<DT, PATH, kBound>;
+
+// Rows on their way from memory: NA tensors of them, `ahead` rows by cp.async
+// into the thread's own words of shared memory.  Odd rows of 16-bit elements, which
+// cp.async cannot move: the next row's elements in registers, asked for once
+// the current row's have been taken. CTAs of over 512 threads have neither room nor
+// registers and read a row when it is wanted.
+template <int DT, int NV, int PATH, int NA, int kBound>
 struct Ring {
   using T = typename Elem<DT>::T;
   static constexpr int kWords = kChunk * sizeof(T) / 16;  // of one tensor's chunk
   static constexpr int kRow = NA * NV * kWords;           // 16-byte words of a thread per row
+  static constexpr bool kSmall = kBySmall<DT, PATH, kBound>;
+  static constexpr int kUnits = PATH == P_PAIRS ? kPairs : kChunk;  // of a chunk, one copy each
+  static constexpr int kUnit = kChunk / kUnits * sizeof(T);         // bytes of one
   uint4 *base;
   int threads, ahead, D;
   Columns<PATH> col;
-  static constexpr bool kRaw = PATH >= P_STRIDED && kEarly;
+  static constexpr bool kRaw = PATH == P_STRIDED && kBound <= kVecThreads && !kSmall;
   T raw[kRaw ? NA : 1][kRaw ? NV : 1][kChunk];
 
   __device__ __forceinline__ Ring(uint4 *base_, int threads_, int ahead_, int D_, const Columns<PATH> &col_)
       : base(base_), threads(threads_), ahead(ahead_), D(D_), col(col_) {}
 
+  // unit u of this thread (small copies); `base` is its first 16-byte word
+  __device__ __forceinline__ uint8_t *unit(int u) const {
+    return reinterpret_cast<uint8_t *>(base - threadIdx.x) + (u * threads + static_cast<int>(threadIdx.x)) * kUnit;
+  }
   // row: the row's first element
   __device__ __forceinline__ void issue(int slot, int a, const T *row) {
-    if constexpr (PATH == P_RING) {
+    if constexpr (kSmall) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < kUnits; ++j) {
+          // past the end: some column of the row, dropped when it is taken
+          const int c = min(col(k, j * (kChunk / kUnits)), D - kChunk / kUnits);
+          const uint32_t dst = smem_u32(unit(((slot * NA + a) * NV + k) * kUnits + j));
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(row + c), "n"(kUnit) : "memory");
+        }
+    } else if constexpr (PATH == P_RING) {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -282,7 +311,7 @@ struct Ring {
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int i = 0; i < (PATH == P_PAIRS ? kPairs : kChunk); ++i) take(row, k, i, raw[a][k]);
+        for (int i = 0; i < kChunk; ++i) take(row, k, i, raw[a][k]);
     }
   }
   // element i of chunk k, or its pair i, from a row at least D long
@@ -298,11 +327,11 @@ struct Ring {
     }
   }
   __device__ __forceinline__ void commit() const {
-    if constexpr (PATH == P_RING) asm volatile("cp.async.commit_group;" ::: "memory");
+    if constexpr (kByRing<DT, PATH, kBound>) asm volatile("cp.async.commit_group;" ::: "memory");
   }
   // the oldest row of the ring has landed
   __device__ __forceinline__ void wait() const {
-    if constexpr (PATH == P_RING) {
+    if constexpr (kByRing<DT, PATH, kBound>) {
       if (ahead == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
       else if (ahead == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
       else asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -346,7 +375,16 @@ struct Ring {
         }
       } else {
         T e[kChunk];
-        if constexpr (kRaw) {
+        if constexpr (kSmall) {
+#pragma unroll
+          for (int j = 0; j < kUnits; ++j) {
+            using Word = typename std::conditional<kUnit == 8, uint2, uint32_t>::type;
+            union { Word w; T e[kChunk / kUnits]; } u;
+            u.w = *reinterpret_cast<const Word *>(unit(((slot * NA + a) * NV + k) * kUnits + j));
+#pragma unroll
+            for (int i = 0; i < kChunk / kUnits; ++i) e[j * (kChunk / kUnits) + i] = u.e[i];
+          }
+        } else if constexpr (kRaw) {
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) e[i] = raw[a][k][i];
         } else {
@@ -483,7 +521,7 @@ struct Group {
 template <int DT, int NV, int PATH, int kBound>
 __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__ NormParams p) {
   using T = typename Elem<DT>::T;
-  constexpr bool kAsk = PATH == P_RING;  // rows are asked for ahead of the one at hand
+  constexpr bool kAsk = kByRing<DT, PATH, kBound>;  // rows are asked for ahead of the one at hand
   extern __shared__ __align__(16) uint8_t smem[];
   const Place<PATH> pl(p.row_threads);
   const int rows = blockDim.x / pl.per;
@@ -493,7 +531,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
   const int n = blockDim.x;
   // w_pre; alpha gate w_post of the gate group at hand
   const Own own_pre{words, n}, own_post{words + 2 * NV * n, n};
-  Ring<DT, NV, PATH, 2, kBound <= kVecThreads> ring(reinterpret_cast<uint4 *>(words + 4 * NV * n), n, p.ahead, p.D, col);
+  Ring<DT, NV, PATH, 2, kBound> ring(reinterpret_cast<uint4 *>(words + 4 * NV * n), n, p.ahead, p.D, col);
   const int step = gridDim.x * rows;
   int64_t first = int64_t(blockIdx.x) * rows;  // the CTA's first row: every thread's loop is as long
   int64_t row = first + pl.mine;
@@ -528,7 +566,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
         own_post.fill<NV>(p, col, p.alpha, p.gate, int64_t(at) * p.D, p.w_post);
       }
     };
-    if (PATH < P_STRIDED && b) factors();
+    if ((PATH < P_STRIDED || kAsk) && b) factors();
     ring.wait();
     float2 v[NV][kPairs];
     if (!kAsk || !b) ring.get(slot, 0, x + (on ? row : 0) * p.ldx, on, v);
@@ -536,7 +574,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
       float2 u[NV][kPairs];
       ring.get(slot, 1, b + (on ? row : 0) * p.ldb, on, u);
       if (!kAsk) fetch(0);
-      if (PATH >= P_STRIDED) factors();
+      if (PATH >= P_STRIDED && !kAsk) factors();
       const float r = p.post != GE_NORM_NONE
                           ? divisor(u, p.post, p.eps_post, p.inv_d, p.D, col, row_sum) : 1.f;
       own_post.times(u);
@@ -582,7 +620,7 @@ __device__ __forceinline__ void unit_rows(const NormParams &p, int u, int lane, 
 template <int DT, int NV, int PATH, int kBound, bool kWhole>
 __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_constant__ NormParams p) {
   using T = typename Elem<DT>::T;
-  constexpr bool kAsk = PATH == P_RING;
+  constexpr bool kAsk = kByRing<DT, PATH, kBound>;
   extern __shared__ __align__(16) uint8_t smem[];
   const Place<PATH> pl(p.row_threads);
   const Columns<PATH> col = pl.columns();
@@ -592,7 +630,8 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
   // w_pre; alpha gate w_post of the gate group at hand, or (kWhole) its gate and alpha w_post apart
   constexpr int kFactors = kWhole ? 3 : 2;
   const Own own_pre{words, n}, own_post{words + 2 * NV * n, n}, own_w{words + 4 * NV * n, n};
-  Ring<DT, NV, PATH, 4, kBound <= kVecThreads> ring(reinterpret_cast<uint4 *>(words + kFactors * 2 * NV * n), n, p.ahead, p.D, col);
+  Ring<DT, NV, PATH, 4, kBound> ring(
+      reinterpret_cast<uint4 *>(words + kFactors * 2 * NV * n), n, p.ahead, p.D, col);
   int64_t row, end;
   unit_rows(p, blockIdx.x, pl.mine, row, end);
   const T *yin = static_cast<const T *>(p.yin), *dh = static_cast<const T *>(p.dh),
@@ -640,7 +679,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
         own_post.fill<NV>(p, col, kWhole ? 1.f : p.alpha, p.gate, int64_t(at) * p.D, kWhole ? nullptr : p.w_post);
       }
     };
-    if (PATH < P_STRIDED && b) factors();
+    if ((PATH < P_STRIDED || kAsk) && b) factors();
     ring.wait();
     // y becomes what N_pre divides, d = dh w_pre, q = dh y
     float2 y[NV][kPairs], d[NV][kPairs], q[NV][kPairs];
@@ -710,7 +749,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
     if (on) store_row<DT, NV, PATH>(dx + row * p.ldx, col, p.D, d);
     if (!b) continue;
     // y is now b, or what N_post divides
-    if (PATH >= P_STRIDED) factors();
+    if (PATH >= P_STRIDED && !kAsk) factors();
     if (layer_b) {
       float m[1] = {sum_of(y)};
       row_sum(m);
@@ -789,18 +828,28 @@ __global__ void __launch_bounds__(kBound, 1) norm_grad_kernel(const __grid_const
   }
 }
 
+template <int DT, int NV, int PATH, int kBound>
+const void *run_of() {
+  return reinterpret_cast<const void *>(norm_kernel<DT, NV, PATH, kBound>);
+}
+
 template <int NV, int PATH, int kBound>
 const void *pick_run(int dt) {
-  return dt == GE_F16    ? reinterpret_cast<const void *>(norm_kernel<GE_F16, NV, PATH, kBound>)
-         : dt == GE_BF16 ? reinterpret_cast<const void *>(norm_kernel<GE_BF16, NV, PATH, kBound>)
-                         : reinterpret_cast<const void *>(norm_kernel<GE_F32, NV, PATH, kBound>);
+  return dt == GE_F16    ? run_of<GE_F16, NV, PATH, kBound>()
+         : dt == GE_BF16 ? run_of<GE_BF16, NV, PATH, kBound>()
+                         : run_of<GE_F32, NV, PATH, kBound>();
+}
+
+template <int DT, int NV, int PATH, int kBound, bool kWhole>
+const void *grad_of() {
+  return reinterpret_cast<const void *>(norm_grad_kernel<DT, NV, PATH, kBound, kWhole>);
 }
 
 template <int NV, int PATH, int kBound, bool kWhole>
 const void *pick_grad(int dt) {
-  return dt == GE_F16    ? reinterpret_cast<const void *>(norm_grad_kernel<GE_F16, NV, PATH, kBound, kWhole>)
-         : dt == GE_BF16 ? reinterpret_cast<const void *>(norm_grad_kernel<GE_BF16, NV, PATH, kBound, kWhole>)
-                         : reinterpret_cast<const void *>(norm_grad_kernel<GE_F32, NV, PATH, kBound, kWhole>);
+  return dt == GE_F16    ? grad_of<GE_F16, NV, PATH, kBound, kWhole>()
+         : dt == GE_BF16 ? grad_of<GE_BF16, NV, PATH, kBound, kWhole>()
+                         : grad_of<GE_F32, NV, PATH, kBound, kWhole>();
 }
 
 }  // namespace ge

@@ -187,6 +187,17 @@ def test_grad_sizes(T, D, x):
     c.check_grads(c.grads())
 
 
+# Rows of no whole 16-byte units, on both sides of each change of threads and columns per thread
+@pytest.mark.gpu
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+@pytest.mark.parametrize("groups", ["one", "many"])
+@pytest.mark.parametrize("T,D", [(3, 2), (700, 238), (40, 1030), (500, 4094), (460, 4098), (460, 4099), (9, 8190), (7, 8191), (9, 8194), (5, 16382)])
+def test_other_widths(T, D, groups, x):
+    c = Case(T, D, x, "bf16", "layer", "rms", T if groups == "one" else 2)
+    c.check_forward(*c.forward())
+    c.check_grads(c.grads())
+
+
 KINDS = [("rms", "none"), ("rms", "rms"), ("layer", "none"), ("layer", "layer"), ("rms", "layer"), ("layer", "rms")]
 
 
