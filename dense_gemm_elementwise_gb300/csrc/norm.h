@@ -31,7 +31,7 @@ struct NormParams {
   int32_t row_threads;   // threads that share a row: a power of two up to 32, or whole warps
   int32_t ahead;         // rows of the ring
   int32_t w_vec;         // gate's rows and the vectors are whole 16-byte units
-  // units of the gradient pass
+  // units of the gradient pass; rows_per_unit is also the forward pass's run of a CTA, 0: dealt out
   int32_t units, rows_per_unit, rows_per_lane;
   int32_t units_per_group;  // 0: a lane holds whole groups
 };

@@ -198,6 +198,16 @@ def test_other_widths(T, D, groups, x):
     c.check_grads(c.grads())
 
 
+# Gate groups cut up, put together and over the edges of CTAs' runs of rows, in several waves of CTAs or one
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,D,gate", [(4001, 1100, 12), (4001, 1101, 12), (1999, 4096, 5), (1999, 4096, 8), (5000, 520, 40), (5000, 520, 57), (900, 2056, 899),
+                                      (900, 9000, 3), (20000, 24, 70), (20000, 24, 1)])
+def test_gate_groups(T, D, gate):
+    c = Case(T, D, "bf16", "f32", "rms", "rms", gate)
+    c.check_forward(*c.forward())
+    c.check_grads(c.grads())
+
+
 KINDS = [("rms", "none"), ("rms", "rms"), ("layer", "none"), ("layer", "layer"), ("rms", "layer"), ("layer", "rms")]
 
 
