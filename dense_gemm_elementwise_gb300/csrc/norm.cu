@@ -151,7 +151,7 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
   // up to a warp's chunks, take one; what 512 threads cannot hold so takes four.
   // Rows moved 4 or 8 bytes at a time: two in CTAs of over 512 columns' chunks only (with two,
   // the gradients of 8000 x 2050 fp32 take 193 us, not 107), and above 1024 chunks CTAs of up to
-  // 1024 threads (500 x 12346 bf16 30 us and 86, with four chunks 33 and 97).
+  // 1024 threads (500 x 12346 bf16 35 us and its gradients 85, with four chunks 33 and 97).
   // Odd rows of 16-bit elements: one up to 1024 threads, since each element has a register
   // of its own on its way.
   const int rows_by = pl->vec ? ROWS_16 : pl->even || pl->d.x == GE_F32 ? ROWS_SMALL : ROWS_ODD;
@@ -286,7 +286,7 @@ int gemm_epi_norm_plan_create(gemm_epi_norm_plan **plan, int64_t T, int64_t D, c
   pl->d = d;
   const int64_t es = size_of(d.x);
   pl->vec = true;
-  pl->even = D % 2 == 0;
+  pl->even = true;
   for (int64_t ld : {d.ldx, d.ldb, d.ldy, d.ldh}) {
     pl->vec = pl->vec && (ld * es) % 16 == 0;
     pl->even = pl->even && ld % 2 == 0;

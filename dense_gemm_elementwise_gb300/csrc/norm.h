@@ -39,8 +39,8 @@ struct NormParams {
 // Kernels, by how rows are moved; nv chunks per thread (1 or 2; whole units also 4), `threads` of a CTA.
 enum NormRows {
   ROWS_16 = 0,     // whole 16-byte units (nv 1, 2, 4)
-  ROWS_SMALL = 1,  // even rows, or odd rows of fp32 (`even` says which): 4 or 8 bytes at a time
-  ROWS_ODD = 2,    // odd rows of 16-bit elements, one by one
+  ROWS_SMALL = 1,  // even pitches, or odd ones of fp32 (`even` says which): 4 or 8 bytes at a time
+  ROWS_ODD = 2,    // odd pitches of 16-bit elements, one by one
 };
 const void *norm_kernel_run(int dt, int nv);
 const void *norm_kernel_grad(int dt, int nv);

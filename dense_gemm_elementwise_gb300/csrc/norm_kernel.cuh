@@ -96,8 +96,8 @@ constexpr int kPairs = kChunk / 2;
 //   P_STRIDED  other rows: every row_threads-th column, so that the threads of a
 //              warp read neighbouring elements (8 in a run would have each load
 //              touch four times the cache lines); fp32 through the ring
-//   P_PAIRS    the same, two columns at a time and through the ring, where rows
-//              and widths are even
+//   P_PAIRS    the same, two columns at a time and through the ring, where row
+//              pitches are even
 enum Path { P_RING = 0, P_DIRECT = 1, P_STRIDED = 2, P_PAIRS = 3 };
 
 template <int PATH>
@@ -120,8 +120,9 @@ __device__ __forceinline__ void store_row(typename Elem<DT>::T *row, const Colum
     if constexpr (PATH == P_PAIRS) {
 #pragma unroll
       for (int j = 0; j < kPairs; ++j) {
-        if (col(k, 2 * j) >= D) continue;  // D is even
-        if constexpr (DT == GE_F32) *reinterpret_cast<float2 *>(row + col(k, 2 * j)) = v[k][j];
+        if (col(k, 2 * j) >= D) continue;
+        if (col(k, 2 * j) + 1 == D) row[D - 1] = E::put(v[k][j].x);  // an odd row's last
+        else if constexpr (DT == GE_F32) *reinterpret_cast<float2 *>(row + col(k, 2 * j)) = v[k][j];
         else *reinterpret_cast<uint32_t *>(row + col(k, 2 * j)) = E::put2(v[k][j]);
       }
     } else if (PATH < P_STRIDED && col(k, 0) + kChunk <= D) {
@@ -288,10 +289,17 @@ struct Ring {
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < kUnits; ++j) {
-          // past the end: some column of the row, dropped when it is taken
-          const int c = min(col(k, j * (kChunk / kUnits)), D - kChunk / kUnits);
           const uint32_t dst = smem_u32(unit(((slot * NA + a) * NV + k) * kUnits + j));
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(row + c), "n"(kUnit) : "memory");
+          // past the end: the row's last column or pair, dropped when it is taken
+          if constexpr (PATH == P_PAIRS) {
+            // of an odd row's last pair only what exists is read
+            const int c = min(col(k, 2 * j), (D - 1) & ~1), left = c + 1 == D ? kUnit / 2 : kUnit;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(row + c), "n"(kUnit), "r"(left)
+                         : "memory");
+          } else {
+            const int c = min(col(k, j), D - 1);
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(row + c), "n"(kUnit) : "memory");
+          }
         }
     } else if constexpr (PATH == P_RING) {
 #pragma unroll
@@ -319,7 +327,9 @@ struct Ring {
     if constexpr (PATH == P_PAIRS) {
       using Two = typename std::conditional<sizeof(T) == 4, uint2, uint32_t>::type;
       union { Two w; T e[2]; } u;
-      u.w = *reinterpret_cast<const Two *>(row + min(col(k, 2 * i), D - 2));
+      const int c = min(col(k, 2 * i), (D - 1) & ~1);
+      if (c + 1 == D) u.e[0] = u.e[1] = row[c];
+      else u.w = *reinterpret_cast<const Two *>(row + c);
       e[2 * i] = u.e[0];
       e[2 * i + 1] = u.e[1];
     } else {

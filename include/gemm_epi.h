@@ -506,8 +506,8 @@ void gemm_epi_xent_plan_destroy(gemm_epi_xent_plan *plan);
  * (D,), all three and their gradients of type `w`.  rows_per_gate 1 is a
  * gate for every row, the sequence length one per sequence, T one for all.
  * Any D up to GE_NORM_MAX_D and any pitch: rows that are whole 16-byte units are
- * moved 16 bytes at a time, other rows (with an even D and even pitches) two
- * elements at a time, or one.  Arithmetic in fp32, one rounding per output.
+ * moved 16 bytes at a time, other rows two elements at
+ * a time (even pitches) or one.  Arithmetic in fp32, one rounding per output.
  */
 typedef enum { GE_NORM_NONE = 0, GE_NORM_RMS = 1, GE_NORM_LAYER = 2 } ge_norm_kind;
 #define GE_NORM_MAX_D 16384

@@ -198,6 +198,17 @@ def test_other_widths(T, D, groups, x):
     c.check_grads(c.grads())
 
 
+# Odd widths with even pitches: rows end in half a pair
+@pytest.mark.gpu
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+@pytest.mark.parametrize("T,D", [(3, 1), (4, 3), (700, 237), (301, 1803), (300, 4101), (9, 8189), (7, 8195), (5, 16383)])
+def test_odd_widths_even_pitches(T, D, x):
+    for gate in (0, 2):
+        c = Case(T, D, x, "bf16", "layer", "rms", gate, pad=(1, 3, 1, 5))
+        c.check_forward(*c.forward())
+        c.check_grads(c.grads())
+
+
 # Gate groups cut up, put together and over the edges of CTAs' runs of rows, in several waves of CTAs or one
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,D,gate", [(4001, 1100, 12), (4001, 1101, 12), (1999, 4096, 5), (1999, 4096, 8), (5000, 520, 40), (5000, 520, 57), (900, 2056, 899),
