@@ -9,8 +9,8 @@ constexpr int kChunk = 8;        // columns a thread holds per chunk
 constexpr int kVecThreads = 512;   // threads of a CTA, at most
 constexpr int kMaxThreads = 1024;  // ... with other rows than of whole 16-byte units
 // The forward pass is held to the registers of a CTA of 768 (85), so that three CTAs of 256 share
-// an SM: 8192 x 4096 bf16 in 47.0 us against 48.9 with two.  The gradients keep 128
-// (222 us against 306 for 16384 x 4096, whose sums then spill).
+// an SM: 8192 x 4096 bf16 in 45.0 us against 47.9 with two.  The gradients keep 128
+// (139 us against 307 for 16384 x 4096, whose sums then spill).
 constexpr int kRunBound = 768;
 constexpr int kMaxAhead = 3;     // rows in the ring of a thread
 constexpr int kSumBytes = 2 * (kMaxThreads / 32) * 16;  // shared memory of the rows' sums

@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kBound, 1) norm_kernel(const __grid_constant__
   // w_pre; alpha gate w_post of the gate group at hand
   const Own own_pre{words, n}, own_post{words + 2 * NV * n, n};
   Ring<DT, NV, PATH, 2, kBound> ring(reinterpret_cast<uint4 *>(words + 4 * NV * n), n, p.ahead, p.D, col);
-  // Rows are dealt out in turn (8192 x 4096 bf16 45.0 us, in runs 47), but with gate
+  // Rows are dealt out in turn (8192 x 4096 bf16 45.0 us, in runs 47.1), but with gate
   // groups a CTA takes a run of rows, which meets few of them (groups of 12, 15735 x 1808 f16: 49 us,
   // in turn 84).  Every thread's loop is as long.
   const int step = p.rows_per_unit ? rows : gridDim.x * rows;
