@@ -639,9 +639,10 @@ int configure(gemm_epi_xent_plan *pl) {
   auto single = [&](int64_t M, int64_t N) { return ceil_div(M, 128) * ceil_div(N, 128) <= sms; };
   const int cg = sms < 2 || pl->T <= 128 || single(pl->T, pl->V) ? 1 : 2;
   // The gradients' products too, up to 10^10 operations (about 6 us of the GPU): 200 x 4000 x 512
-  // in 37.6 us against 43.6, 1500 x 1000 x 2048 in 64.3 against 66.1.
+  // in 37.6 us against 43.6, 1500 x 1000 x 2048 in 64.3 against 66.1.  And dW of up to 128 rows, which
+  // is bound by its stores: 64 x 32000 x 2048 in 115 us against 123.
   const bool light = 2.0 * double(pl->T) * double(pl->V) * double(pl->D) <= 1e10;
-  const int cg_out = sms < 2 || (light && single(pl->V, pl->D)) ? 1 : 2;
+  const int cg_out = sms < 2 || pl->T <= 128 || (light && single(pl->V, pl->D)) ? 1 : 2;
   const int cg_part = sms < 2 || pl->T <= 128 || (light && single(pl->T, pl->D)) ? 1 : 2;
   int st = make_product(pl, &pl->stats, X_STATS, cg, 0);
   if (st == GE_OK) st = make_product(pl, &pl->keep, X_KEEP, cg, 0);

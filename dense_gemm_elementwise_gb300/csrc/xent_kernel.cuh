@@ -602,9 +602,18 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
             st_global32(o, w, MODE == X_DLOGIT || p.out32);
             st_global32(o + 16, w + 8, MODE == X_DLOGIT || p.out32);
           } else {
+            // the last columns: 16 bytes at a time as far as they go (one by one, each row's
+            // elements cost as much as the 32 bytes of the others)
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e < limit) o[e] = static_cast<uint16_t>(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
+            for (int u = 0; u < 4; ++u) {
+              if (c0 + 8 * u + 8 <= limit) {
+                *reinterpret_cast<uint4 *>(o + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+              } else {
+#pragma unroll
+                for (int e = 8 * u; e < 8 * u + 8; ++e)
+                  if (c0 + e < limit) o[e] = static_cast<uint16_t>(e & 1 ? w[e / 2] >> 16 : w[e / 2]);
+              }
+            }
           }
         }
       }
