@@ -672,18 +672,14 @@ int configure(gemm_epi_xent_plan *pl) {
   // One tile of rows: its time is that of reading W, and every CTA is given as many of W's
   // rows as the next (to 32) where whole tiles would leave CTAs idle at the end (32000 rows:
   // 224 to a CTA instead of one or two tiles of 128).
-  pl->band = cg == 1 && pl->T <= 128 ? 32 * ceil_div(ceil_div(pl->V, 32), units_of(pl, pl->stats)) : 0;
+  pl->band = cg == 1 && pl->T <= 128 ? band_of(pl->V, units_of(pl, pl->stats)) : 0;
   // Packing costs a launch (4 to 5 us) and saves the products of ignored rows: it is left
   // out where a batch fills one tile anyway and where the logits' product takes less than
   // about 20 us.  (A step without it needs a block of finish for every row.)
   const bool small = pl->T <= 128 || 2.0 * double(pl->T) * double(pl->V) * double(pl->D) < 3e10;
   pl->pack_loss = !small;
   pl->pack_step = !small || pl->T > 2 * pl->sms;
-  // pieces of the vocabulary: as wide as the buffer allows, equal, whole tiles
-  const int64_t bound = pl->d.buffer_bytes ? pl->d.buffer_bytes : int64_t(1) << 29;
-  const int64_t widest = std::max<int64_t>(256, bound / (2 * pl->T) / 256 * 256);
-  const int64_t pieces = ceil_div(pl->V, widest);
-  pl->piece = round_up(ceil_div(pl->V, pieces), 256);
+  pl->piece = piece_of(pl->T, pl->V, pl->d.buffer_bytes ? pl->d.buffer_bytes : int64_t(1) << 29);
   // dH: slices of its sum over a piece, decided on the device by the rows that
   // take part, within 64 MiB or what four waves of CTAs take of the tiles left over
   const int64_t tiles = tiles_of(pl->part, pl->T, pl->D);

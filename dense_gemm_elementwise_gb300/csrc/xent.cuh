@@ -2,6 +2,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "xent_bands.h"
 
 namespace ge {
 

@@ -500,14 +500,14 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
         }
         top *= p.c2;
         const float off = top == -INFINITY ? 0.f : top;
-        const bool keep = MODE == X_KEEP && n0 < p.keep_cols && live;
+        const bool keep = MODE == X_KEEP && live;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kParts; ++j) {
 #pragma unroll
           for (int e = 0; e < 32; ++e) v[j][e] = fmaf(v[j][e], p.c2, -off);
           const int c0 = grp * 64 + part(j);
-          if (keep && c0 < t.width) {
+          if (keep && keeps(n0, c0, t.width, p.keep_cols)) {
             // the distances, rounded to integers in the low bits of floats of 2^23 and more
             constexpr float k0 = 8388608.f, kStepsPerOctave = 1 << kKeptBits;
             uint32_t w[16];

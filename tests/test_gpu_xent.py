@@ -203,6 +203,23 @@ def test_pieces_of_the_vocabulary(T):
     c.check(c.step())
 
 
+# up to 128 rows: bands of columns whose last tile ends past the vocabulary, or which a piece's end cuts
+BANDS = [(2, 32000, {}), (64, 32000, {}), (128, 32000, {}), (64, 32768, {}), (2, 51200, {}), (128, 51200, {}), (64, 131072, {}),
+         (2, 262144, {}), (64, 10000, dict(buffer_bytes=1)), (64, 10240, dict(buffer_bytes=1)), (128, 1024, dict(max_ctas=6)),
+         (64, 10000, dict(max_ctas=19, buffer_bytes=1)), (40, 32000, dict(max_ctas=19, ignored=0.2))]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,kw", BANDS, ids=str)
+def test_bands_over_a_vocabulary(T, V, kw):
+    c = Case(T, V, 24, seed=T + V, **kw)
+    first = c.step()
+    c.check(first)
+    again = c.step()
+    for k in first:
+        assert torch.equal(first[k], again[k]), k
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 50, 300])
 def test_all_rows_ignored(T):
