@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
   bool there[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int c = c0 + 256 * h, of_band = p.band ? c % p.band : c;
-    slot[h] = int64_t(2 * ((p.band ? c / p.band * p.band_tiles : 0) + of_band / p.bn) + ((of_band / 64) & 1)) * p.T;
+    const int c = c0 + 256 * h;
+    slot[h] = int64_t(slot_of(c, p.N, p.band, p.band_tiles, p.bn)) * p.T;
     there[h] = c < (p.N + 255) / 256 * 256;
   }
   const float ds = p.sc->dl_scale;
@@ -569,8 +569,7 @@ namespace {
 
 // column ranges that leave a maximum and a sum
 int slots_of(const gemm_epi_xent_plan *pl) {
-  if (pl->band) return static_cast<int>(2 * ceil_div(pl->V, pl->band) * ceil_div(pl->band, pl->stats.bn));
-  return static_cast<int>(2 * ceil_div(pl->V, pl->stats.bn));
+  return static_cast<int>(ge::slots_of(pl->V, pl->band, pl->stats.bn));
 }
 
 Workspace workspace_of(const gemm_epi_xent_plan *pl, bool grads) {

@@ -33,4 +33,17 @@ GE_HOST_DEVICE bool keeps(int n0, int c0, int width, int keep_cols) {
   return c0 < width && n0 + c0 < keep_cols;
 }
 
+// Column ranges that leave a maximum and a sum: two to a tile of bn columns, its odd and even runs of 64.
+inline int64_t slots_of(int64_t V, int64_t band, int64_t bn) {
+  return band ? 2 * ((V + band - 1) / band) * ((band + bn - 1) / bn) : 2 * ((V + bn - 1) / bn);
+}
+
+// The range of column c, of N that exist.  Past them there is none, and the first is named:
+// what is read of it is dropped.
+GE_HOST_DEVICE int slot_of(int c, int N, int band, int band_tiles, int bn) {
+  if (c >= N) return 0;
+  const int of_band = band ? c % band : c;
+  return 2 * ((band ? c / band * band_tiles : 0) + of_band / bn) + ((of_band / 64) & 1);
+}
+
 }  // namespace ge

@@ -11,6 +11,8 @@ SOURCE = """
 extern "C" {
 int64_t band_of(int64_t V, int64_t units) { return ge::band_of(V, units); }
 int64_t piece_of(int64_t T, int64_t V, int64_t bytes) { return ge::piece_of(T, V, bytes); }
+int64_t slots_of(int64_t V, int64_t band, int64_t bn) { return ge::slots_of(V, band, bn); }
+int slot_of(int c, int N, int band, int band_tiles, int bn) { return ge::slot_of(c, N, band, band_tiles, bn); }
 int keeps(int n0, int c0, int width, int keep_cols) { return ge::keeps(n0, c0, width, keep_cols); }
 }
 """
@@ -24,8 +26,9 @@ def lib(tmp_path_factory):
     src.write_text(SOURCE)
     subprocess.run(["g++", "-O2", "-Wall", "-fPIC", "-shared", "-I", CSRC, "-o", str(so), str(src)], check=True)
     L = ctypes.CDLL(str(so))
-    for f, n in ((L.band_of, 2), (L.piece_of, 3)):
+    for f, n in ((L.band_of, 2), (L.piece_of, 3), (L.slots_of, 3)):
         f.restype, f.argtypes = ctypes.c_int64, [ctypes.c_int64] * n
+    L.slot_of.argtypes = [ctypes.c_int] * 5
     L.keeps.argtypes = [ctypes.c_int] * 4
     return L
 
@@ -64,3 +67,19 @@ def check_kept(lib, units, V, band, piece):
                 assert n0 + c0 not in seen
                 seen.add(n0 + c0)
     assert seen >= set(range(0, min(V, keep_cols), PART))
+
+
+@pytest.mark.parametrize("units", [0, 1, 5, 6, 19, 148, 152])
+def test_every_column_has_the_range_its_tile_left(lib, units):
+    """units 0: no bands, tiles of 128 and of 256 columns."""
+    for V, band, piece in shapes(lib, max(units, 1)):
+        for bn in (BN,) if units else (BN, 256):
+            band = band if units else 0
+            slots, per = lib.slots_of(V, band, bn), -(-band // bn)
+            N = min(piece, V)  # columns of the piece; whole multiples of 256 are converted, a lane's 8 at a time
+            for c in range(0, -(-N // 256) * 256, 8):
+                slot = lib.slot_of(c, N, band, per, bn)
+                assert 0 <= slot < slots, (V, band, bn, c)
+                if c < N:
+                    unit, of = (c // band, c % band) if band else (0, c)
+                    assert slot == 2 * (unit * per + of // bn) + of // 64 % 2
