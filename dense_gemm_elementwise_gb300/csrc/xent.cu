@@ -427,6 +427,13 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
           const float code = __uint_as_float(__byte_perm(u[e / 2], 0x4b000000u, e & 1 ? 0x7432 : 0x7410)) - 8388608.f;
           d[e] = ex2(fmaf(code, -1.f / (1 << kKeptBits), shift)) * f;
         }
+        // the farthest code stands for every distance from there on: p is 0 (or NaN, like its row)
+        const uint32_t most = __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3]));
+        if ((most & 0xffffu) == 0xffffu || most >> 16 == 0xffffu) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if ((u[e / 2] >> (16 * (e & 1)) & 0xffffu) == 0xffffu) d[e] *= 0.f;
+        }
         if (live && at >= 0 && at < 8) {
           // the target's own logit is at hand in fp32: p - 1 loses nothing to the rounding of p
           const float v = ex2(p.at_target[r] * (p.c2 / p.c) - lse2[i]) * f - coef[i].y * ds;

@@ -28,7 +28,7 @@ struct XentScalars {
 // A kept logit is its distance below its range's maximum in log2 units, in
 // fixed point with 11 bits after the point: p comes out off by at most 2^-12 ln 2 =
 // 1.7e-4, a twentieth of bf16's rounding (2^-8), and what is below 2^-32 of the maximum of
-// its own 64 to 128 columns counts as that.  fp16 rounds too finely for that
+// its own 64 to 128 columns counts as 0.  fp16 rounds too finely for that
 // (2^-11), so its logits are not kept but computed twice.
 constexpr int kKeptBits = 11;
 

@@ -221,6 +221,29 @@ def test_bands_over_a_vocabulary(T, V, kw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("c,buffer_bytes", [(1.0, 0), (-0.5, 0), (1.0, 1)])
+@pytest.mark.parametrize("T", [40, 300])
+def test_words_of_no_probability(T, c, buffer_bytes):
+    """Words whose logit is 64 below their neighbours' have p = 2e-28: no gradient of theirs is seen beside 2^-38 of
+    a row's.  All logits are exact in fp32; a kept distance moves p by at most 2^-12 of itself."""
+    V, D = 512, 8
+    gen = torch.Generator().manual_seed(T)
+    s = Case(T, V, D, c=c, mean=False, buffer_bytes=buffer_bytes)
+    s.H.copy_(torch.randint(-8, 9, (T, D), generator=gen).to(s.H))
+    s.H[:, 0] = 64.0
+    s.W.zero_()
+    s.W[[5, 70, 130, 300, 511], 0] = 1 / c
+    s.target.copy_(torch.randint(256, 300, (T,), generator=gen))
+    o = s.step()
+    torch.cuda.synchronize()
+    ref, m = reference(s.H, s.W, s.target, None, c, 0.0, False, 1.0)
+    e = U["bf16"] * m["d"] + 2.0 ** -12 * m["p"] + 2.0 ** -38
+    for k, off in (("dH", e @ m["Wd"].abs()), ("dW", e.T @ m["Hd"].abs())):
+        bound = abs(c) * off * (1 + 2.0 ** -10) + U["bf16"] * ref[k].abs()
+        assert bool(((o[k].double() - ref[k]).abs() <= bound).all()), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 50, 300])
 def test_all_rows_ignored(T):
     c = Case(T, 500, 64, ignored=2.0)
