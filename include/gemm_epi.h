@@ -426,9 +426,10 @@ int gemm_epi_plan_info(const gemm_epi_plan *plan, ge_plan_info *info);
  * The vocabulary is worked through in pieces, so that the 16-bit values that
  * pass from one kernel to the next take at most buffer_bytes.  With bf16, the
  * forward pass leaves each logit of the first piece in that buffer as its
- * distance below its neighbours' maximum, in 16 bits, and dl is made from it (p off by
- * up to 1.7e-4 of itself more, and 0 where it is below 2^-32 of its neighbours' largest); other pieces' logits, and fp16's, are computed again.  A
- * larger buffer so saves up to a quarter of the products.
+ * distance below its neighbours' maximum, in 16 bits, and dl is made from it
+ * (p off by up to 1.7e-4 of itself more, and 0 where it is below 2^-32 of its
+ * neighbours' largest); other pieces' logits, and fp16's, are computed again.
+ * A larger buffer so saves up to a quarter of the products.
  */
 typedef enum { GE_XENT_SUM = 0, GE_XENT_MEAN = 1 } ge_xent_reduction;
 typedef enum { GE_INDEX_I64 = 0, GE_INDEX_I32 = 1 } ge_index;

@@ -244,6 +244,37 @@ def test_words_of_no_probability(T, c, buffer_bytes):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("ab,c,pieces", [("bf16", 1.0, 1), ("bf16", -0.5, 1), ("bf16", 1.0, 2), ("bf16", -0.25, 2), ("f16", 1.0, 1)])
+@pytest.mark.parametrize("T", [40, 300])
+def test_logits_of_thousands(T, ab, c, pieces):
+    """Largest logits of 2000 to 16000 that are not the target's.  They and the differences between them are exact in
+    fp32; in log2 units they are below 2^15, so that rounding lse moves p by at most 2^-10 of itself, and a kept
+    distance by 2^-12: 2^-9 of p in all, beside the roundings of dl and of the results."""
+    V, D = 512, 8
+    gen = torch.Generator().manual_seed(T)
+    s = Case(T, V, D, ab, c=c, mean=False, buffer_bytes=1 if pieces == 2 else 0)
+    s.H.zero_()
+    s.W.zero_()
+    s.H[:, 0] = (torch.randint(128, 256, (T,), generator=gen) * 2.0 ** torch.randint(4, 7, (T,), generator=gen)).to(s.H)
+    s.H[:, 1] = 1.0
+    near = torch.tensor([5, 6, 70, 130, 250, 300, 511])
+    s.W[near, 0] = 1 / c
+    s.W[near, 1] = torch.tensor([0.0, -0.25, -1.0, -0.5, 0.0, -0.75, -2.0]).to(s.W) / c
+    s.W[:, 2:] = (torch.randint(-8, 9, (V, D - 2), generator=gen) / 8).to(s.W)  # seen by dH alone
+    s.target.copy_(torch.randint(7, 60, (T,), generator=gen))
+    o = s.step()
+    torch.cuda.synchronize()
+    assert B.gemm_epi_last_error() == B.GE_OK
+    ref, m = reference(s.H, s.W, s.target, None, c, 0.0, False, 1.0)
+    assert bool(((o["lse"].double() - ref["lse"]).abs() <= 2.0 ** -20 * ref["lse"]).all())
+    e = U[ab] * m["d"] + 2.0 ** -9 * m["p"] + 2.0 ** -38
+    for k, off in (("dH", e @ m["Wd"].abs()), ("dW", e.T @ m["Hd"].abs())):
+        bound = abs(c) * off * (1 + 2.0 ** -10) + U[ab] * ref[k].abs() + 2.0 ** -24
+        past = torch.isinf(o[k]) & (ref[k].abs() > torch.finfo(TYPE[ab]).max)  # no number of the type
+        assert bool((past | ((o[k].double() - ref[k]).abs() <= bound)).all()), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [1, 50, 300])
 def test_all_rows_ignored(T):
     c = Case(T, 500, 64, ignored=2.0)
