@@ -356,6 +356,7 @@ struct ConvertParams {
   int64_t pitch;
   int32_t T, N, bn;          // N columns exist of the piece
   int32_t band, band_tiles;  // as in the product that kept them
+  int32_t row_ctas;          // CTAs that share the rows of 512 columns
   float c2, c;               // logit_scale log2(e), logit_scale
 };
 
@@ -371,7 +372,8 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // last columns first: the product wrote them last, and what is left in L2 for
   // the next product is what that reads first
-  const int c0 = (gridDim.y - 1 - blockIdx.y) * kConvertCols + lane * 8;
+  const int across = gridDim.x / p.row_ctas, by = blockIdx.x / p.row_ctas, bx = blockIdx.x - by * p.row_ctas;
+  const int c0 = (across - 1 - by) * kConvertCols + lane * 8;
   int64_t slot[2];
   bool there[2];
 #pragma unroll
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant
     there[h] = c < (p.N + 255) / 256 * 256;
   }
   const float ds = p.sc->dl_scale;
-  for (int first = blockIdx.x * kConvertRows + warp; first < end; first += gridDim.x * kConvertRows) {
+  for (int first = bx * kConvertRows + warp; first < end; first += p.row_ctas * kConvertRows) {
     uint4 w[2][2];
     float top[2][2], lse2[2];
     float2 coef[2];
@@ -893,10 +895,11 @@ int run(gemm_epi_xent_plan *pl, bool grads, const void *H, const void *W, const 
       cp.band_tiles = sl.band_tiles;
       cp.c2 = sl.c2;
       cp.c = sl.c;
-      const unsigned cols = static_cast<unsigned>(ceil_div(n, kConvertCols));
-      const unsigned rows = static_cast<unsigned>(
+      const int64_t cols = ceil_div(n, kConvertCols);
+      cp.row_ctas = static_cast<int32_t>(
           std::max<int64_t>(1, std::min<int64_t>(ceil_div(T, kConvertRows), ceil_div(16 * pl->sms, cols))));
-      if (!go(launch(reinterpret_cast<const void *>(xent_convert_kernel), dim3(rows, cols), 256, 0, 1, &cp, s)))
+      const dim3 grid(static_cast<unsigned>(cols * cp.row_ctas));
+      if (!go(launch(reinterpret_cast<const void *>(xent_convert_kernel), grid, 256, 0, 1, &cp, s)))
         return GE_ERR_CUDA;
     } else {
       XentParams q = params_of(pl, pl->dlogit, sc, T, n, D);

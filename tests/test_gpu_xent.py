@@ -391,6 +391,36 @@ def test_long_rows_of_offsets_past_32_bits():
 
 
 @pytest.mark.gpu
+def test_a_vocabulary_of_more_column_blocks_than_a_grid_has_rows():
+    # 512 columns each, and 65535: a step that keeps the logits of 33.6 million words
+    T, V, D = 2, 33_600_000, 8
+    dev = torch.device("cuda", 0)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    W = torch.randn(V, D, generator=gen, device=dev, dtype=torch.bfloat16)
+    H = torch.randn(T, D, generator=gen, device=dev, dtype=torch.bfloat16)
+    t = torch.tensor([V - 1, 77], device=dev)
+    plan = B.gemm_epi_xent_plan_create(T, V, D, B.make_xent_desc("bf16", reduction="sum"))
+    ws = torch.full((B.gemm_epi_xent_workspace_bytes(plan, True),), 0xFF, dtype=torch.uint8, device=dev)
+    loss, lse, total, dW, dH = torch.empty(T, device=dev), torch.empty(T, device=dev), None, torch.full_like(W, 7.0), torch.empty_like(H)
+    assert B.gemm_epi_xent_step(plan, H, W, t, None, 1.0, loss, lse, total, dH, dW, ws, check=False) == B.GE_OK
+    torch.cuda.synchronize()
+    assert B.gemm_epi_last_error() == B.GE_OK
+    l = H.double() @ W.double().T
+    want = torch.logsumexp(l, 1)
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -18 * want).all())
+    d = torch.exp(l - want[:, None])
+    d[torch.arange(T), t] -= 1
+    mag = H.double().abs()
+    for first in (0, V // 2, V - 4096):  # dl, its products with H and their sum are rounded to bf16, p is off by 2^-12
+        at = slice(first, first + 4096)
+        bound = (2 * U["bf16"] + 2.0 ** -10) * (d[:, at].abs().T @ mag) + 2.0 ** -60
+        assert bool(((dW[at].double() - d[:, at].T @ H.double()).abs() <= bound).all()), first
+    bound = (U["bf16"] + 2.0 ** -10 + 2 * acc(V)) * (d.abs() @ W.double().abs()) + U["bf16"] * (d @ W.double()).abs()
+    assert bool(((dH.double() - d @ W.double()).abs() <= bound).all())
+    B.gemm_epi_xent_plan_destroy(plan)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [20, 300])
 def test_a_load_that_never_comes_is_reported(T):
     """The first k-block of every product is left out: its wait runs out after 20 ms and the run ends by itself."""
