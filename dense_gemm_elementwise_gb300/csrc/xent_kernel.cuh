@@ -101,10 +101,12 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   constexpr int kEpi0 = 2;                                   // first epilogue warp
   // k-blocks that the tensor unit sums before the epilogue adds them up in
   // registers.  Its sums are cut off, not rounded: left to itself over all of K it gives an
-  // lse that is low by 2.0e-6 of its value at D = 4096 and 4.0e-6 at 8192, in runs of K = 1024 by
-  // 4.8e-7, of 1536 by 7.2e-7 whatever D is (256: 1.2e-7, but a run's 2000 clocks are then
-  // less than its sums take to be read, and 4096 x 65536 x 2048 takes 771 us instead of 622).
-  constexpr int kMostRun = 24;
+  // lse that is low by 2.0e-6 of its value at D = 4096 and 4.0e-6 at 8192 (bf16: 4.8e-10 for every column;
+  // fp16, whose products have more bits to lose: 5.9e-10), in runs of K = 1024 and of 832 by 5.0e-7
+  // whatever D is.  (Runs of 1536 lose 7.4e-7 and 8.8e-7, and save 2 % of a step at D = 1280; runs of 256 lose
+  // 1.2e-7, but their 2000 clocks are less than their sums take to be read: 4096 x 65536 x 2048 in
+  // 24 % more time.)
+  const int most_run = p.bf16 ? 16 : 13;
   constexpr int kTogether = 2;  // k-blocks loaded together in bands
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -160,7 +162,7 @@ __global__ void __launch_bounds__(kXentThreads, 1) xent_kernel(const __grid_cons
   const int rest = per_slice - num_full;
   const int num_tiles = num_full + rest * (MODE == X_PART ? (num_kb + kb_split - 1) / kb_split : 2);
   // (Runs of equal length: a short last one would be waited for.)
-  const int runs = kStats ? (num_kb + kMostRun - 1) / kMostRun : 1;
+  const int runs = kStats ? (num_kb + most_run - 1) / most_run : 1;
   const int run = kStats ? (num_kb + runs - 1) / runs : num_kb;
   // In bands: unit u takes columns [u band, (u + 1) band) in tiles of up to BN.
   const bool bands = kStats && CG == 1 && p.band > 0;

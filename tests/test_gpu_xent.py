@@ -203,6 +203,22 @@ def test_pieces_of_the_vocabulary(T):
     c.check(c.step())
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [1280, 1536, 4096])
+def test_sums_of_a_long_width_are_taken_in_runs(D, ab):
+    """The tensor unit's fp32 sums are cut off, which lowers lse by 4.8e-10 of itself for every column in a run (bf16;
+    fp16 a quarter more).  Runs hold it to what 1024 columns of bf16 lose; beside that mean there are only roundings of
+    either sign."""
+    T, V = 300, 8000
+    c = Case(T, V, D, ab, seed=D, scale=2.5)
+    near = torch.arange(0, T, 2, device=c.H.device)
+    c.H[near] += c.W[c.target[near]]
+    o = c.loss()
+    ref = c.check(o, grads=False)
+    assert abs(float((o["lse"].double() / ref["lse"] - 1).mean())) <= 4.8e-10 * 1024 + 2.0 ** -24
+
+
 # up to 128 rows: bands of columns whose last tile ends past the vocabulary, or which a piece's end cuts
 BANDS = [(2, 32000, {}), (64, 32000, {}), (128, 32000, {}), (64, 32768, {}), (2, 51200, {}), (128, 51200, {}), (64, 131072, {}),
          (2, 262144, {}), (64, 10000, dict(buffer_bytes=1)), (64, 10240, dict(buffer_bytes=1)), (128, 1024, dict(max_ctas=6)),
