@@ -303,6 +303,31 @@ def test_in_place(T, D):
     assert torch.equal(dy, o["dx"]) and torch.equal(b, o["db"])
 
 
+# outputs in every place that may be theirs, however rows are moved: whole 16-byte units, read when wanted above 8192
+# columns, pairs and single elements, with and without a ring
+@pytest.mark.gpu
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [12, 1026, 1111, 5000, 5001, 5002, 9000, 9001, 9002, 16384])
+def test_in_place_whatever_the_width(D, x):
+    c = Case(90, D, x, "bf16", "layer", "rms", 7)
+    want = c.forward()
+    c.check_forward(*want)
+    for places in ("xb", "bx", "x-", "-b", "b-", "-x"):
+        at = dict(x=c.xs.clone(), b=c.b.clone())
+        y, h = (at.get(k, None) if k != "-" else c.out(D) for k in places)
+        B.gemm_epi_norm_run(c.plan, at["x"], at["b"], c.gate, c.w_post, c.w_pre, y, h)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[0]) and torch.equal(h, want[1]), places
+    o = c.grads()
+    c.check_grads(o)
+    ws = torch.empty(B.gemm_epi_norm_workspace_bytes(c.plan), dtype=torch.uint8, device=c.b.device)
+    for dx, db in (("dy", "b"), ("dy", "dh"), ("dh", "b")):
+        at = dict(dy=c.dy.clone(), dh=c.dh.clone(), b=c.b.clone())
+        B.gemm_epi_norm_grad(c.plan, at["dy"], at["dh"], c.y, at["b"], c.gate, c.w_post, c.w_pre, at[dx], at[db], None, None, None, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(at[dx], o["dx"]) and torch.equal(at[db], o["db"]), (dx, db)
+
+
 @pytest.mark.gpu
 def test_another_stream_a_graph_and_the_same_bits():
     c = Case(500, 320, gate=100)

@@ -204,6 +204,14 @@ def test_pieces_of_the_vocabulary(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(), dict(ignored=0.3, buffer_bytes=1777 * 2 * 2048), dict(weights="positive", z=1e-3)], ids=str)
+def test_step_of_many_fp16_rows(kw):
+    # four products, three of them after one another for each piece
+    c = Case(1777, 6001, 304, "f16", seed=3, g=256.0, **kw)
+    c.check(c.step())
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("ab", ["bf16", "f16"])
 @pytest.mark.parametrize("D", [1280, 1536, 4096])
 def test_sums_of_a_long_width_are_taken_in_runs(D, ab):
