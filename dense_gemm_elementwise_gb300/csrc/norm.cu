@@ -385,9 +385,11 @@ int gemm_epi_norm_grad(gemm_epi_norm_plan *pl, const void *dy, const void *dh, c
   if ((!b && (db || dgate || dw_post)) || (!gate && dgate) || (!w_post && dw_post) || (!w_pre && dw_pre))
     return GE_ERR_INVALID;
   const ge_norm_desc &d = pl->d;
-  if (dx == db || (dx == dy && d.ldx != d.ldy) || (dx == dh && d.ldx != d.ldh) ||
-      (db && db == dh && d.ldb != d.ldh))
-    return GE_ERR_INVALID;
+  // in place, as in the forward pass
+  if (dx == db) return GE_ERR_INVALID;
+  const struct { const void *p; int64_t ld; } in[] = {{dy, d.ldy}, {dh, d.ldh}, {y, d.ldy}, {b, d.ldb}};
+  for (const auto &q : in)
+    if ((dx == q.p && d.ldx != q.ld) || (db && db == q.p && d.ldb != q.ld)) return GE_ERR_INVALID;
   if (!workspace || !is_aligned16(workspace) || workspace_bytes < gemm_epi_norm_workspace_bytes(pl))
     return GE_ERR_WORKSPACE;
   NormParams p = pl->p;

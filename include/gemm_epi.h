@@ -540,7 +540,8 @@ size_t gemm_epi_norm_workspace_bytes(const gemm_epi_norm_plan *plan);
  * One launch on `stream`.  b NULL: y = x (the first norm of a network).
  * gate must be given exactly when rows_per_gate > 0 and b is given; w_post
  * (post not GE_NORM_NONE) and w_pre may be NULL (all 1); y or h may be NULL
- * (not both).  y may be x or b, h may be b: a row is read whole before it is written.
+ * (not both).  y and h may each be x or b, if pitches are equal: a row is read whole
+ * before it is written.
  * Errors: GE_ERR_INVALID, _MISSING_ARG, _MISALIGNED, _CUDA.
  */
 int gemm_epi_norm_run(gemm_epi_norm_plan *plan, const void *x, const void *b, const void *gate,
@@ -553,8 +554,8 @@ int gemm_epi_norm_run(gemm_epi_norm_plan *plan, const void *x, const void *b, co
  *   dx = dy + dN_pre(dh * w_pre)    db = d(N_post)(alpha * gate * w_post * dx)
  *   dgate, dw_post, dw_pre: sums over the rows that share them
  * b NULL: dx (and dw_pre) alone.  db, dgate, dw_post and dw_pre may be NULL.  Two
- * launches; sums over rows run in a fixed order, no atomics.  dx may be dy or dh, db may be
- * b or dh, dx and db not the same.  Errors: as gemm_epi_norm_run, and GE_ERR_WORKSPACE.
+ * launches; sums over rows run in a fixed order, no atomics.  dx and db may each be dy, dh, y
+ * or b, if pitches are equal, and not the same.  Errors: as gemm_epi_norm_run, and GE_ERR_WORKSPACE.
  */
 int gemm_epi_norm_grad(gemm_epi_norm_plan *plan, const void *dy, const void *dh, const void *y,
                        const void *b, const void *gate, const void *w_post, const void *w_pre,

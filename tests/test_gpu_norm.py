@@ -321,9 +321,9 @@ def test_in_place_whatever_the_width(D, x):
     o = c.grads()
     c.check_grads(o)
     ws = torch.empty(B.gemm_epi_norm_workspace_bytes(c.plan), dtype=torch.uint8, device=c.b.device)
-    for dx, db in (("dy", "b"), ("dy", "dh"), ("dh", "b")):
-        at = dict(dy=c.dy.clone(), dh=c.dh.clone(), b=c.b.clone())
-        B.gemm_epi_norm_grad(c.plan, at["dy"], at["dh"], c.y, at["b"], c.gate, c.w_post, c.w_pre, at[dx], at[db], None, None, None, ws)
+    for dx, db in (("dy", "b"), ("dy", "dh"), ("dh", "b"), ("y", "dy"), ("b", "y")):
+        at = dict(dy=c.dy.clone(), dh=c.dh.clone(), y=c.y.clone(), b=c.b.clone())
+        B.gemm_epi_norm_grad(c.plan, at["dy"], at["dh"], at["y"], at["b"], c.gate, c.w_post, c.w_pre, at[dx], at[db], None, None, None, ws)
         torch.cuda.synchronize()
         assert torch.equal(at[dx], o["dx"]) and torch.equal(at[db], o["db"]), (dx, db)
 
@@ -398,6 +398,25 @@ def test_gradient_formula_against_differences(pre, post):
             up, dn = list(args), list(args)
             up[k], dn[k] = v + e.view_as(v), v - e.view_as(v)
             assert abs((f(*up) - f(*dn)) / (2 * h) - float(flat[i])) < 1e-7
+
+
+@pytest.mark.gpu
+def test_in_place_of_another_pitch_is_refused():
+    c = Case(8, 64, pad=(0, 8, 16, 24))  # x, b, y, h
+    big = lambda: torch.zeros(8 * 88, dtype=torch.bfloat16, device=c.xs.device)  # noqa: E731
+    a = {k: big() for k in ("dy", "dh", "y", "b", "dx", "db")}
+    ws = torch.empty(B.gemm_epi_norm_workspace_bytes(c.plan), dtype=torch.uint8, device=c.xs.device)
+
+    def grad(**kw):
+        p = {**a, **{k: a[v] for k, v in kw.items()}}
+        return B.gemm_epi_norm_grad(c.plan, p["dy"], p["dh"], p["y"], p["b"], None, None, None, p["dx"], p["db"], None, None, None, ws, check=False)
+
+    for k in ("dy", "dh", "y", "b"):
+        assert grad(dx=k) == B.GE_ERR_INVALID, k
+    for k in ("dy", "dh", "y"):
+        assert grad(db=k) == B.GE_ERR_INVALID, k
+    assert grad() == grad(db="b") == B.GE_OK
+    torch.cuda.synchronize()
 
 
 def _create(T=4, D=8, **kw):
