@@ -361,7 +361,8 @@ struct ConvertParams {
 };
 
 // Kept distances to dl, in place: a warp per row of 512 columns, two times 16 bytes per
-// lane, two rows ahead.  Bound by memory: 4 bytes and one exponential per logit.
+// lane, two rows ahead.  Bound by memory: 4 bytes and one exponential per logit (4096 x 32000 in 85 us alone,
+// 6.1 TB/s).
 constexpr int kConvertRows = 16;   // rows of a CTA (8 warps, 2 rows each)
 constexpr int kConvertCols = 512;
 __global__ void __launch_bounds__(256) xent_convert_kernel(const __grid_constant__ ConvertParams p) {
@@ -641,14 +642,14 @@ int64_t tiles_of(const Product &pr, int64_t M, int64_t N) { return ceil_div(M, 1
 int configure(gemm_epi_xent_plan *pl) {
   // Tiles: 256 x 256 on CTA pairs, or 128 x 128 on single CTAs where a batch fills no more
   // rows than that or the whole product is at most one tile for every SM, which
-  // is then bound by its start and its end (256 x 8000 x 1024: a loss 17.2 us against
-  // 18.8 on pairs, a step 57.3 against 60.1).
+  // is then bound by its start and its end (256 x 8000 x 1024: a loss 17.0 us against
+  // 18.9 on pairs, a step 54.5 against 59.7).
   const int sms = pl->d.max_ctas ? std::min(pl->d.max_ctas, pl->sms) : pl->sms;
   auto single = [&](int64_t M, int64_t N) { return ceil_div(M, 128) * ceil_div(N, 128) <= sms; };
   const int cg = sms < 2 || pl->T <= 128 || single(pl->T, pl->V) ? 1 : 2;
   // The gradients' products too, up to 10^10 operations (about 6 us of the GPU): 200 x 4000 x 512
-  // in 37.6 us against 43.6, 1500 x 1000 x 2048 in 64.3 against 66.1.  And dW of up to 128 rows, which
-  // is bound by its stores: 64 x 32000 x 2048 in 115 us against 123.
+  // in 36.7 us against 45.5, 1500 x 1000 x 2048 in 63.3 against 67.6.  And dW of up to 128 rows, which
+  // is bound by its stores: 64 x 32000 x 2048 in 122 us against 129.
   const bool light = 2.0 * double(pl->T) * double(pl->V) * double(pl->D) <= 1e10;
   const int cg_out = sms < 2 || pl->T <= 128 || (light && single(pl->V, pl->D)) ? 1 : 2;
   const int cg_part = sms < 2 || pl->T <= 128 || (light && single(pl->T, pl->D)) ? 1 : 2;
