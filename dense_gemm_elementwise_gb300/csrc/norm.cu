@@ -188,7 +188,8 @@ int shape_of(const gemm_epi_norm_plan *pl, int pass, int max_smem, RowShape *out
   }
   if (r.smem > max_smem) return GE_ERR_SMEM;
   int per_sm = 0;
-  if (cudaFuncSetAttribute(r.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, r.smem) != cudaSuccess ||
+  // the kernel's limit, which all of its plans share: the most there is, not what this one needs
+  if (cudaFuncSetAttribute(r.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess ||
       cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, r.fn, r.threads, static_cast<size_t>(r.smem)) !=
           cudaSuccess ||
       per_sm < 1) {

@@ -350,6 +350,17 @@ def test_another_stream_a_graph_and_the_same_bits():
     c.check_forward(y2, h2)
 
 
+# rows per batch, the wider and the narrower rows of two plans that share kernels
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,wide,narrow,x", [(700, 4096, 2560, "bf16"), (5, 4096, 320, "bf16"), (40, 4094, 1026, "f32"), (40, 4001, 1001, "f32"),
+                                             (40, 4001, 301, "f16"), (9, 16384, 9000, "f16"), (9, 16382, 9002, "bf16"), (9, 16383, 9001, "f16")])
+def test_a_plan_outlives_the_making_of_smaller_ones(T, wide, narrow, x):
+    c = [Case(T, D, x, gate=2) for D in (wide, narrow)]
+    for k in c:
+        k.check_forward(*k.forward())
+        k.check_grads(k.grads())
+
+
 @pytest.mark.gpu
 def test_offsets_past_32_bits():
     T, D = 140000, 16384
