@@ -417,8 +417,9 @@ int gemm_epi_plan_info(const gemm_epi_plan *plan, ge_plan_info *info);
  * A logit that is NaN or +infinity makes its row's loss NaN and reaches the
  * gradients as in the formulas.
  *
- * Arithmetic: exact products summed in fp32, softmax statistics in fp32,
- * sums over rows in fp32 in a tree of fixed shape.  dl is rounded once to `ab` on its way into the
+ * Arithmetic: exact products summed in fp32 (which the tensor unit cuts off:
+ * lse is low by up to 5e-7 of itself), softmax statistics in fp32, sums over
+ * rows in fp32 in a tree of fixed shape.  dl is rounded once to `ab` on its way into the
  * gradient products, scaled by a power of two (found on the device) that
  * keeps it clear of fp16's subnormals; dH and dW are summed in fp32 and rounded
  * once.  Results are bit-for-bit repeatable for a given plan and device.
