@@ -11,7 +11,7 @@ import os
 
 from . import build as _build
 
-GE_F16, GE_BF16, GE_F32 = 0, 1, 2
+GE_F16, GE_BF16, GE_F32, GE_E4M3, GE_E5M2 = 0, 1, 2, 3, 4
 (GE_ACCFETCH, GE_LOAD, GE_SCALAR, GE_BROADCAST, GE_MUL, GE_ADD, GE_RELU, GE_STORE, GE_SUB, GE_DIV,
  GE_MIN, GE_MAX, GE_COL_BROADCAST, GE_SIGMOID, GE_TANH, GE_GELU, GE_SILU, GE_HARDSWISH,
  GE_LEAKY_RELU) = range(19)
@@ -27,7 +27,7 @@ STATUS = ["GE_OK", "GE_ERR_NO_ACCUM", "GE_ERR_NO_D", "GE_ERR_SSA", "GE_ERR_MISSI
 for _i, _n in enumerate(STATUS):
     globals()[_n] = _i
 
-DTYPE = {"f16": GE_F16, "bf16": GE_BF16, "f32": GE_F32}
+DTYPE = {"f16": GE_F16, "bf16": GE_BF16, "f32": GE_F32, "e4m3": GE_E4M3, "e5m2": GE_E5M2}
 OP = {"accum": GE_ACCFETCH, "load": GE_LOAD, "scalar": GE_SCALAR, "broadcast": GE_BROADCAST,
       "mul": GE_MUL, "add": GE_ADD, "relu": GE_RELU, "store": GE_STORE, "sub": GE_SUB,
       "div": GE_DIV, "min": GE_MIN, "max": GE_MAX, "col_broadcast": GE_COL_BROADCAST,
@@ -42,16 +42,24 @@ EXPORTS = ["gemm_epi_plan_create", "gemm_epi_plan_create_ex", "gemm_epi_validate
            "gemm_epi_xent_plan_create", "gemm_epi_xent_workspace_bytes", "gemm_epi_xent_loss",
            "gemm_epi_xent_step", "gemm_epi_xent_plan_destroy", "gemm_epi_norm_plan_create",
            "gemm_epi_norm_workspace_bytes", "gemm_epi_norm_run", "gemm_epi_norm_grad",
-           "gemm_epi_norm_plan_destroy"]
+           "gemm_epi_norm_plan_destroy", "gemm_epi_quant_plan_create", "gemm_epi_quant_run",
+           "gemm_epi_quant_plan_destroy", "gemm_epi_fp8_plan_create", "gemm_epi_fp8_workspace_bytes",
+           "gemm_epi_fp8_run", "gemm_epi_fp8_plan_destroy", "gemm_epi_moe_plan_create",
+           "gemm_epi_moe_workspace_bytes", "gemm_epi_moe_run", "gemm_epi_moe_plan_destroy"]
 GE_NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 GE_MAX_GROUPS = 4096
 GE_XENT_SUM, GE_XENT_MEAN = 0, 1
 GE_INDEX_I64, GE_INDEX_I32 = 0, 1
 GE_NORM_NONE, GE_NORM_RMS, GE_NORM_LAYER = 0, 1, 2
 GE_NORM_MAX_D = 16384
+GE_BLOCK_ROW, GE_BLOCK_SQUARE = 0, 1
+GE_SCORE_SOFTMAX, GE_SCORE_SIGMOID = 0, 1
+GE_MOE_MAX_TOKENS, GE_MOE_MAX_EXPERTS, GE_MOE_MAX_K = 128, 512, 16
 REDUCTION = {"sum": GE_XENT_SUM, "mean": GE_XENT_MEAN}
 INDEX = {"i64": GE_INDEX_I64, "i32": GE_INDEX_I32}
 NORM = {"none": GE_NORM_NONE, "rms": GE_NORM_RMS, "layer": GE_NORM_LAYER}
+BLOCK = {"row": GE_BLOCK_ROW, "square": GE_BLOCK_SQUARE}
+SCORE = {"softmax": GE_SCORE_SOFTMAX, "sigmoid": GE_SCORE_SIGMOID}
 
 
 class ge_node(ctypes.Structure):
@@ -105,6 +113,28 @@ class ge_norm_desc(ctypes.Structure):
                 ("alpha", ctypes.c_float), ("reserved", ctypes.c_int32),
                 ("rows_per_gate", ctypes.c_int64), ("ldx", ctypes.c_int64), ("ldb", ctypes.c_int64),
                 ("ldy", ctypes.c_int64), ("ldh", ctypes.c_int64)]
+
+
+class ge_quant_desc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int32), ("q", ctypes.c_int32), ("block", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("ldx", ctypes.c_int64), ("ldq", ctypes.c_int64),
+                ("ldqt", ctypes.c_int64), ("lds", ctypes.c_int64), ("ldst", ctypes.c_int64)]
+
+
+class ge_fp8_desc(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_int32), ("b", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("b_block", ctypes.c_int32), ("timeout_ms", ctypes.c_int32),
+                ("max_ctas", ctypes.c_int32), ("debug_flags", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32), ("lda", ctypes.c_int64), ("ldb", ctypes.c_int64),
+                ("ldd", ctypes.c_int64), ("lds_a", ctypes.c_int64), ("lds_b", ctypes.c_int64)]
+
+
+class ge_moe_desc(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_int32), ("w", ctypes.c_int32), ("router", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("timeout_ms", ctypes.c_int32), ("debug_flags", ctypes.c_uint32),
+                ("route_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
 
 
 class GemmEpiError(RuntimeError):
@@ -174,6 +204,28 @@ def _load():
     L.gemm_epi_norm_grad.argtypes = [P] * 14 + [sz, P]
     L.gemm_epi_norm_plan_destroy.restype = None
     L.gemm_epi_norm_plan_destroy.argtypes = [P]
+    L.gemm_epi_quant_plan_create.restype = ctypes.c_int
+    L.gemm_epi_quant_plan_create.argtypes = [pp, i64, i64, ctypes.POINTER(ge_quant_desc)]
+    L.gemm_epi_quant_run.restype = ctypes.c_int
+    L.gemm_epi_quant_run.argtypes = [P] * 7
+    L.gemm_epi_quant_plan_destroy.restype = None
+    L.gemm_epi_quant_plan_destroy.argtypes = [P]
+    L.gemm_epi_fp8_plan_create.restype = ctypes.c_int
+    L.gemm_epi_fp8_plan_create.argtypes = [pp, i64, i64, i64, ctypes.POINTER(ge_fp8_desc)]
+    L.gemm_epi_fp8_workspace_bytes.restype = sz
+    L.gemm_epi_fp8_workspace_bytes.argtypes = [P]
+    L.gemm_epi_fp8_run.restype = ctypes.c_int
+    L.gemm_epi_fp8_run.argtypes = [P] * 8 + [sz, P]
+    L.gemm_epi_fp8_plan_destroy.restype = None
+    L.gemm_epi_fp8_plan_destroy.argtypes = [P]
+    L.gemm_epi_moe_plan_create.restype = ctypes.c_int
+    L.gemm_epi_moe_plan_create.argtypes = [pp, i64, i64, i64, i64, i64, ctypes.POINTER(ge_moe_desc)]
+    L.gemm_epi_moe_workspace_bytes.restype = sz
+    L.gemm_epi_moe_workspace_bytes.argtypes = [P]
+    L.gemm_epi_moe_run.restype = ctypes.c_int
+    L.gemm_epi_moe_run.argtypes = [P] * 12 + [sz, P]
+    L.gemm_epi_moe_plan_destroy.restype = None
+    L.gemm_epi_moe_plan_destroy.argtypes = [P]
     L.gemm_epi_status_string.restype = ctypes.c_char_p
     L.gemm_epi_status_string.argtypes = [ctypes.c_int]
     L.gemm_epi_last_error.restype = ctypes.c_int
@@ -488,6 +540,133 @@ def gemm_epi_norm_grad(plan, dy, dh, y, b, gate, w_post, w_pre, dx, db, dgate, d
     return _checked(prepare_norm_grad(plan, dy, dh, y, b, gate, w_post, w_pre, dx, db, dgate,
                                       dw_post, dw_pre, workspace, workspace_bytes, stream)(),
                     "gemm_epi_norm_grad", check)
+
+
+# ------------------------------------------- 8-bit floats, scaled by block --
+
+def make_quant_desc(x, q, block="row", ldx=0, ldq=0, ldqt=0, lds=0, ldst=0):
+    d = ge_quant_desc()
+    d.x = DTYPE[x] if isinstance(x, str) else x
+    d.q = DTYPE[q] if isinstance(q, str) else q
+    d.block = BLOCK[block] if isinstance(block, str) else block
+    d.ldx, d.ldq, d.ldqt, d.lds, d.ldst = ldx, ldq, ldqt, lds, ldst
+    return d
+
+
+def gemm_epi_quant_plan_create(T, D, desc):
+    """Returns the plan handle; raises GemmEpiError with the status code."""
+    h = ctypes.c_void_p()
+    st = lib.gemm_epi_quant_plan_create(ctypes.byref(h), T, D, ctypes.byref(desc))
+    if st != GE_OK:
+        raise GemmEpiError(st, "gemm_epi_quant_plan_create")
+    return h
+
+
+def gemm_epi_quant_plan_destroy(plan):
+    lib.gemm_epi_quant_plan_destroy(plan)
+
+
+def prepare_quant_run(plan, x, q, scale, qt, scale_t, stream=None):
+    """As prepare_run, for gemm_epi_quant_run."""
+    args = (plan, _addr(x), _addr(q), _addr(scale), _addr(qt), _addr(scale_t), _stream(stream))
+    fn = lib.gemm_epi_quant_run
+    return lambda: fn(*args)
+
+
+def gemm_epi_quant_run(plan, x, q, scale, qt=None, scale_t=None, stream=None, check=True):
+    return _checked(prepare_quant_run(plan, x, q, scale, qt, scale_t, stream)(), "gemm_epi_quant_run", check)
+
+
+def make_fp8_desc(a, b, d, b_block="square", lda=0, ldb=0, ldd=0, lds_a=0, lds_b=0, timeout_ms=0, max_ctas=0,
+                  debug_flags=0):
+    r = ge_fp8_desc()
+    r.a = DTYPE[a] if isinstance(a, str) else a
+    r.b = DTYPE[b] if isinstance(b, str) else b
+    r.d = DTYPE[d] if isinstance(d, str) else d
+    r.b_block = BLOCK[b_block] if isinstance(b_block, str) else b_block
+    r.lda, r.ldb, r.ldd, r.lds_a, r.lds_b = lda, ldb, ldd, lds_a, lds_b
+    r.timeout_ms, r.max_ctas, r.debug_flags = timeout_ms, max_ctas, debug_flags
+    return r
+
+
+def gemm_epi_fp8_plan_create(M, N, K, desc):
+    """Returns the plan handle; raises GemmEpiError with the status code."""
+    h = ctypes.c_void_p()
+    st = lib.gemm_epi_fp8_plan_create(ctypes.byref(h), M, N, K, ctypes.byref(desc))
+    if st != GE_OK:
+        raise GemmEpiError(st, "gemm_epi_fp8_plan_create")
+    return h
+
+
+def gemm_epi_fp8_plan_destroy(plan):
+    lib.gemm_epi_fp8_plan_destroy(plan)
+
+
+def gemm_epi_fp8_workspace_bytes(plan):
+    return lib.gemm_epi_fp8_workspace_bytes(plan)
+
+
+def prepare_fp8_run(plan, A, scale_a, B, scale_b, C, D, workspace, workspace_bytes=None, stream=None):
+    """As prepare_run, for gemm_epi_fp8_run; workspace None where none is needed."""
+    if workspace is None and workspace_bytes is None:
+        workspace_bytes = 0
+    args = (plan, _addr(A), _addr(scale_a), _addr(B), _addr(scale_b), _addr(C), _addr(D), _addr(workspace),
+            _bytes_of(workspace, workspace_bytes), _stream(stream))
+    fn = lib.gemm_epi_fp8_run
+    return lambda: fn(*args)
+
+
+def gemm_epi_fp8_run(plan, A, scale_a, B, scale_b, C, D, workspace, workspace_bytes=None, stream=None, check=True):
+    return _checked(prepare_fp8_run(plan, A, scale_a, B, scale_b, C, D, workspace, workspace_bytes, stream)(),
+                    "gemm_epi_fp8_run", check)
+
+
+# --------------------------------------------- experts for a few tokens --
+
+def make_moe_desc(x, w, router, score="softmax", renormalise=True, act="silu", route_scale=1.0, ldx=0, ldy=0,
+                  timeout_ms=0, debug_flags=0):
+    d = ge_moe_desc()
+    d.x = DTYPE[x] if isinstance(x, str) else x
+    d.w = DTYPE[w] if isinstance(w, str) else w
+    d.router = DTYPE[router] if isinstance(router, str) else router
+    d.score = SCORE[score] if isinstance(score, str) else score
+    d.act = OP[act] if isinstance(act, str) else act
+    d.renormalise, d.route_scale = int(renormalise), route_scale
+    d.ldx, d.ldy, d.timeout_ms, d.debug_flags = ldx, ldy, timeout_ms, debug_flags
+    return d
+
+
+def gemm_epi_moe_plan_create(T, D, F, E, k, desc):
+    """Returns the plan handle; raises GemmEpiError with the status code."""
+    h = ctypes.c_void_p()
+    st = lib.gemm_epi_moe_plan_create(ctypes.byref(h), T, D, F, E, k, ctypes.byref(desc))
+    if st != GE_OK:
+        raise GemmEpiError(st, "gemm_epi_moe_plan_create")
+    return h
+
+
+def gemm_epi_moe_plan_destroy(plan):
+    lib.gemm_epi_moe_plan_destroy(plan)
+
+
+def gemm_epi_moe_workspace_bytes(plan):
+    return lib.gemm_epi_moe_workspace_bytes(plan)
+
+
+def prepare_moe_run(plan, x, w_router, bias, w_gate_up, s_gate_up, w_down, s_down, y, index, weight, workspace,
+                    workspace_bytes=None, stream=None):
+    """As prepare_run, for gemm_epi_moe_run."""
+    args = (plan, _addr(x), _addr(w_router), _addr(bias), _addr(w_gate_up), _addr(s_gate_up), _addr(w_down),
+            _addr(s_down), _addr(y), _addr(index), _addr(weight), _addr(workspace),
+            _bytes_of(workspace, workspace_bytes), _stream(stream))
+    fn = lib.gemm_epi_moe_run
+    return lambda: fn(*args)
+
+
+def gemm_epi_moe_run(plan, x, w_router, bias, w_gate_up, s_gate_up, w_down, s_down, y, index, weight, workspace,
+                     workspace_bytes=None, stream=None, check=True):
+    return _checked(prepare_moe_run(plan, x, w_router, bias, w_gate_up, s_gate_up, w_down, s_down, y, index, weight,
+                                    workspace, workspace_bytes, stream)(), "gemm_epi_moe_run", check)
 
 
 def gemm_epi_status_string(status):

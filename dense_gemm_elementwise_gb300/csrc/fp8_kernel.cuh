@@ -1,0 +1,394 @@
+// fp8_kernel.cuh -- the product of 8-bit floats with a scale for each block of 128, on sm_103a.
+//
+//   D = C + sum_j scale_a[j] scale_b[j] (A_j @ B_j^T)
+//
+// Persistent and warp-specialised: warp 0 loads operands (TMA, a ring of k-blocks of 128 bytes),
+// warp 1 allocates TMEM and issues tcgen05.mma.kind::f8f6f4, warps 2..9 hold the tile's sums.  The
+// scales differ from k-block to k-block, so each k-block is a product of its own: it
+// lands in one of two TMEM accumulators, and the epilogue warps add it, scaled, to fp32
+// registers (a thread has one row and half of the tile's columns) while the tensor unit fills
+// the other.  fp32 additions in registers are rounded, which the tensor unit's are not.
+//
+// Every wait is bounded, as in gemm_kernel.cuh.  No epilogue warp waits for another.
+#pragma once
+
+#include "fp8.cuh"
+#include "gemm_kernel.cuh"
+#include "xent_math.cuh"
+
+namespace ge {
+
+// barrier block
+constexpr uint32_t kFFull = 0, kFEmpty = 64, kFTmemFull = 128, kFTmemEmpty = 144, kFDrain = 160, kFTmemSlot = 168,
+                   kFAbort = 172;
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// n (up to 8) consecutive outputs of a row: 16 bytes at a time where rows allow it
+__device__ __forceinline__ float load_one(const void *p, int64_t at, int dt) {
+  if (dt == GE_F32) return static_cast<const float *>(p)[at];
+  const uint16_t v = static_cast<const uint16_t *>(p)[at];
+  return dt == GE_BF16 ? __uint_as_float(uint32_t(v) << 16) : __half2float(__ushort_as_half(v));
+}
+
+__device__ __forceinline__ void store_one(void *p, int64_t at, int dt, float v) {
+  if (dt == GE_F32) static_cast<float *>(p)[at] = v;
+  else static_cast<uint16_t *>(p)[at] = static_cast<uint16_t>(pack16(dt == GE_BF16, v, 0.f));
+}
+
+__device__ __forceinline__ void load16(const uint16_t *p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p)
+               : "memory");
+}
+
+__device__ __forceinline__ void store_words(void *p, const uint32_t *w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// 16 sums of a row, C added, into D
+__device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float (&v)[16]) {
+  const int left = p.N - n;
+  const int64_t at = int64_t(m) * p.ldd + n;
+  if (p.vec && left >= 16) {
+    if (p.dt == GE_F32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[8];
+        if (p.c) {
+          load16(reinterpret_cast<const uint16_t *>(static_cast<const float *>(p.c) + at + 8 * h), w);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[8 * h + e] += __uint_as_float(w[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[8 * h + e]);
+        store_words(static_cast<float *>(p.d) + at + 8 * h, w);
+      }
+    } else {
+      const bool bf16 = p.dt == GE_BF16;
+      uint32_t w[8];
+      if (p.c) {
+        load16(static_cast<const uint16_t *>(p.c) + at, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 c = bf16 ? make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u))
+                                : __half22float2(*reinterpret_cast<const __half2 *>(&w[e]));
+          v[2 * e] += c.x;
+          v[2 * e + 1] += c.y;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = pack16(bf16, v[2 * e], v[2 * e + 1]);
+      store_words(static_cast<uint16_t *>(p.d) + at, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (e < left) store_one(p.d, at + e, p.dt, v[e] + (p.c ? load_one(p.c, at + e, p.dt) : 0.f));
+}
+
+template <int CG, int BN, bool SQUARE>
+__global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
+  using T = TileCfg<CG, BN>;
+  constexpr int kEpi0 = 2;
+  constexpr int kCols = BN / 2;  // columns of an epilogue thread
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = CG > 1 ? cluster_ctarank() : 0u;
+  const int unit = blockIdx.x / CG, n_units = gridDim.x / CG;
+  const uint32_t bar = sb + p.off_bar;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + p.off_bar + kFTmemSlot);
+  volatile uint32_t *abort_flag = reinterpret_cast<volatile uint32_t *>(smem + p.off_bar + kFAbort);
+
+  if (warp == 0) {
+    if (lane < p.stages) {
+      mbar_init(bar + kFFull + 8 * lane, 1);
+      mbar_init(bar + kFEmpty + 8 * lane, 1);
+    }
+    if (lane < 2) {
+      mbar_init(bar + kFTmemFull + 8 * lane, 1);
+      mbar_init(bar + kFTmemEmpty + 8 * lane, 8 * CG);
+    }
+    if (lane == 0) {
+      mbar_init(bar + kFDrain, 1);
+      *abort_flag = 0u;
+      prefetch_tensormap(&p.tmA);
+      prefetch_tensormap(&p.tmB);
+    }
+    fence_mbarrier_init();
+    __syncwarp();
+  }
+  if (warp == 1) {
+    tmem_alloc<CG>(smem_u32(tmem_slot), T::kTmemCols);
+    tmem_relinquish<CG>();
+  }
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG > 1) cluster_sync_all(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t *>(tmem_slot);
+  griddep_wait();
+
+  const Waiter wt{abort_flag, p.status, p.timeout_ns};
+  const int tiles = p.num_m_blk * p.num_n_blk, num_units = tiles * p.slices;
+  struct Tile { int z, m0, n0, kb0, kb1; };
+  auto tile = [&](int at) {
+    Tile t;
+    t.z = at / tiles;
+    int l, mb, nb;
+    tile_coords(p.num_m_blk, p.num_n_blk, p.raster_group, at - t.z * tiles, l, mb, nb);
+    t.m0 = mb * T::kMmaM + static_cast<int>(rank) * BM;
+    t.n0 = nb * BN;
+    t.kb0 = t.z * p.kb_split;
+    t.kb1 = min(p.num_kb, t.kb0 + p.kb_split);
+    return t;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------ TMA producer --
+    if (lane == 0) {
+      int stage = 0, fills = 0, skipped = -1;
+      uint32_t phase = 0;
+      bool ok = true, skip = (p.debug_flags & GE_DEBUG_SKIP_FIRST_LOAD) != 0u;
+      auto next_stage = [&]() {
+        ++fills;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int at = unit; ok && at < num_units; at += n_units) {
+        const Tile t = tile(at);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wt.wait(bar + kFEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (skip) {
+            skip = false;
+            skipped = fills;
+            next_stage();
+            continue;
+          }
+          const uint32_t full = bar + kFFull + 8 * stage;
+          const uint32_t sa = sb + stage * T::kABytes, sbb = sb + p.off_B + stage * T::kBBytes;
+          const int n0 = t.n0 + static_cast<int>(rank) * T::kBnLocal;
+          if constexpr (CG == 2) {
+            const uint32_t fb = mapa_shared(full, 0);
+            if (rank == 0) mbar_arrive_expect_tx(full, CG * (T::kABytes + T::kBBytes));
+            tma_load_3d_pair(sa, &p.tmA, fb, kb * kF8Block, t.m0, 0);
+            tma_load_3d_pair(sbb, &p.tmB, fb, kb * kF8Block, n0, 0);
+          } else {
+            // few rows: only theirs are loaded; what the others' accumulators then hold is not read
+            mbar_arrive_expect_tx(full, p.a_rows * 128 + T::kBBytes);
+            tma_load_3d(sa, &p.tmA, full, kb * kF8Block, t.m0, 0);
+            tma_load_3d(sbb, &p.tmB, full, kb * kF8Block, n0, 0);
+          }
+          next_stage();
+        }
+      }
+      griddep_launch_dependents();
+      if (ok) {
+        for (int i = 0; i < p.stages; ++i) {
+          if (!wt.wait(bar + kFEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
+            ok = false;
+            break;
+          }
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        for (int f = max(fills - p.stages, 0); f < fills; ++f)
+          if (f != skipped) wt.drain(bar + kFFull + 8 * (f % p.stages), static_cast<uint32_t>(f / p.stages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------- MMA issuer --
+    if (lane == 0 && rank == 0) {
+      const uint64_t a_desc0 = smem_desc_sw128(sb, 16u, 1024u), b_desc0 = smem_desc_sw128(sb + p.off_B, 16u, 1024u);
+      const uint32_t id = make_idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, T::kMmaM, BN);
+      int stage = 0, abuf = 0;
+      uint32_t phase = 0, aphase = 0;
+      bool ok = true;
+      for (int at = unit; ok && at < num_units; at += n_units) {
+        const Tile t = tile(at);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          if (!wt.wait(bar + kFFull + 8 * stage, phase, SITE_MMA_FULL) ||
+              !wt.wait<CG == 2>(bar + kFTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * BN);
+          const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (T::kABytes >> 4));
+          const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage * (T::kBBytes >> 4));
+#pragma unroll
+          for (int k = 0; k < kF8Block / 32; ++k) umma_f8<CG>(d, ad + 2 * k, bd + 2 * k, id, k != 0 ? 1u : 0u);
+          umma_commit<CG>(bar + kFEmpty + 8 * stage);
+          umma_commit<CG>(bar + kFTmemFull + 8 * abuf);
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          abuf ^= 1;
+          if (abuf == 0) aphase ^= 1u;
+        }
+      }
+      if (ok) {
+        for (int i = 0; i < 2; ++i) {
+          if (!wt.wait<CG == 2>(bar + kFTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) break;
+          abuf ^= 1;
+          if (abuf == 0) aphase ^= 1u;
+        }
+      } else {
+        umma_commit<CG>(bar + kFDrain);
+        wt.drain(bar + kFDrain, 0u);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue --
+    const int q = warp & 3;             // TMEM lane quarter
+    const int grp = (warp - kEpi0) >> 2;  // half of the columns
+    const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(grp * kCols);
+    float *my_sb = reinterpret_cast<float *>(smem + p.off_bar + kF8BarBytes) + (warp - kEpi0) * 2 * kCols;
+    int abuf = 0, half = 0;
+    uint32_t aphase = 0;
+    bool ok = true;
+    for (int at = unit; ok && at < num_units; at += n_units) {
+      const Tile t = tile(at);
+      const int m = t.m0 + q * 32 + lane, n0 = t.n0 + grp * kCols;
+      const bool live = m < p.M;
+      // the next k-block's scales are on their way while this one's product finishes
+      constexpr int kMine = SQUARE ? 1 : kCols / 32;
+      float sa_next, sb_next[kMine];
+      auto fetch = [&](int kb) {
+        sa_next = live && kb < t.kb1 ? __ldg(p.sa + int64_t(kb) * p.lds_a + m) : 0.f;
+        if constexpr (SQUARE) {
+          sb_next[0] = n0 < p.N && kb < t.kb1 ? __ldg(p.sb + int64_t(kb) * p.lds_b + n0 / kF8Block) : 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) {
+            const int n = n0 + i * 32 + lane;
+            sb_next[i] = n < p.N && kb < t.kb1 ? __ldg(p.sb + int64_t(kb) * p.lds_b + n) : 0.f;
+          }
+        }
+      };
+      float2 acc[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      fetch(t.kb0);
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+        float *sb_now = my_sb + half * kCols;
+        half ^= 1;
+        float s = sa_next;
+        if constexpr (SQUARE) {
+          s *= sb_next[0];
+        } else {
+          // two deep: the warp read this half two k-blocks ago, before its last __syncwarp
+#pragma unroll
+          for (int i = 0; i < kMine; ++i) sb_now[i * 32 + lane] = sb_next[i];
+          __syncwarp();
+        }
+        fetch(kb + 1);
+        const float2 s2 = make_float2(s, s);
+        ok = __all_sync(0xffffffffu, wt.wait(bar + kFTmemFull + 8 * abuf, aphase, SITE_EPI_TMEM_FULL));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t src = tq + static_cast<uint32_t>(abuf * BN);
+        // 16 columns are on their way while the 16 before them are added
+        float v[2][16];
+        tmem_ld16(src, v[0]);
+#pragma unroll
+        for (int c = 0; c < kCols / 16; ++c) {
+          tmem_wait_ld();
+          if (c + 1 < kCols / 16) {
+            tmem_ld16(src + 16 * (c + 1), v[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              const uint32_t tb = bar + kFTmemEmpty + 8 * abuf;
+              if constexpr (CG == 2) mbar_arrive_remote(mapa_shared(tb, 0));
+              else mbar_arrive(tb);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float2 x = make_float2(v[c & 1][2 * e], v[c & 1][2 * e + 1]);
+            if constexpr (!SQUARE) x = mul2(x, *reinterpret_cast<const float2 *>(sb_now + 16 * c + 2 * e));
+            acc[8 * c + e] = fma2(x, s2, acc[8 * c + e]);
+          }
+        }
+        abuf ^= 1;
+        if (abuf == 0) aphase ^= 1u;
+      }
+      if (!ok) break;
+      if (!live) continue;
+#pragma unroll
+      for (int c = 0; c < kCols / 16; ++c) {
+        const int n = n0 + 16 * c;
+        if (n >= p.N) break;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[2 * e] = acc[8 * c + e].x;
+          v[2 * e + 1] = acc[8 * c + e].y;
+        }
+        if (p.part) {  // rows of whole tiles
+          float *o = p.part + (int64_t(t.z) * p.M + m) * p.ld_part + n;
+          store_words(o, reinterpret_cast<const uint32_t *>(v));
+          store_words(o + 8, reinterpret_cast<const uint32_t *>(v + 8));
+        } else {
+          finish16(p, m, n, v);
+        }
+      }
+    }
+    __syncwarp();
+  }
+
+  // -------------------------------------------------------------- teardown --
+  __syncwarp();
+  tc_fence_before();
+  if constexpr (CG > 1) cluster_sync_all(); else __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<CG>(tmem_base, T::kTmemCols);
+  }
+}
+
+template <int CG, int BN>
+const void *pick_fp8(bool square) {
+  return square ? reinterpret_cast<const void *>(fp8_kernel<CG, BN, true>)
+                : reinterpret_cast<const void *>(fp8_kernel<CG, BN, false>);
+}
+
+}  // namespace ge

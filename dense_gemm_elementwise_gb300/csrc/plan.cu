@@ -35,7 +35,7 @@ __device__ uint32_t g_ge_status[4];
 
 namespace {
 
-int esize(int dt) { return dt == GE_F32 ? 4 : 2; }
+int esize(int dt) { return dt == GE_F32 ? 4 : dt == GE_E4M3 || dt == GE_E5M2 ? 1 : 2; }
 bool valid_dtype(int dt) { return dt == GE_F16 || dt == GE_BF16 || dt == GE_F32; }
 
 bool log_enabled() {
@@ -157,6 +157,7 @@ EncodeTiledFn encode_fn() {
 }
 
 CUtensorMapDataType tma_dtype(int dt) {
+  if (esize(dt) == 1) return CU_TENSOR_MAP_DATA_TYPE_UINT8;
   return dt == GE_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                       : (dt == GE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }

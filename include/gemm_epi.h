@@ -77,7 +77,13 @@ extern "C" {
 #define GE_MAX_SCALARS 16 /* scalar slots */
 
 /* element types */
-typedef enum { GE_F16 = 0, GE_BF16 = 1, GE_F32 = 2 } ge_dtype;
+typedef enum {
+  GE_F16 = 0,
+  GE_BF16 = 1,
+  GE_F32 = 2,
+  GE_E4M3 = 3, /* 8 bits, largest 448, no infinities: block-scaled products and expert layers only */
+  GE_E5M2 = 4  /* 8 bits, largest 57344: the same                                                  */
+} ge_dtype;
 
 /* DAG node kinds.  `a`, `b` name earlier nodes; `slot` picks the operand. */
 typedef enum {
@@ -564,6 +570,177 @@ int gemm_epi_norm_grad(gemm_epi_norm_plan *plan, const void *dy, const void *dh,
                        void *workspace, size_t workspace_bytes, void *stream);
 
 void gemm_epi_norm_plan_destroy(gemm_epi_norm_plan *plan);
+
+/*
+ * 8-bit floats with a scale for each block of 128.
+ *
+ * A matrix is held as values q (GE_E4M3 or GE_E5M2) and fp32 scales: x ~ q * scale of
+ * its block.  GE_BLOCK_ROW: a block is 128 consecutive elements of a row.
+ * GE_BLOCK_SQUARE: 128 rows by 128 columns.  The last blocks of a row or column may be
+ * shorter.  Scales lie with those of one block of columns side by side:
+ *   GE_BLOCK_ROW     scale[j * lds + i]        row i, columns 128 j .. 128 j + 127
+ *   GE_BLOCK_SQUARE  scale[j * lds + i / 128]
+ *
+ * gemm_epi_quant_run makes them, and those of the transposed matrix, from
+ * one reading of it:
+ *   scale = max(largest |x| of the block / largest q, 2^-126)      (fp32)
+ *   q     = x * (1 / scale), rounded to nearest even, within +-largest q
+ * NaN stays at its place; an infinity makes its block's scale infinite, so that what the block
+ * stands for is NaN throughout.
+ */
+typedef enum { GE_BLOCK_ROW = 0, GE_BLOCK_SQUARE = 1 } ge_block;
+
+typedef struct {
+  int32_t x;        /* GE_F16, GE_BF16 or GE_F32                                              */
+  int32_t q;        /* GE_E4M3 or GE_E5M2                                                     */
+  int32_t block;    /* ge_block, of q and of qt                                               */
+  int32_t reserved; /* 0                                                                      */
+  int64_t ldx;      /* row pitch of x in elements; 0 = D                                      */
+  int64_t ldq;      /* row pitch of q (T, D) in bytes, a multiple of 16; 0 = D                */
+  int64_t ldqt;     /* row pitch of qt (D, T) in bytes, a multiple of 16; 0 = T               */
+  int64_t lds;      /* scale is (ceil(D / 128), T or ceil(T / 128)); 0 = packed               */
+  int64_t ldst;     /* scale_t is (ceil(T / 128), D or ceil(D / 128)); 0 = packed             */
+} ge_quant_desc;
+
+typedef struct gemm_epi_quant_plan gemm_epi_quant_plan;
+
+/* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID (NULL, bad block or
+ * option), _UNSUPPORTED (types), _SHAPE (T or D <= 0 or above 2^31 - 1, a pitch too small),
+ * _MISALIGNED (a pitch of q or qt that is given and is no multiple of 16), _ARCH. */
+int gemm_epi_quant_plan_create(gemm_epi_quant_plan **plan, int64_t T, int64_t D,
+                               const ge_quant_desc *desc);
+
+/*
+ * One launch on `stream`.  q with scale, or qt with scale_t, may be NULL together; a pitch
+ * (D or T by default) that is no multiple of 16 is refused for the one that is asked for.
+ * Bytes between the rows of q and qt are left as they are.  Outputs must not overlap x.
+ * Errors: GE_ERR_INVALID, _MISSING_ARG, _MISALIGNED (a pointer that is not 16-byte aligned,
+ * a pitch), _CUDA.
+ */
+int gemm_epi_quant_run(gemm_epi_quant_plan *plan, const void *x, void *q, float *scale, void *qt,
+                       float *scale_t, void *stream);
+
+void gemm_epi_quant_plan_destroy(gemm_epi_quant_plan *plan);
+
+/*
+ * Product of two such matrices:
+ *   D = C + sum over blocks j of 128 columns  scale_a[j] scale_b[j] (A_j @ B_j^T)
+ * A is (M, K) with GE_BLOCK_ROW scales, B is (N, K) with scales of either kind, both with K
+ * contiguous and pitches of whole 16 bytes; C and D are (M, N) with any pitch ldd.  A linear
+ * layer's three products are this call: y = x W^T with q of x (ROW) and of W (SQUARE);
+ * dx = dy W with q of dy (ROW) and qt of W (SQUARE); dW = dy^T x with qt of dy (ROW) and qt of
+ * x (ROW), C = D = the gradient's sum so far.
+ *
+ * Products are exact and summed in fp32 over a block, each block's sum is scaled and
+ * added in fp32, C is added last, and the result is rounded once.  Results are bit-for-bit
+ * repeatable for a given plan and device.
+ */
+typedef struct {
+  int32_t a, b;         /* GE_E4M3 or GE_E5M2 each                                            */
+  int32_t d;            /* GE_F16, GE_BF16 or GE_F32: C and D                                 */
+  int32_t b_block;      /* ge_block of B's scales                                             */
+  int32_t timeout_ms;   /* 0 = 1000; bound on every device-side wait                          */
+  int32_t max_ctas;     /* 0 = one CTA per SM, else a cap on the product's grid               */
+  uint32_t debug_flags; /* 0; GE_DEBUG_SKIP_FIRST_LOAD for tests only                         */
+  int32_t reserved;     /* 0                                                                  */
+  int64_t lda, ldb;     /* row pitches in bytes, multiples of 16; 0 = K                       */
+  int64_t ldd;          /* row pitch of C and D in elements; 0 = N                            */
+  int64_t lds_a;        /* pitch of scale_a (ceil(K / 128), M); 0 = M                         */
+  int64_t lds_b;        /* ... of scale_b (ceil(K / 128), N or ceil(N / 128)); 0 = packed     */
+} ge_fp8_desc;
+
+typedef struct gemm_epi_fp8_plan gemm_epi_fp8_plan;
+
+/* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID, _UNSUPPORTED (types),
+ * _SHAPE (M, N or K <= 0 or above 2^31 - 1, a pitch too small), _MISALIGNED (lda, ldb), _ARCH,
+ * _SMEM, _CUDA. */
+int gemm_epi_fp8_plan_create(gemm_epi_fp8_plan **plan, int64_t M, int64_t N, int64_t K,
+                             const ge_fp8_desc *desc);
+
+/* Bytes of caller-owned device workspace (0: none is needed). */
+size_t gemm_epi_fp8_workspace_bytes(const gemm_epi_fp8_plan *plan);
+
+/*
+ * Run on `stream`: one or two launches, asynchronous, nothing allocates; any run can be captured
+ * into a CUDA graph.  C may be NULL (0) or D itself.  D must not overlap the other inputs.
+ * Errors: GE_ERR_INVALID, _MISSING_ARG, _MISALIGNED (A, B, C, D or the workspace not 16-byte aligned,
+ * scales not 4-byte), _WORKSPACE, _CUDA; a device-side timeout is reported later by
+ * gemm_epi_last_error.
+ */
+int gemm_epi_fp8_run(gemm_epi_fp8_plan *plan, const void *A, const float *scale_a, const void *B,
+                     const float *scale_b, const void *C, void *D, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+void gemm_epi_fp8_plan_destroy(gemm_epi_fp8_plan *plan);
+
+/*
+ * A mixture-of-experts layer for a few tokens, whole, in two launches: its experts' weights
+ * are read once for all tokens that chose them.
+ *
+ *   l      = x @ w_router^T                             (T, E)
+ *   p      = softmax(l) over the experts (GE_SCORE_SOFTMAX) or sigmoid(l) (GE_SCORE_SIGMOID)
+ *   index  = the k experts of largest l, or of largest p + bias where there is a bias, in
+ *            falling order, ties to the lowest index
+ *   weight = p[index] (/ their sum, with renormalise) * route_scale
+ *   y      = sum_j weight_j w_down[e_j] @ (act(w_gate[e_j] @ x) * (w_up[e_j] @ x))
+ *
+ * x and y are (T, D) of type `x`, w_router (E, D) of type `router`, bias (E,) fp32,
+ * w_gate_up (E, 2 F, D): an expert's F gate rows, then its F up rows; w_down (E, D, F),
+ * both packed, of type `w`.  With `w` GE_E4M3 or GE_E5M2 they have GE_BLOCK_SQUARE scales,
+ * s_gate_up (E, ceil(D / 128), ceil(2 F / 128)) and s_down (E, ceil(F / 128), ceil(D / 128)), packed:
+ * what gemm_epi_quant_run makes of each expert's matrix.  F then has to be a multiple of
+ * 16 and so has D, otherwise of 8.
+ *
+ * Arithmetic: logits in fp32 pairs (about 2^-40), so that the choice is that of exact logits;
+ * the experts' products are exact and summed in fp32; act(gate) * up is passed on as the sum of two
+ * values of type `x` (fp16: infinite above 65504); one rounding per output.  A NaN in a token
+ * reaches that token alone.  Results are bit-for-bit repeatable for a given plan and device.
+ */
+typedef enum { GE_SCORE_SOFTMAX = 0, GE_SCORE_SIGMOID = 1 } ge_score;
+#define GE_MOE_MAX_TOKENS 128
+#define GE_MOE_MAX_EXPERTS 512
+#define GE_MOE_MAX_K 16
+
+typedef struct {
+  int32_t x;           /* GE_F16 or GE_BF16                                                   */
+  int32_t w;           /* the experts' weights: as x, GE_E4M3 or GE_E5M2                      */
+  int32_t router;      /* as x, or GE_F32                                                     */
+  int32_t score;       /* ge_score                                                            */
+  int32_t renormalise; /* 0 or 1                                                              */
+  int32_t act;         /* GE_SILU, GE_GELU (exact) or GE_RELU; 0 = GE_SILU                    */
+  int32_t timeout_ms;  /* 0 = 1000; bound on every device-side wait                           */
+  uint32_t debug_flags; /* 0; GE_DEBUG_SKIP_FIRST_LOAD for tests only: the first unit of the gate
+                           and up products is left out, and those that wait for it give up    */
+  float route_scale;   /* 0 = 1                                                               */
+  int32_t reserved;    /* 0                                                                   */
+  int64_t ldx, ldy;    /* row pitches in elements, multiples of 8; 0 = D                      */
+} ge_moe_desc;
+
+typedef struct gemm_epi_moe_plan gemm_epi_moe_plan;
+
+/* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID, _UNSUPPORTED (types,
+ * activation), _SHAPE (T outside 1..GE_MOE_MAX_TOKENS, E outside 1..GE_MOE_MAX_EXPERTS, k outside
+ * 1..min(E, GE_MOE_MAX_K), D or F <= 0 or above 2^20, a pitch below D), _MISALIGNED (D, F or
+ * a pitch not as above), _ARCH, _CUDA. */
+int gemm_epi_moe_plan_create(gemm_epi_moe_plan **plan, int64_t T, int64_t D, int64_t F, int64_t E,
+                             int64_t k, const ge_moe_desc *desc);
+
+/* Bytes of caller-owned device workspace, for one run at a time. */
+size_t gemm_epi_moe_workspace_bytes(const gemm_epi_moe_plan *plan);
+
+/*
+ * Run on `stream`, asynchronous; nothing allocates, and any run can be captured into a CUDA graph.
+ * bias may be NULL; s_gate_up and s_down must be given exactly with 8-bit weights; index (T, k) int32
+ * and weight (T, k) fp32 may be NULL.  Outputs must not overlap inputs.  Errors: GE_ERR_INVALID,
+ * _MISSING_ARG, _MISALIGNED (a pointer that is not 16-byte aligned), _WORKSPACE, _CUDA; a device-side
+ * timeout is reported later by gemm_epi_last_error.
+ */
+int gemm_epi_moe_run(gemm_epi_moe_plan *plan, const void *x, const void *w_router, const float *bias,
+                     const void *w_gate_up, const float *s_gate_up, const void *w_down,
+                     const float *s_down, void *y, int32_t *index, float *weight, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+void gemm_epi_moe_plan_destroy(gemm_epi_moe_plan *plan);
 
 /* Static name of a status code ("GE_OK", ...); never NULL. */
 const char *gemm_epi_status_string(int status);
