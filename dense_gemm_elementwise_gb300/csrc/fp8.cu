@@ -82,11 +82,17 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   p.raster_group = num_m <= 16 ? static_cast<int32_t>(num_m) : 12;
   p.a_rows = pl->cg == 1 ? static_cast<int32_t>(std::min<int64_t>(128, round_up(M, 8))) : 128;
   const int stage = 128 * 128 + 128 * bn / pl->cg;
-  const int fixed = 1024 + static_cast<int>(kF8BarBytes + fp8_scale_bytes(bn));
+  const int fixed = 1024 + static_cast<int>(kF8BarBytes + fp8_scale_bytes(bn, square));
   p.stages = std::min(kMaxStages, (max_smem - fixed) / stage);
   if (p.stages < 2) return GE_ERR_SMEM;
   p.off_B = static_cast<uint32_t>(p.stages * 128 * 128);
   p.off_bar = static_cast<uint32_t>(p.stages * stage);
+  // the kernel's warps pass registers on, which have to be there
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, pl->fn) != cudaSuccess || fa.numRegs < kF8Regs) {
+    cudaGetLastError();
+    return GE_ERR_CUDA;
+  }
   // all of an SM's shared memory, so that its TMEM is this CTA's alone
   pl->smem = max_smem;
   if (cudaFuncSetAttribute(pl->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess) {
@@ -176,9 +182,8 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
   if (need && (!workspace || workspace_bytes < need)) return GE_ERR_WORKSPACE;
   if (need && !is_aligned16(workspace)) return GE_ERR_MISALIGNED;
   Fp8Params p = pl->p;
-  const int bn = 128 * pl->cg;
   if (!encode_rows(&p.tmA, GE_E4M3, A, pl->K, pl->M, 1, pl->d.lda, pl->d.lda * pl->M, kF8Block, p.a_rows) ||
-      !encode_rows(&p.tmB, GE_E4M3, B, pl->K, pl->N, 1, pl->d.ldb, pl->d.ldb * pl->N, kF8Block, bn / pl->cg))
+      !encode_rows(&p.tmB, GE_E4M3, B, pl->K, pl->N, 1, pl->d.ldb, pl->d.ldb * pl->N, kF8Block, 128))
     return GE_ERR_CUDA;
   p.sa = scale_a;
   p.sb = scale_b;

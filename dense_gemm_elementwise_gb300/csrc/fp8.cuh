@@ -8,7 +8,7 @@ namespace ge {
 constexpr int kF8Block = 128;  // columns that share a scale: one k-block, one 128-byte swizzle row
 
 struct Fp8Params {
-  CUtensorMap tmA, tmB;    // (K, M), (K, N): boxes of 128 bytes by 128 rows (A) and BN / CG (B)
+  CUtensorMap tmA, tmB;    // (K, M), (K, N): boxes of 128 bytes by up to 128 rows
   uint32_t *status;
   uint64_t timeout_ns;
   const float *sa, *sb;    // [k-block][row], [k-block][column or column block]
@@ -27,10 +27,18 @@ struct Fp8Params {
   uint32_t off_B, off_bar;
 };
 
-constexpr int kF8Threads = 32 * (2 + 8);  // producer, MMA, 8 epilogue warps
+constexpr int kF8Epi0 = 4;                // warps: producer, two MMA, scales, 8 epilogue
+constexpr int kF8Threads = 32 * (kF8Epi0 + 8);
+// Registers of a thread: all start with 168; the first four warps give some of theirs to the others, whose 128
+// sums and 64 values on their way would not fit otherwise.
+constexpr int kF8Regs = 168, kF8RegsLess = 72, kF8RegsMore = 216;
+static_assert(128 * kF8RegsLess + 256 * kF8RegsMore <= kF8Threads * kF8Regs, "registers to give away");
 constexpr uint32_t kF8BarBytes = 256;
-// B's row scales of a k-block, a copy for each epilogue warp of its half of the columns, two deep
-__host__ __device__ constexpr uint32_t fp8_scale_bytes(int bn) { return 8u * 2u * static_cast<uint32_t>(bn / 2) * 4u; }
+// Scales of some k-blocks, two deep: the tile's rows', and its column blocks' or columns'.
+__host__ __device__ constexpr int fp8_batch(bool square) { return square ? 8 : 4; }
+__host__ __device__ constexpr uint32_t fp8_scale_bytes(int bn, bool square) {
+  return 2u * 4u * static_cast<uint32_t>(fp8_batch(square)) * static_cast<uint32_t>(128 + (square ? 2 : bn));
+}
 
 // square: B's scales are one for each 128 columns
 const void *fp8_kernel_cg1(bool square);  // 128 x 128 tiles, one CTA

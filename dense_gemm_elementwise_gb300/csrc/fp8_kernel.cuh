@@ -2,12 +2,28 @@
 //
 //   D = C + sum_j scale_a[j] scale_b[j] (A_j @ B_j^T)
 //
-// Persistent and warp-specialised: warp 0 loads operands (TMA, a ring of k-blocks of 128 bytes),
-// warp 1 allocates TMEM and issues tcgen05.mma.kind::f8f6f4, warps 2..9 hold the tile's sums.  The
-// scales differ from k-block to k-block, so each k-block is a product of its own: it
+// Persistent and warp-specialised: warp 0 loads operands (TMA, a ring of k-blocks of 128 bytes), warps 1 and
+// 2 issue tcgen05.mma.kind::f8f6f4 (1 also allocates TMEM), warp 3 brings the scales, warps 4..11 hold the
+// tile's sums.  The scales differ from k-block to k-block, so each k-block is a product of its own: it
 // lands in one of two TMEM accumulators, and the epilogue warps add it, scaled, to fp32
 // registers (a thread has one row and half of the tile's columns) while the tensor unit fills
 // the other.  fp32 additions in registers are rounded, which the tensor unit's are not.
+//
+// That is a hand-over between the tensor unit and the epilogue for every 512 clocks of tensor work, whose
+// latencies bound the kernel (8192^3: 412 us, 2.67 PFLOP/s; without hand-overs, one sum over all of K, 375):
+//   * Accumulators are handed back by arrivals without release and waited for without acquire; nothing
+//     but tensor memory is passed on, which the tcgen05 fences order.  (975 -> 519 us: release and acquire at
+//     cluster scope take about 1000 clocks each.)
+//   * One commit for each k-block: a stage's "done" barrier tells the producer that the stage is
+//     free and the epilogue that the accumulator is complete.  (It cannot be a phase ahead of an epilogue warp:
+//     that takes the stage's next k-block, for which the warps have to hand back this accumulator.)
+//   * Two threads issue, one for each accumulator: a k-block costs such a thread about 1000 clocks, most of
+//     them the latencies of its looks at barriers and of its issues.  (Four accumulators of half the columns
+//     took 490 us and more: A is then read twice from shared memory.)
+//   * Scales come through shared memory, some k-blocks at a time: loaded by the epilogue itself, a
+//     k-block ahead, they came too late (with constants in their place it took 30 us less).
+//   * 32 columns are on their way to an epilogue thread while it adds 32 others, which its registers
+//     have room for because the other warps give theirs away.  (Sixteen epilogue warps took 530 us.)
 //
 // Every wait is bounded, as in gemm_kernel.cuh.  No epilogue warp waits for another.
 #pragma once
@@ -19,8 +35,24 @@
 namespace ge {
 
 // barrier block
-constexpr uint32_t kFFull = 0, kFEmpty = 64, kFTmemFull = 128, kFTmemEmpty = 144, kFDrain = 160, kFTmemSlot = 168,
-                   kFAbort = 172;
+constexpr uint32_t kFFull = 0, kFDone = 64, kFTmemEmpty = 128, kFDrain = 144, kFScaleFull = 160, kFScaleEmpty = 176,
+                   kFTmemSlot = 192, kFAbort = 196;
+
+// A wait that is short as a rule: the clock is looked at when it is not.
+__device__ __forceinline__ bool wait_soon(const Waiter &wt, uint32_t bar, uint32_t parity, uint32_t site) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wt.wait(bar, parity, site);
+}
+
+// the same for an accumulator that both CTAs of a pair hand back (see above)
+__device__ __forceinline__ bool wait_soon_relaxed(const Waiter &wt, uint32_t bar, uint32_t parity, uint32_t site) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait_relaxed(bar, parity)) return true;
+  return wt.wait<true>(bar, parity, site);
+}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -114,8 +146,9 @@ __device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float
 template <int CG, int BN, bool SQUARE>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
   using T = TileCfg<CG, BN>;
-  constexpr int kEpi0 = 2;
+  constexpr int kEpi0 = kF8Epi0;
   constexpr int kCols = BN / 2;  // columns of an epilogue thread
+  constexpr int kBatch = fp8_batch(SQUARE), kSb = SQUARE ? 2 : BN, kBatchFloats = kBatch * (128 + kSb);
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sb = smem_u32(smem);
@@ -129,14 +162,15 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
   if (warp == 0) {
     if (lane < p.stages) {
       mbar_init(bar + kFFull + 8 * lane, 1);
-      mbar_init(bar + kFEmpty + 8 * lane, 1);
+      mbar_init(bar + kFDone + 8 * lane, 1);
     }
+    if (lane < 2) mbar_init(bar + kFTmemEmpty + 8 * lane, 8 * CG);
     if (lane < 2) {
-      mbar_init(bar + kFTmemFull + 8 * lane, 1);
-      mbar_init(bar + kFTmemEmpty + 8 * lane, 8 * CG);
+      mbar_init(bar + kFDrain + 8 * lane, 1);
+      mbar_init(bar + kFScaleFull + 8 * lane, 1);
+      mbar_init(bar + kFScaleEmpty + 8 * lane, 8);
     }
     if (lane == 0) {
-      mbar_init(bar + kFDrain, 1);
       *abort_flag = 0u;
       prefetch_tensormap(&p.tmA);
       prefetch_tensormap(&p.tmB);
@@ -170,6 +204,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
     return t;
   };
 
+  // (the registers that each side may use differ from here on: nothing runs on both before the end)
+  if (warp < kEpi0) {
+  set_registers<false, kF8RegsLess>();
   if (warp == 0) {
     // ------------------------------------------------------ TMA producer --
     if (lane == 0) {
@@ -186,7 +223,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
       for (int at = unit; ok && at < num_units; at += n_units) {
         const Tile t = tile(at);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wt.wait(bar + kFEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
+          if (!wait_soon(wt, bar + kFDone + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
             ok = false;
             break;
           }
@@ -198,9 +235,9 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
           }
           const uint32_t full = bar + kFFull + 8 * stage;
           const uint32_t sa = sb + stage * T::kABytes, sbb = sb + p.off_B + stage * T::kBBytes;
-          const int n0 = t.n0 + static_cast<int>(rank) * T::kBnLocal;
           if constexpr (CG == 2) {
             const uint32_t fb = mapa_shared(full, 0);
+            const int n0 = t.n0 + static_cast<int>(rank) * (BN / 2);
             if (rank == 0) mbar_arrive_expect_tx(full, CG * (T::kABytes + T::kBBytes));
             tma_load_3d_pair(sa, &p.tmA, fb, kb * kF8Block, t.m0, 0);
             tma_load_3d_pair(sbb, &p.tmB, fb, kb * kF8Block, n0, 0);
@@ -208,7 +245,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
             // few rows: only theirs are loaded; what the others' accumulators then hold is not read
             mbar_arrive_expect_tx(full, p.a_rows * 128 + T::kBBytes);
             tma_load_3d(sa, &p.tmA, full, kb * kF8Block, t.m0, 0);
-            tma_load_3d(sbb, &p.tmB, full, kb * kF8Block, n0, 0);
+            tma_load_3d(sbb, &p.tmB, full, kb * kF8Block, t.n0, 0);
           }
           next_stage();
         }
@@ -216,7 +253,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
       griddep_launch_dependents();
       if (ok) {
         for (int i = 0; i < p.stages; ++i) {
-          if (!wt.wait(bar + kFEmpty + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
+          if (!wait_soon(wt, bar + kFDone + 8 * stage, phase ^ 1u, SITE_PRODUCER_EMPTY)) {
             ok = false;
             break;
           }
@@ -231,125 +268,173 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
           if (f != skipped) wt.drain(bar + kFFull + 8 * (f % p.stages), static_cast<uint32_t>(f / p.stages) & 1u);
       }
     }
-  } else if (warp == 1) {
-    // -------------------------------------------------------- MMA issuer --
+  } else if (warp == 1 || warp == 2) {
+    // ------------------------------------------------------- MMA issuers --
     if (lane == 0 && rank == 0) {
       const uint64_t a_desc0 = smem_desc_sw128(sb, 16u, 1024u), b_desc0 = smem_desc_sw128(sb + p.off_B, 16u, 1024u);
       const uint32_t id = make_idesc_f8(p.a_e5m2 != 0, p.b_e5m2 != 0, T::kMmaM, BN);
-      int stage = 0, abuf = 0;
+      // this thread's accumulator takes every other k-block of the CTA's
+      const int mine = warp - 1;
+      const uint32_t d = tmem_base + static_cast<uint32_t>(mine * BN), empty = bar + kFTmemEmpty + 8 * mine;
+      int stage = 0, count = 0;
       uint32_t phase = 0, aphase = 0;
       bool ok = true;
       for (int at = unit; ok && at < num_units; at += n_units) {
         const Tile t = tile(at);
-        for (int kb = t.kb0; kb < t.kb1; ++kb) {
-          if (!wt.wait(bar + kFFull + 8 * stage, phase, SITE_MMA_FULL) ||
-              !wt.wait<CG == 2>(bar + kFTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem_base + static_cast<uint32_t>(abuf * BN);
-          const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (T::kABytes >> 4));
-          const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage * (T::kBBytes >> 4));
+        for (int kb = t.kb0; kb < t.kb1; ++kb, ++count) {
+          if ((count & 1) == mine) {
+            if (!wait_soon(wt, bar + kFFull + 8 * stage, phase, SITE_MMA_FULL) ||
+                !wait_soon_relaxed(wt, empty, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) {
+              ok = false;
+              break;
+            }
+            aphase ^= 1u;
+            tc_fence_after();
+            const uint64_t ad = a_desc0 + static_cast<uint32_t>(stage * (T::kABytes >> 4));
+            const uint64_t bd = b_desc0 + static_cast<uint32_t>(stage * (T::kBBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < kF8Block / 32; ++k) umma_f8<CG>(d, ad + 2 * k, bd + 2 * k, id, k != 0 ? 1u : 0u);
-          umma_commit<CG>(bar + kFEmpty + 8 * stage);
-          umma_commit<CG>(bar + kFTmemFull + 8 * abuf);
+            for (int k = 0; k < kF8Block / 32; ++k) umma_f8<CG>(d, ad + 2 * k, bd + 2 * k, id, k != 0 ? 1u : 0u);
+            umma_commit<CG>(bar + kFDone + 8 * stage);
+          }
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1u;
           }
-          abuf ^= 1;
-          if (abuf == 0) aphase ^= 1u;
         }
       }
       if (ok) {
-        for (int i = 0; i < 2; ++i) {
-          if (!wt.wait<CG == 2>(bar + kFTmemEmpty + 8 * abuf, aphase ^ 1u, SITE_MMA_TMEM_EMPTY)) break;
-          abuf ^= 1;
-          if (abuf == 0) aphase ^= 1u;
-        }
+        wt.wait<CG == 2>(empty, aphase ^ 1u, SITE_MMA_TMEM_EMPTY);
       } else {
-        umma_commit<CG>(bar + kFDrain);
-        wt.drain(bar + kFDrain, 0u);
+        umma_commit<CG>(bar + kFDrain + 8 * mine);
+        wt.drain(bar + kFDrain + 8 * mine, 0u);
       }
     }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ scales --
+    float *buf = reinterpret_cast<float *>(smem + p.off_bar + kF8BarBytes);
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int at = unit; ok && at < num_units; at += n_units) {
+      const Tile t = tile(at);
+      for (int kb0 = t.kb0; kb0 < t.kb1; kb0 += kBatch) {
+        // all of a batch's loads are under way before one is waited for
+        float a[kBatch][4], b[SQUARE ? 1 : kBatch][SQUARE ? 1 : kSb / 32];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const bool on = kb0 + k < t.kb1;
+          const float *sa = p.sa + int64_t(kb0 + k) * p.lds_a;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int m = t.m0 + 32 * i + lane;
+            a[k][i] = on && m < p.M ? __ldg(sa + m) : 0.f;
+          }
+          if constexpr (!SQUARE) {
+            const float *sbk = p.sb + int64_t(kb0 + k) * p.lds_b;
+#pragma unroll
+            for (int i = 0; i < kSb / 32; ++i) {
+              const int n = t.n0 + 32 * i + lane;
+              b[k][i] = on && n < p.N ? __ldg(sbk + n) : 0.f;
+            }
+          }
+        }
+        if constexpr (SQUARE) {
+          const int n = t.n0 + (lane & 1) * kCols, k = kb0 + (lane >> 1);
+          b[0][0] = lane < 2 * kBatch && n < p.N && k < t.kb1 ? __ldg(p.sb + int64_t(k) * p.lds_b + n / kF8Block) : 0.f;
+        }
+        ok = __all_sync(0xffffffffu, wait_soon(wt, bar + kFScaleEmpty + 8 * slot, phase ^ 1u, SITE_EPI_AUX_FULL));
+        if (!ok) break;
+        float *to = buf + slot * kBatchFloats;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) to[k * 128 + 32 * i + lane] = a[k][i];
+          if constexpr (!SQUARE) {
+#pragma unroll
+            for (int i = 0; i < kSb / 32; ++i) to[kBatch * 128 + k * kSb + 32 * i + lane] = b[k][i];
+          }
+        }
+        if (SQUARE && lane < 2 * kBatch) to[kBatch * 128 + lane] = b[0][0];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + kFScaleFull + 8 * slot);
+        slot ^= 1;
+        if (slot == 0) phase ^= 1u;
+      }
+    }
+  }
   } else {
+    set_registers<true, kF8RegsMore>();
     // ---------------------------------------------------------- epilogue --
     const int q = warp & 3;             // TMEM lane quarter
     const int grp = (warp - kEpi0) >> 2;  // half of the columns
     const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(grp * kCols);
-    float *my_sb = reinterpret_cast<float *>(smem + p.off_bar + kF8BarBytes) + (warp - kEpi0) * 2 * kCols;
-    int abuf = 0, half = 0;
-    uint32_t aphase = 0;
+    const float *buf = reinterpret_cast<const float *>(smem + p.off_bar + kF8BarBytes);
+    int abuf = 0, stage = 0, slot = 0;
+    uint32_t phase = 0, sphase = 0;
     bool ok = true;
     for (int at = unit; ok && at < num_units; at += n_units) {
       const Tile t = tile(at);
       const int m = t.m0 + q * 32 + lane, n0 = t.n0 + grp * kCols;
       const bool live = m < p.M;
-      // the next k-block's scales are on their way while this one's product finishes
-      constexpr int kMine = SQUARE ? 1 : kCols / 32;
-      float sa_next, sb_next[kMine];
-      auto fetch = [&](int kb) {
-        sa_next = live && kb < t.kb1 ? __ldg(p.sa + int64_t(kb) * p.lds_a + m) : 0.f;
-        if constexpr (SQUARE) {
-          sb_next[0] = n0 < p.N && kb < t.kb1 ? __ldg(p.sb + int64_t(kb) * p.lds_b + n0 / kF8Block) : 0.f;
-        } else {
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) {
-            const int n = n0 + i * 32 + lane;
-            sb_next[i] = n < p.N && kb < t.kb1 ? __ldg(p.sb + int64_t(kb) * p.lds_b + n) : 0.f;
-          }
-        }
-      };
       float2 acc[kCols / 2];
 #pragma unroll
       for (int j = 0; j < kCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      fetch(t.kb0);
+      int in_batch = 0;
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        float *sb_now = my_sb + half * kCols;
-        half ^= 1;
-        float s = sa_next;
-        if constexpr (SQUARE) {
-          s *= sb_next[0];
-        } else {
-          // two deep: the warp read this half two k-blocks ago, before its last __syncwarp
-#pragma unroll
-          for (int i = 0; i < kMine; ++i) sb_now[i * 32 + lane] = sb_next[i];
-          __syncwarp();
+        if (in_batch == 0) {
+          ok = __all_sync(0xffffffffu, wait_soon(wt, bar + kFScaleFull + 8 * slot, sphase, SITE_EPI_AUX_FULL));
+          if (!ok) break;
         }
-        fetch(kb + 1);
+        const float *sa_now = buf + slot * kBatchFloats + in_batch * 128;
+        const float *sb_now = buf + slot * kBatchFloats + kBatch * 128 + in_batch * kSb + (SQUARE ? grp : grp * kCols);
+        float s = sa_now[q * 32 + lane];
+        if constexpr (SQUARE) s *= *sb_now;
         const float2 s2 = make_float2(s, s);
-        ok = __all_sync(0xffffffffu, wt.wait(bar + kFTmemFull + 8 * abuf, aphase, SITE_EPI_TMEM_FULL));
+        ok = __all_sync(0xffffffffu, wait_soon(wt, bar + kFDone + 8 * stage, phase, SITE_EPI_TMEM_FULL));
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = tq + static_cast<uint32_t>(abuf * BN);
-        // 16 columns are on their way while the 16 before them are added
-        float v[2][16];
-        tmem_ld16(src, v[0]);
+        // 32 columns are on their way while the 32 before them are added
+        float v[2][32];
+        tmem_ld32(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < kCols / 16; ++c) {
+        for (int c = 0; c < kCols / 32; ++c) {
           tmem_wait_ld();
-          if (c + 1 < kCols / 16) {
-            tmem_ld16(src + 16 * (c + 1), v[(c + 1) & 1]);
+          if (c + 1 < kCols / 32) {
+            tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
               const uint32_t tb = bar + kFTmemEmpty + 8 * abuf;
-              if constexpr (CG == 2) mbar_arrive_remote(mapa_shared(tb, 0));
+              if constexpr (CG == 2) mbar_arrive_remote_relaxed(mapa_shared(tb, 0));
               else mbar_arrive(tb);
             }
           }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float2 x = make_float2(v[c & 1][2 * e], v[c & 1][2 * e + 1]);
-            if constexpr (!SQUARE) x = mul2(x, *reinterpret_cast<const float2 *>(sb_now + 16 * c + 2 * e));
-            acc[8 * c + e] = fma2(x, s2, acc[8 * c + e]);
+          for (int e = 0; e < 16; e += 2) {
+            float2 x = make_float2(v[c & 1][2 * e], v[c & 1][2 * e + 1]), y = make_float2(v[c & 1][2 * e + 2], v[c & 1][2 * e + 3]);
+            if constexpr (!SQUARE) {
+              const float4 b = *reinterpret_cast<const float4 *>(sb_now + 32 * c + 2 * e);
+              x = mul2(x, make_float2(b.x, b.y));
+              y = mul2(y, make_float2(b.z, b.w));
+            }
+            acc[16 * c + e] = fma2(x, s2, acc[16 * c + e]);
+            acc[16 * c + e + 1] = fma2(y, s2, acc[16 * c + e + 1]);
           }
         }
         abuf ^= 1;
-        if (abuf == 0) aphase ^= 1u;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        if (++in_batch == kBatch || kb + 1 == t.kb1) {
+          in_batch = 0;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar + kFScaleEmpty + 8 * slot);
+          slot ^= 1;
+          if (slot == 0) sphase ^= 1u;
+        }
       }
       if (!ok) break;
       if (!live) continue;
