@@ -14,11 +14,15 @@
 //            no CTA has to be resident for another to finish.
 //
 // Few tokens leave the tensor unit idle: the layer is bound by reading the chosen experts'
-// weights once.  They go straight from memory to registers in the places where mma.sync
-// wants them (tcgen05 would want them in shared memory, and 128 rows): a lane reads 16
-// consecutive bytes of a row, and what it holds is called columns 2q, 2q + 1, 2q + 8, 2q + 9 of a
-// step; the tokens' side is read the same way, so the sum runs over the same columns.
-// The eight warps of a CTA share a unit's columns, 128 at a time.
+// weights once.  So a CTA's warps are there to keep that reading going:
+//   producer  takes tickets and copies their rows, 2 KiB of 16 rows at a time, into a ring of
+//             shared memory (bulk copies), several units ahead of
+//   eight consumers, which share a stage's columns and multiply them by mma.sync (tcgen05 would want
+//             128 rows of tokens): a lane reads 16 consecutive bytes of a row, and what it holds
+//             is called columns 2q, 2q + 1, 2q + 8, 2q + 9 of a step; the tokens' side is read
+//             the same way, so the sum runs over the same columns
+//   watcher   waits for the h of units that are still on their way into the ring
+//   finisher  tells the GPU that a unit is done, and adds the shares of y
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -39,10 +43,16 @@ using namespace ge;
 namespace {
 
 constexpr int kPairs = GE_MOE_MAX_TOKENS * GE_MOE_MAX_K;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kChunk = 128;        // columns of a unit that a warp takes at a time
+constexpr int kWarps = 8;           // consumers; then the producer, the watcher and the finisher
+constexpr int kProducer = kWarps, kWatcher = kWarps + 1, kFinisher = kWarps + 2;
+constexpr int kThreads = 32 * (kWarps + 3);
+constexpr int kBlock = 128;        // columns that share a scale
 constexpr int kTile = 8;           // tokens of one mma
-constexpr int kMostTiles = 4;      // of them in one pass over the weights
+constexpr int kRoundTiles = 2;     // of them whose sums are joined at a time
+constexpr int kSegment = 2048;     // bytes of a row in a stage
+constexpr int kPitch = kSegment + 64;  // lanes of two rows touch different banks
+constexpr int kStages = 5;
+constexpr int kQueue = 8;          // units under way in a CTA
 constexpr int kUpCols = 8, kDownCols = 16;  // a unit's columns of h, of y
 constexpr int kRouterTokens = 4, kRouterWarps = 4;
 
@@ -361,13 +371,6 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// weights: read once
-__device__ __forceinline__ uint4 load_weights(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
 // h: written by other CTAs of this launch
 __device__ __forceinline__ uint4 load_shared(const void *p) {
   uint4 v;
@@ -386,117 +389,87 @@ __device__ __forceinline__ uint32_t widen(uint16_t v) {
   return pack16(true, f.x, f.y);
 }
 
-struct Rows {
-  const uint8_t *lo, *hi;   // the weights' rows g and g + 8 of this lane, nullptr: zeros
-  const float *s_lo, *s_hi;  // 8-bit weights: their scales' first k-block
-  int64_t ld_s;             // from one k-block's to the next's
-};
-
-// acc[tile][..] += rows (16, K) x tokens (8 per tile, K)^T over this warp's columns.
-// `from[n]`: this lane's token of tile n (nullptr: zeros); LO: and `rest` elements further what
-// their rounding left.
+// acc[tile][..] += a stage's rows (16) x tokens (8 per tile)^T over this warp's columns of the stage, which are
+// `first` and up of the whole; `bytes` of each row exist.  `from[n]`: this lane's token of tile n
+// (nullptr: zeros); LO: and `rest` elements further what their rounding left.  8-bit weights: scales of this warp's first
+// 128 columns at s_lo and s_hi, of the next ld_s further.
 template <int XT, int WT, int NT, bool LO>
-__device__ __forceinline__ void product(float (&acc)[NT][4], const Rows &w, const uint16_t *const (&from)[NT], int64_t rest, int K,
-                                        int warp, int q) {
+__device__ __forceinline__ void consume(float (&acc)[NT][4], const uint8_t *stage, int first, int bytes, const uint16_t *const (&from)[NT],
+                                        int64_t rest, const float *s_lo, const float *s_hi, int64_t ld_s, int warp, int lane) {
   constexpr bool k8 = WT == GE_E4M3 || WT == GE_E5M2;
-  constexpr int kPer = k8 ? 16 : 8;                 // columns of a lane's 16 bytes
-  constexpr int kSteps = kChunk / (4 * kPer);       // of 4 kPer columns
+  constexpr int kPer = k8 ? 16 : 8;                          // columns of a lane's 16 bytes
+  constexpr int kSteps = kSegment / 64 / kWarps;             // of 64 bytes
+  constexpr int kStepsOfBlock = k8 ? kBlock / 64 : NT <= 4 ? kSteps : 1;  // whose weights are held at a time
+  const int g = lane >> 2, q = lane & 3;
+  const int at = warp * kSteps * 64;
+  if (at >= bytes) return;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 a[2][kSteps][2];
-  auto fetch = [&](uint4 (&v)[kSteps][2], int c) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int col = c + i * 4 * kPer + q * kPer;
-      const int64_t at = k8 ? col : 2 * int64_t(col);
-      v[i][0] = w.lo && col < K ? load_weights(w.lo + at) : zero;
-      v[i][1] = w.hi && col < K ? load_weights(w.hi + at) : zero;
-    }
-  };
-  auto use = [&](const uint4 (&v)[kSteps][2], int c) {
-    float sum[k8 ? NT : 1][4];
+  for (int i0 = 0; i0 < kSteps; i0 += kStepsOfBlock) {
+    if (at + i0 * 64 >= bytes) break;
+    // the weights of a block, or of a step
+    uint32_t x0[kStepsOfBlock][kPer / 2], x1[kStepsOfBlock][kPer / 2];
+    float s0 = 0.f, s1 = 0.f;
     if constexpr (k8) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sum[n][r] = 0.f;
+      s0 = __ldg(s_lo + i0 / kStepsOfBlock * ld_s);
+      s1 = __ldg(s_hi + i0 / kStepsOfBlock * ld_s);
     }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      const int col = c + i * 4 * kPer + q * kPer;
-      uint32_t x0[kPer / 2], x1[kPer / 2];
+    for (int i = 0; i < kStepsOfBlock; ++i) {
+      const int byte = at + (i0 + i) * 64 + q * 16;
+      const bool on = byte < bytes;
+      const uint4 w0 = on ? *reinterpret_cast<const uint4 *>(stage + g * kPitch + byte) : zero;
+      const uint4 w1 = on ? *reinterpret_cast<const uint4 *>(stage + (g + 8) * kPitch + byte) : zero;
       if constexpr (k8) {
-        const uint32_t y0[4] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w}, y1[4] = {v[i][1].x, v[i][1].y, v[i][1].z, v[i][1].w};
+        const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          x0[2 * j] = widen<XT, WT>(static_cast<uint16_t>(y0[j]));
-          x0[2 * j + 1] = widen<XT, WT>(static_cast<uint16_t>(y0[j] >> 16));
-          x1[2 * j] = widen<XT, WT>(static_cast<uint16_t>(y1[j]));
-          x1[2 * j + 1] = widen<XT, WT>(static_cast<uint16_t>(y1[j] >> 16));
+          x0[i][2 * j] = widen<XT, WT>(static_cast<uint16_t>(y0[j]));
+          x0[i][2 * j + 1] = widen<XT, WT>(static_cast<uint16_t>(y0[j] >> 16));
+          x1[i][2 * j] = widen<XT, WT>(static_cast<uint16_t>(y1[j]));
+          x1[i][2 * j + 1] = widen<XT, WT>(static_cast<uint16_t>(y1[j] >> 16));
         }
       } else {
-        x0[0] = v[i][0].x, x0[1] = v[i][0].y, x0[2] = v[i][0].z, x0[3] = v[i][0].w;
-        x1[0] = v[i][1].x, x1[1] = v[i][1].y, x1[2] = v[i][1].z, x1[3] = v[i][1].w;
+        x0[i][0] = w0.x, x0[i][1] = w0.y, x0[i][2] = w0.z, x0[i][3] = w0.w;
+        x1[i][0] = w1.x, x1[i][1] = w1.y, x1[i][2] = w1.z, x1[i][3] = w1.w;
       }
+    }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float(&d)[4] = k8 ? sum[k8 ? n : 0] : acc[n];
+    for (int n = 0; n < NT; ++n) {
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      float(&d)[4] = k8 ? sum : acc[n];
+#pragma unroll
+      for (int i = 0; i < kStepsOfBlock; ++i) {
+        const bool on = at + (i0 + i) * 64 + q * 16 < bytes;
+        const int col = first + (at + (i0 + i) * 64) / (k8 ? 1 : 2) + q * kPer;
 #pragma unroll
         for (int l = 0; l < (LO ? 2 : 1); ++l) {
 #pragma unroll
           for (int u = 0; u < kPer / 8; ++u) {
             uint4 b = zero;
-            if (from[n] && col < K) {
+            if (from[n] && on) {
               const uint16_t *s = from[n] + (l ? rest : 0) + col + 8 * u;
               b = LO ? load_shared(s) : __ldg(reinterpret_cast<const uint4 *>(s));
             }
-            mma<XT>(d, x0[4 * u], x1[4 * u], x0[4 * u + 1], x1[4 * u + 1], b.x, b.y);
-            mma<XT>(d, x0[4 * u + 2], x1[4 * u + 2], x0[4 * u + 3], x1[4 * u + 3], b.z, b.w);
+            mma<XT>(d, x0[i][4 * u], x1[i][4 * u], x0[i][4 * u + 1], x1[i][4 * u + 1], b.x, b.y);
+            mma<XT>(d, x0[i][4 * u + 2], x1[i][4 * u + 2], x0[i][4 * u + 3], x1[i][4 * u + 3], b.z, b.w);
           }
         }
       }
-    }
-    if constexpr (k8) {
-      const int64_t at = c / kChunk * w.ld_s;
-      const float s0 = w.lo ? __ldg(w.s_lo + at) : 0.f, s1 = w.hi ? __ldg(w.s_hi + at) : 0.f;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        acc[n][0] = fmaf(sum[n][0], s0, acc[n][0]);
-        acc[n][1] = fmaf(sum[n][1], s0, acc[n][1]);
-        acc[n][2] = fmaf(sum[n][2], s1, acc[n][2]);
-        acc[n][3] = fmaf(sum[n][3], s1, acc[n][3]);
+      if constexpr (k8) {
+        acc[n][0] = fmaf(sum[0], s0, acc[n][0]);
+        acc[n][1] = fmaf(sum[1], s0, acc[n][1]);
+        acc[n][2] = fmaf(sum[2], s1, acc[n][2]);
+        acc[n][3] = fmaf(sum[3], s1, acc[n][3]);
       }
     }
-  };
-  constexpr int kStride = kChunk * kWarps;
-  int c = warp * kChunk;
-  if (c >= K) return;
-  fetch(a[0], c);
-  for (;;) {
-    if (c + kStride < K) fetch(a[1], c + kStride);
-    use(a[0], c);
-    if ((c += kStride) >= K) break;
-    if (c + kStride < K) fetch(a[0], c + kStride);
-    use(a[1], c);
-    if ((c += kStride) >= K) break;
   }
 }
 
-// The warps' sums of a unit, side by side for whoever adds them: [warp][token][row]
+// The warps' sums of some tokens, side by side for whoever adds them: [warp][token][row]
 struct Sums {
-  float v[kWarps][kMostTiles * kTile][16];
+  float v[kWarps][kRoundTiles * kTile][16];
 };
-
-template <int NT>
-__device__ __forceinline__ void put(Sums &s, const float (&acc)[NT][4], int warp, int lane) {
-  const int g = lane >> 2, q = lane & 3;
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    s.v[warp][n * kTile + 2 * q][g] = acc[n][0];
-    s.v[warp][n * kTile + 2 * q + 1][g] = acc[n][1];
-    s.v[warp][n * kTile + 2 * q][g + 8] = acc[n][2];
-    s.v[warp][n * kTile + 2 * q + 1][g + 8] = acc[n][3];
-  }
-}
 
 __device__ __forceinline__ float total(const Sums &s, int token, int row) {
   float v = s.v[0][token][row];
@@ -517,82 +490,22 @@ __device__ __forceinline__ float round_trip(uint16_t v) {
   else return __half2float(__ushort_as_half(v));
 }
 
-// 8 columns of h for up to 8 NT pairs
-template <int XT, int WT, int NT>
-__device__ void up_unit(const MoeParams &p, const Choice &c, Sums &s, int e, const uint16_t *list, int n, int col) {
-  constexpr bool k8 = WT == GE_E4M3 || WT == GE_E5M2;
-  constexpr int ws = k8 ? 1 : 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const uint8_t *w = static_cast<const uint8_t *>(p.w_up) + (int64_t(e) * 2 * p.F + col) * p.D * ws;
-  Rows r{w + int64_t(g) * p.D * ws, w + (int64_t(p.F) + g) * p.D * ws, nullptr, nullptr, 0};
-  if constexpr (k8) {
-    r.ld_s = (2 * p.F + kChunk - 1) / kChunk;
-    const float *f = p.s_up + int64_t(e) * r.ld_s * ((p.D + kChunk - 1) / kChunk);
-    r.s_lo = f + col / kChunk;
-    r.s_hi = f + (p.F + col) / kChunk;
-  }
-  const uint16_t *from[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i)
-    from[i] = i * kTile + g < n ? static_cast<const uint16_t *>(p.x) + int64_t(list[i * kTile + g] / p.k) * p.ldx : nullptr;
-  float acc[NT][4] = {};
-  product<XT, WT, NT, false>(acc, r, from, 0, p.D, warp, q);
-  put(s, acc, warp, lane);
-  __syncthreads();
-  for (int i = threadIdx.x; i < n * kUpCols; i += kThreads) {
-    const int token = i / kUpCols, row = i % kUpCols;
-    const float v = activate(p.act, total(s, token, row)) * total(s, token, row + 8);
-    const uint16_t hi = static_cast<uint16_t>(pack16(XT == GE_BF16, v, 0.f));
-    const float rest = v - round_trip<XT>(hi);
-    uint16_t *h = p.h + int64_t(list[token]) * p.F + col + row;
-    h[0] = hi;
-    // (nothing is left of an infinity)
-    h[int64_t(p.T) * p.k * p.F] = isfinite(rest) ? static_cast<uint16_t>(pack16(XT == GE_BF16, rest, 0.f)) : 0;
-  }
-}
+struct Shared {
+  Choice c;
+  Sums sums[2];
+  alignas(8) uint64_t full[kStages], empty[kStages];          // stages of the ring
+  alignas(8) uint64_t taken[kQueue], ready[kQueue], out[kQueue], free[kQueue];  // a unit: named, its h there, written, forgotten
+  uint32_t unit[kQueue];
+  volatile uint32_t quit;
+  alignas(128) uint8_t ring[kStages][16 * kPitch];
+};
 
-// 16 columns of the expert's share of y
-template <int XT, int WT, int NT>
-__device__ void down_unit(const MoeParams &p, const Choice &c, Sums &s, int e, const uint16_t *list, int n, int col) {
-  constexpr bool k8 = WT == GE_E4M3 || WT == GE_E5M2;
-  constexpr int ws = k8 ? 1 : 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const uint8_t *w = static_cast<const uint8_t *>(p.w_down) + (int64_t(e) * p.D + col) * p.F * ws;
-  Rows r{w + int64_t(g) * p.F * ws, col + g + 8 < p.D ? w + int64_t(g + 8) * p.F * ws : nullptr, nullptr, nullptr, 0};
-  if constexpr (k8) {
-    r.ld_s = (p.D + kChunk - 1) / kChunk;
-    r.s_lo = r.s_hi = p.s_down + int64_t(e) * r.ld_s * ((p.F + kChunk - 1) / kChunk) + col / kChunk;
-  }
-  const uint16_t *from[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) from[i] = i * kTile + g < n ? p.h + int64_t(list[i * kTile + g]) * p.F : nullptr;
-  float acc[NT][4] = {};
-  product<XT, WT, NT, true>(acc, r, from, int64_t(p.T) * p.k * p.F, p.F, warp, q);
-  put(s, acc, warp, lane);
-  __syncthreads();
-  for (int i = threadIdx.x; i < n * kDownCols; i += kThreads) {
-    const int token = i / kDownCols, row = i % kDownCols;
-    if (col + row < p.D) p.part[int64_t(list[token]) * p.D + col + row] = total(s, token, row) * c.weight[list[token]];
-  }
-}
+constexpr uint32_t kNoUnit = 0xffffffffu;
 
-template <int XT, int WT, bool UP>
-__device__ void any_unit(const MoeParams &p, const Choice &c, Sums &s, int a, int col) {
-  const int e = c.active[a];
-  for (int at = 0; at < c.count[a]; at += kMostTiles * kTile) {
-    const uint16_t *list = c.list + c.begin[a] + at;
-    const int n = min(c.count[a] - at, kMostTiles * kTile);
-    if (at) __syncthreads();  // the sums before these have been read
-    if constexpr (UP) {
-      if (n <= kTile) up_unit<XT, WT, 1>(p, c, s, e, list, n, col);
-      else if (n <= 2 * kTile) up_unit<XT, WT, 2>(p, c, s, e, list, n, col);
-      else up_unit<XT, WT, 4>(p, c, s, e, list, n, col);
-    } else {
-      if (n <= kTile) down_unit<XT, WT, 1>(p, c, s, e, list, n, col);
-      else if (n <= 2 * kTile) down_unit<XT, WT, 2>(p, c, s, e, list, n, col);
-      else down_unit<XT, WT, 4>(p, c, s, e, list, n, col);
-    }
-  }
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
@@ -601,88 +514,316 @@ __device__ __forceinline__ uint32_t load_acquire(const uint32_t *p) {
   return v;
 }
 
-__device__ __forceinline__ uint32_t add_release(uint32_t *p, uint32_t by) {
+__device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p, uint32_t by) {
   uint32_t v;
   asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(v) : "l"(p), "r"(by) : "memory");
   return v;
 }
 
-// bounded: false where the time ran out or another CTA's did
-__device__ bool wait_for(const MoeParams &p, const uint32_t *counter, uint32_t want) {
+__device__ __forceinline__ void add_release(uint32_t *p, uint32_t by) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(by) : "memory");
+}
+
+__device__ void give_up(const MoeParams &p, Shared &sh) {
+  if (atomicCAS(p.status, 0u, static_cast<uint32_t>(GE_ERR_TIMEOUT)) == 0u) {
+    p.status[1] = 0;
+    p.status[2] = blockIdx.x;
+  }
+  atomicExch(&p.head->abort, 1u);
+  sh.quit = 1u;
+}
+
+// Waits within a CTA: false where it gives up.  (They last as long as another CTA's h does, and four times the
+// time a watcher waits for that at most.)
+__device__ __forceinline__ bool wait_bar(const MoeParams &p, Shared &sh, const uint64_t &bar, uint32_t parity) {
+  const uint32_t b = smem_u32(&bar);
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(b, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  for (;;) {
+    if (mbar_try_wait_sleep(b, parity, 20000u)) return true;
+    if (sh.quit) return false;
+    if (globaltimer_ns() - t0 > 4 * p.timeout_ns) {
+      give_up(p, sh);
+      return false;
+    }
+  }
+}
+
+// an expert's h: false where the time ran out or another CTA's did
+__device__ bool wait_for(const MoeParams &p, Shared &sh, const uint32_t *counter, uint32_t want) {
   if (load_acquire(counter) >= want) return true;
   const uint64_t t0 = globaltimer_ns();
   for (;;) {
     if (load_acquire(counter) >= want) return true;
-    if (load_acquire(&p.head->abort)) return false;
+    if (load_acquire(&p.head->abort)) {
+      sh.quit = 1u;
+      return false;
+    }
     if (globaltimer_ns() - t0 > p.timeout_ns) {
-      if (atomicCAS(p.status, 0u, static_cast<uint32_t>(GE_ERR_TIMEOUT)) == 0u) {
-        p.status[1] = 0;
-        p.status[2] = blockIdx.x;
-      }
-      atomicExch(&p.head->abort, 1u);
+      give_up(p, sh);
       return false;
     }
     __nanosleep(64);
   }
 }
 
-template <int XT, int WT>
-__global__ void __launch_bounds__(kThreads, 2) moe_experts_kernel(const __grid_constant__ MoeParams p) {
-  __shared__ Choice c;
-  __shared__ Sums s;
-  __shared__ uint32_t ticket, flag;
-  griddep_wait();
-  griddep_launch_dependents();
-  for (int t = threadIdx.x >> 5; t < p.T; t += kWarps) choose(p, t, c, blockIdx.x == 0);
-  __syncthreads();
-  make_lists(p, c);
-  const uint32_t up_cols = p.F / kUpCols, down_cols = (p.D + kDownCols - 1) / kDownCols;
-  const uint32_t n_up = c.n_active * up_cols, n_all = n_up + c.n_active * down_cols;
-  for (;;) {
-    if (threadIdx.x == 0) ticket = atomicAdd(&p.head->ticket, 1u);
-    __syncthreads();
-    const uint32_t u = ticket;
-    if (u >= n_all) break;
-    if (u < n_up) {
-      const int a = u / up_cols, col = (u - a * up_cols) * kUpCols;
-      if (u == 0 && (p.debug_flags & GE_DEBUG_SKIP_FIRST_LOAD)) {
-        __syncthreads();
-        continue;
-      }
-      any_unit<XT, WT, true>(p, c, s, a, col);
-      __syncthreads();
-      if (threadIdx.x == 0) add_release(&p.done[c.active[a]], 1u);
-    } else {
-      const uint32_t d = u - n_up;
-      const int a = d / down_cols, tile = d - a * down_cols, col = tile * kDownCols;
-      if (threadIdx.x == 0) flag = wait_for(p, &p.done[c.active[a]], up_cols);
-      __syncthreads();
-      if (!flag) break;
-      any_unit<XT, WT, false>(p, c, s, a, col);
-      __syncthreads();
-      if (threadIdx.x == 0) flag = add_release(&p.shares[tile], 1u) == static_cast<uint32_t>(c.n_active) - 1u;
-      __syncthreads();
-      if (flag) {
-        // all shares of these columns are there: a thread adds 8 columns of a token, in the order of its choice
-        for (int i = threadIdx.x; i < p.T * 2; i += kThreads) {
-          const int t = i >> 1, d0 = col + (i & 1) * 8;
-          if (d0 >= p.D) continue;
-          float v[8] = {};
-          for (int j = 0; j < p.k; ++j) {
-            const float4 *f = reinterpret_cast<const float4 *>(p.part + (int64_t(t) * p.k + j) * p.D + d0);
-            const float4 x = __ldcg(f), y = __ldcg(f + 1);
-            v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
-            v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
-          }
-          uint32_t w[4];
+// A unit of work: `a` the active expert, `col` its first column of h or of y.
+struct Unit {
+  int a, col;
+  bool up;
+};
+
+struct Units {
+  uint32_t up_cols, down_cols, n_up, n_all;
+  __device__ __forceinline__ Units(const MoeParams &p, int n_active) {
+    up_cols = p.F / kUpCols;
+    down_cols = (p.D + kDownCols - 1) / kDownCols;
+    n_up = n_active * up_cols;
+    n_all = n_up + n_active * down_cols;
+  }
+  __device__ __forceinline__ Unit of(uint32_t u) const {
+    Unit r;
+    r.up = u < n_up;
+    const uint32_t v = r.up ? u : u - n_up, per = r.up ? up_cols : down_cols;
+    r.a = v / per;
+    r.col = (v - r.a * per) * (r.up ? kUpCols : kDownCols);
+    return r;
+  }
+};
+
+// A position in a ring of N.
+template <int N>
+struct Turn {
+  int at = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++at == N) {
+      at = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// The consumers' part of a unit with up to 8 NT tokens; false where a wait gave up.
+template <int XT, int WT, int NT, bool UP>
+__device__ bool do_unit(const MoeParams &p, Shared &sh, const Unit &u, Turn<kStages> &st, int &round) {
+  constexpr bool k8 = WT == GE_E4M3 || WT == GE_E5M2;
+  constexpr int ws = k8 ? 1 : 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const Choice &c = sh.c;
+  const int e = c.active[u.a], n = c.count[u.a];
+  const uint16_t *list = c.list + c.begin[u.a];
+  const int K = UP ? p.D : p.F, segments = (K * ws + kSegment - 1) / kSegment;
+  const int64_t rest = int64_t(p.T) * p.k * p.F;
+  const float *s_lo = nullptr, *s_hi = nullptr;
+  int64_t ld_s = 0;
+  if constexpr (k8) {
+    ld_s = ((UP ? 2 * p.F : p.D) + kBlock - 1) / kBlock;
+    const float *f = (UP ? p.s_up : p.s_down) + int64_t(e) * ld_s * ((K + kBlock - 1) / kBlock) + warp * (kSegment / kWarps / kBlock) * ld_s;
+    s_lo = f + u.col / kBlock;
+    s_hi = f + (UP ? p.F + u.col : u.col) / kBlock;
+  }
+  const uint16_t *from[NT];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack16(XT == GE_BF16, v[2 * e], v[2 * e + 1]);
-          *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + int64_t(t) * p.ldy + d0) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+  for (int i = 0; i < NT; ++i) {
+    const int at = i * kTile + g;
+    from[i] = at >= n ? nullptr : UP ? static_cast<const uint16_t *>(p.x) + int64_t(list[at] / p.k) * p.ldx : p.h + int64_t(list[at]) * p.F;
+  }
+  float acc[NT][4] = {};
+  for (int j = 0; j < segments; ++j) {
+    if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.full[st.at], st.phase))) return false;
+    consume<XT, WT, NT, !UP>(acc, sh.ring[st.at], j * (kSegment / ws), min(kSegment, K * ws - j * kSegment), from, rest, s_lo, s_hi, ld_s, warp,
+                             lane);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st.at]));
+    st.next();
+    if constexpr (k8) {
+      s_lo += kSegment / kBlock * ld_s;
+      s_hi += kSegment / kBlock * ld_s;
+    }
+  }
+  // the warps' sums, 16 tokens at a time (a buffer's last readers have passed the barrier of the round between)
+#pragma unroll
+  for (int r = 0; r < NT; r += kRoundTiles) {
+    if (r * kTile >= n) break;
+    Sums &s = sh.sums[round++ & 1];
+#pragma unroll
+    for (int i = 0; i < kRoundTiles; ++i) {
+      if (r + i >= NT) break;
+      s.v[warp][i * kTile + 2 * q][g] = acc[r + i][0];
+      s.v[warp][i * kTile + 2 * q + 1][g] = acc[r + i][1];
+      s.v[warp][i * kTile + 2 * q][g + 8] = acc[r + i][2];
+      s.v[warp][i * kTile + 2 * q + 1][g + 8] = acc[r + i][3];
+    }
+    asm volatile("barrier.cta.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+    const int some = min(n - r * kTile, kRoundTiles * kTile);
+    const uint16_t *of = list + r * kTile;
+    if constexpr (UP) {
+      for (int i = threadIdx.x; i < some * kUpCols; i += 32 * kWarps) {
+        const int token = i / kUpCols, row = i % kUpCols;
+        const float v = activate(p.act, total(s, token, row)) * total(s, token, row + 8);
+        const uint16_t hi = static_cast<uint16_t>(pack16(XT == GE_BF16, v, 0.f));
+        const float left = v - round_trip<XT>(hi);
+        uint16_t *h = p.h + int64_t(of[token]) * p.F + u.col + row;
+        h[0] = hi;
+        // (nothing is left of an infinity)
+        h[rest] = isfinite(left) ? static_cast<uint16_t>(pack16(XT == GE_BF16, left, 0.f)) : 0;
+      }
+    } else {
+      for (int i = threadIdx.x; i < some * kDownCols; i += 32 * kWarps) {
+        const int token = i / kDownCols, row = i % kDownCols;
+        if (u.col + row < p.D) p.part[int64_t(of[token]) * p.D + u.col + row] = total(s, token, row) * c.weight[of[token]];
       }
     }
   }
+  return true;
 }
+
+template <int XT, int WT, bool UP>
+__device__ bool any_unit(const MoeParams &p, Shared &sh, const Unit &u, Turn<kStages> &st, int &round) {
+  const int n = sh.c.count[u.a];
+  if (n <= kTile) return do_unit<XT, WT, 1, UP>(p, sh, u, st, round);
+  if (n <= 2 * kTile) return do_unit<XT, WT, 2, UP>(p, sh, u, st, round);
+  if (n <= 4 * kTile) return do_unit<XT, WT, 4, UP>(p, sh, u, st, round);
+  return do_unit<XT, WT, GE_MOE_MAX_TOKENS / kTile, UP>(p, sh, u, st, round);
+}
+
+// y's 16 columns of all tokens: a lane adds 8 columns of a token, in the order of its choice
+template <int XT>
+__device__ void add_shares(const MoeParams &p, int col) {
+  for (int i = threadIdx.x & 31; i < p.T * 2; i += 32) {
+    const int t = i >> 1, d0 = col + (i & 1) * 8;
+    if (d0 >= p.D) continue;
+    float v[8] = {};
+#pragma unroll 4
+    for (int j = 0; j < p.k; ++j) {
+      const float4 *f = reinterpret_cast<const float4 *>(p.part + (int64_t(t) * p.k + j) * p.D + d0);
+      const float4 x = __ldcg(f), y = __ldcg(f + 1);
+      v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+      v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack16(XT == GE_BF16, v[2 * e], v[2 * e + 1]);
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + int64_t(t) * p.ldy + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+template <int XT, int WT>
+__global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_constant__ MoeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  Shared &sh = *reinterpret_cast<Shared *>(smem_raw + ((128u - (smem_u32(smem_raw) & 127u)) & 127u));
+  constexpr int ws = WT == GE_E4M3 || WT == GE_E5M2 ? 1 : 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), kWarps);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(smem_u32(&sh.taken[i]), 1);
+      mbar_init(smem_u32(&sh.ready[i]), 1);
+      mbar_init(smem_u32(&sh.out[i]), kWarps);
+      mbar_init(smem_u32(&sh.free[i]), 1);
+    }
+    sh.quit = 0u;
+    fence_mbarrier_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int t = warp; t < p.T; t += kThreads / 32) choose(p, t, sh.c, blockIdx.x == 0);
+  __syncthreads();
+  make_lists(p, sh.c);
+  const Units units(p, sh.c.n_active);
+  Turn<kQueue> slot;
+  Turn<kStages> st;
+
+  if (warp == kProducer) {
+    int filled = 0;
+    bool ok = true;
+    while (ok) {
+      uint32_t t = 0;
+      if (lane == 0) t = atomicAdd(&p.head->ticket, 1u);
+      t = __shfl_sync(0xffffffffu, t, 0);
+      const bool last = t >= units.n_all;
+      ok = __all_sync(0xffffffffu, wait_bar(p, sh, sh.free[slot.at], slot.phase ^ 1u));
+      if (!ok) break;
+      if (lane == 0) {
+        sh.unit[slot.at] = last ? kNoUnit : t;
+        mbar_arrive(smem_u32(&sh.taken[slot.at]));
+      }
+      slot.next();
+      if (last) break;
+      const Unit u = units.of(t);
+      const int e = sh.c.active[u.a], K = u.up ? p.D : p.F;
+      // this lane's row
+      const int64_t r = u.up ? int64_t(e) * 2 * p.F + u.col + (lane & 7) + (lane & 8 ? p.F : 0) : int64_t(e) * p.D + u.col + (lane & 15);
+      const uint8_t *row = static_cast<const uint8_t *>(u.up ? p.w_up : p.w_down) + r * K * ws;
+      const int rows = u.up ? 16 : min(16, p.D - u.col);
+      for (int at = 0; at < K * ws; at += kSegment) {
+        ok = __all_sync(0xffffffffu, wait_bar(p, sh, sh.empty[st.at], st.phase ^ 1u));
+        if (!ok) break;
+        const uint32_t bytes = min(kSegment, K * ws - at), full = smem_u32(&sh.full[st.at]);
+        if (lane == 0) mbar_arrive_expect_tx(full, bytes * rows);
+        __syncwarp();
+        if (lane < rows) bulk_load(smem_u32(sh.ring[st.at] + lane * kPitch), row + at, bytes, full);
+        st.next();
+        ++filled;
+      }
+    }
+    if (!ok)  // what is on its way lands before the CTA's shared memory is another's
+      for (int f = max(0, filled - kStages); f < filled; ++f) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&sh.full[f % kStages]), static_cast<uint32_t>(f / kStages) & 1u))
+          if (globaltimer_ns() - t0 > p.timeout_ns) break;
+      }
+  } else if (warp == kWatcher) {
+    if (lane == 0)
+      for (;;) {
+        if (!wait_bar(p, sh, sh.taken[slot.at], slot.phase)) break;
+        const uint32_t t = sh.unit[slot.at];
+        if (t != kNoUnit && t >= units.n_up && !wait_for(p, sh, &p.done[sh.c.active[units.of(t).a]], units.up_cols)) break;
+        mbar_arrive(smem_u32(&sh.ready[slot.at]));
+        slot.next();
+        if (t == kNoUnit) break;
+      }
+  } else if (warp == kFinisher) {
+    for (;;) {
+      if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.out[slot.at], slot.phase))) break;
+      const uint32_t t = sh.unit[slot.at];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.free[slot.at]));
+      slot.next();
+      if (t == kNoUnit) break;
+      const Unit u = units.of(t);
+      if (u.up) {
+        if (lane == 0 && !(t == 0 && (p.debug_flags & GE_DEBUG_SKIP_FIRST_LOAD))) add_release(&p.done[sh.c.active[u.a]], 1u);
+      } else {
+        uint32_t before = 0;
+        if (lane == 0) before = add_acq_rel(&p.shares[u.col / kDownCols], 1u);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == static_cast<uint32_t>(sh.c.n_active) - 1u) add_shares<XT>(p, u.col);
+      }
+    }
+  } else {
+    int round = 0;
+    for (;;) {
+      if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.ready[slot.at], slot.phase))) break;
+      const uint32_t t = sh.unit[slot.at];
+      if (t != kNoUnit) {
+        const Unit u = units.of(t);
+        if (!(u.up ? any_unit<XT, WT, true>(p, sh, u, st, round) : any_unit<XT, WT, false>(p, sh, u, st, round))) break;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.out[slot.at]));
+      slot.next();
+      if (t == kNoUnit) break;
+    }
+  }
+}
+
+constexpr int kSmem = static_cast<int>(sizeof(Shared)) + 128;
 
 template <int XT>
 const void *experts(int wt) {
@@ -783,7 +924,8 @@ int gemm_epi_moe_plan_create(gemm_epi_moe_plan **plan, int64_t T, int64_t D, int
     pl->router = f32 ? reinterpret_cast<const void *>(moe_router_kernel<GE_F16, true>)
                      : reinterpret_cast<const void *>(moe_router_kernel<GE_F16, false>);
   int per_sm = 0;
-  if (!p.status || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, pl->experts, kThreads, 0) != cudaSuccess || per_sm < 1) {
+  if (!p.status || cudaFuncSetAttribute(pl->experts, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, pl->experts, kThreads, kSmem) != cudaSuccess || per_sm < 1) {
     cudaGetLastError();
     delete pl;
     return GE_ERR_CUDA;
@@ -834,7 +976,7 @@ int gemm_epi_moe_run(gemm_epi_moe_plan *pl, const void *x, const void *w_router,
   if (launch_pdl(pl->router, dim3(static_cast<unsigned>(p.E), static_cast<unsigned>(ceil_div(p.T, kRouterTokens))),
                  dim3(32 * kRouterWarps), 0, args, st) != cudaSuccess)
     return GE_ERR_CUDA;
-  return launch_pdl(pl->experts, dim3(static_cast<unsigned>(pl->grid)), dim3(kThreads), 0, args, st) == cudaSuccess ? GE_OK
+  return launch_pdl(pl->experts, dim3(static_cast<unsigned>(pl->grid)), dim3(kThreads), kSmem, args, st) == cudaSuccess ? GE_OK
                                                                                                                    : GE_ERR_CUDA;
 }
 
