@@ -57,6 +57,30 @@ struct Eight {
     else return __half2float(__ushort_as_half(static_cast<unsigned short>(j & 1 ? w >> 16 : w)));
   }
   __device__ __forceinline__ void load(const void *p) { r = __ldg(static_cast<const uint4 *>(p)); }
+  // magnitudes' maxima, two at a time; NaN is none
+  struct Tops {
+    uint32_t w[4];
+  };
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t m;
+    if constexpr (XT == GE_BF16) asm("max.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    else asm("max.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+    return m;
+  }
+  static __device__ __forceinline__ float wide(uint32_t w, int half) {
+    Eight e;
+    e.r.x = w;
+    return e.at(half);
+  }
+  // this row's maximum; the columns' so far go into `cols`
+  __device__ __forceinline__ float top(Tops &cols) const {
+    const uint32_t a[4] = {r.x & 0x7fff7fffu, r.y & 0x7fff7fffu, r.z & 0x7fff7fffu, r.w & 0x7fff7fffu};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cols.w[j] = max2(cols.w[j], a[j]);
+    const uint32_t m = max2(max2(a[0], a[1]), max2(a[2], a[3]));
+    return fmaxf(wide(m, 0), wide(m, 1));
+  }
+  static __device__ __forceinline__ float at(const Tops &c, int j) { return wide(c.w[j >> 1], j & 1); }
   __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void load_some(const void *p, int n) {
     const uint16_t *s = static_cast<const uint16_t *>(p);
@@ -74,6 +98,20 @@ struct Eight<GE_F32> {
     const float4 &v = j < 4 ? a : b;
     return (j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w;
   }
+  struct Tops {
+    float w[8];
+  };
+  __device__ __forceinline__ float top(Tops &cols) const {
+    float m = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float x = fabsf(at(j));
+      m = fmaxf(m, x);
+      cols.w[j] = fmaxf(cols.w[j], x);
+    }
+    return m;
+  }
+  static __device__ __forceinline__ float at(const Tops &c, int j) { return c.w[j]; }
   __device__ __forceinline__ void load(const void *p) {
     a = __ldg(static_cast<const float4 *>(p));
     b = __ldg(static_cast<const float4 *>(p) + 1);
@@ -100,10 +138,21 @@ __device__ __forceinline__ void store8(uint8_t *p, uint32_t lo, uint32_t hi, int
   }
 }
 
+// The maxima of 2 N values over the two lanes that differ in bit `o`: each keeps N of them, the upper half where it has the bit.
+template <int N>
+__device__ __forceinline__ void halve(float (&v)[8], int o) {
+  const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float keep = upper ? v[N + i] : v[i], give = upper ? v[i] : v[N + i];
+    v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+  }
+}
+
 template <int XT, bool COLS>
-__global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 3) quant_kernel(const __grid_constant__ QuantParams p, bool vec) {
-  __shared__ float part[8][kB];                      // columns' maxima, by warp
-  __shared__ float top[kB];                          // columns' maxima
+__global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 4) quant_kernel(const __grid_constant__ QuantParams p, bool vec) {
+  __shared__ __align__(16) float part[8][kB];        // columns' maxima, by warp
+  __shared__ __align__(16) float inverse[kB];        // columns' inverse scales
   __shared__ __align__(16) uint8_t turned[COLS ? kB * kB : 16];
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t d0 = int64_t(blockIdx.x) * kB, t0 = int64_t(blockIdx.y) * kB;
@@ -120,23 +169,17 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 3) quant_ker
     else if (vec && cols == 8) v[i].load(s);
     else v[i].load_some(s, cols);
   }
-  float row_top[8], col_top[8];
+  typename Eight<XT>::Tops tops = {};
+  float top[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) col_top[j] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    row_top[i] = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float a = fabsf(v[i].at(j));
-      row_top[i] = fmaxf(row_top[i], a);
-      if (COLS) col_top[j] = fmaxf(col_top[j], a);
-    }
-  }
+  for (int i = 0; i < 8; ++i) top[i] = v[i].top(tops);
+  // A scale is a division and its inverse another, which take as many instructions as all else that an
+  // element needs: each is made by one thread (81 us for 16384 x 4096 both ways, when every thread made its own).
+  float row_inv[8], col_inv[8];
   if (p.square) {
-    float m = row_top[0];
+    float m = top[0];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, row_top[i]);
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, top[i]);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) part[0][warp] = m;
@@ -144,65 +187,65 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 3) quant_ker
     m = part[0][0];
 #pragma unroll
     for (int w = 1; w < 8; ++w) m = fmaxf(m, part[0][w]);
+    const float s = scale_of(m, p.largest), inv = __frcp_rn(s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) row_top[i] = m;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) col_top[j] = m;
+    for (int i = 0; i < 8; ++i) row_inv[i] = col_inv[i] = inv;
     if (threadIdx.x == 0) {
-      const float s = scale_of(m, p.largest);
       if (p.q) p.scale[blockIdx.x * p.lds + blockIdx.y] = s;
       if (COLS) p.scale_t[blockIdx.y * p.ldst + blockIdx.x] = s;
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int o = 8; o; o >>= 1) row_top[i] = fmaxf(row_top[i], __shfl_xor_sync(0xffffffffu, row_top[i], o));
     if (COLS) {
+      float c[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        col_top[j] = fmaxf(col_top[j], __shfl_xor_sync(0xffffffffu, col_top[j], 16));
-        if (lane < 16) part[warp][cg * 8 + j] = col_top[j];
-      }
+      for (int j = 0; j < 8; ++j) c[j] = Eight<XT>::at(tops, j);
+      halve<4>(c, 16);
+      *reinterpret_cast<float4 *>(&part[warp][cg * 8 + (lane >> 4) * 4]) = make_float4(c[0], c[1], c[2], c[3]);
       __syncthreads();
       if (threadIdx.x < kB) {
         float m = part[0][threadIdx.x];
 #pragma unroll
         for (int w = 1; w < 8; ++w) m = fmaxf(m, part[w][threadIdx.x]);
-        top[threadIdx.x] = m;
-        if (d0 + threadIdx.x < p.D) p.scale_t[blockIdx.y * p.ldst + d0 + threadIdx.x] = scale_of(m, p.largest);
+        const float s = scale_of(m, p.largest);
+        inverse[threadIdx.x] = __frcp_rn(s);
+        if (d0 + threadIdx.x < p.D) p.scale_t[blockIdx.y * p.ldst + d0 + threadIdx.x] = s;
       }
-      __syncthreads();
+    }
+    if (p.q) {
+      // lanes 2i and 2i + 1 of 16 end with row i's maximum
+      halve<4>(top, 8);
+      halve<2>(top, 4);
+      halve<1>(top, 2);
+      const float m = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 1));
+      const float s = scale_of(m, p.largest), inv = __frcp_rn(s);
+      const int i = cg >> 1;
+      if ((cg & 1) == 0 && i < rows) p.scale[blockIdx.x * p.lds + t + i] = s;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) col_top[j] = top[cg * 8 + j];
+      for (int k = 0; k < 8; ++k) row_inv[k] = __shfl_sync(0xffffffffu, inv, (lane & 16) | (2 * k));
     }
   }
   if (p.q) {
-    float inv[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = scale_of(row_top[i], p.largest);
-      inv[i] = __frcp_rn(s);
-      if (!p.square && cg == i && i < rows) p.scale[blockIdx.x * p.lds + t + i] = s;
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i >= rows) break;
-      const uint32_t lo = pack8(p.e5m2, v[i].at(0) * inv[i], v[i].at(1) * inv[i]) |
-                          pack8(p.e5m2, v[i].at(2) * inv[i], v[i].at(3) * inv[i]) << 16;
-      const uint32_t hi = pack8(p.e5m2, v[i].at(4) * inv[i], v[i].at(5) * inv[i]) |
-                          pack8(p.e5m2, v[i].at(6) * inv[i], v[i].at(7) * inv[i]) << 16;
+      const float r = row_inv[i];
+      const uint32_t lo = pack8(p.e5m2, v[i].at(0) * r, v[i].at(1) * r) | pack8(p.e5m2, v[i].at(2) * r, v[i].at(3) * r) << 16;
+      const uint32_t hi = pack8(p.e5m2, v[i].at(4) * r, v[i].at(5) * r) | pack8(p.e5m2, v[i].at(6) * r, v[i].at(7) * r) << 16;
       if (cols > 0) store8(p.q + (t + i) * p.ldq + d, lo, hi, cols);
     }
   }
   if constexpr (COLS) {
+    if (!p.square) {
+      __syncthreads();
+      const float4 a = *reinterpret_cast<const float4 *>(&inverse[cg * 8]), b = *reinterpret_cast<const float4 *>(&inverse[cg * 8 + 4]);
+      col_inv[0] = a.x, col_inv[1] = a.y, col_inv[2] = a.z, col_inv[3] = a.w;
+      col_inv[4] = b.x, col_inv[5] = b.y, col_inv[6] = b.z, col_inv[7] = b.w;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float inv = __frcp_rn(scale_of(col_top[j], p.largest));
-      const uint32_t lo = pack8(p.e5m2, v[0].at(j) * inv, v[1].at(j) * inv) |
-                          pack8(p.e5m2, v[2].at(j) * inv, v[3].at(j) * inv) << 16;
-      const uint32_t hi = pack8(p.e5m2, v[4].at(j) * inv, v[5].at(j) * inv) |
-                          pack8(p.e5m2, v[6].at(j) * inv, v[7].at(j) * inv) << 16;
+      const float r = col_inv[j];
+      const uint32_t lo = pack8(p.e5m2, v[0].at(j) * r, v[1].at(j) * r) | pack8(p.e5m2, v[2].at(j) * r, v[3].at(j) * r) << 16;
+      const uint32_t hi = pack8(p.e5m2, v[4].at(j) * r, v[5].at(j) * r) | pack8(p.e5m2, v[6].at(j) * r, v[7].at(j) * r) << 16;
       *reinterpret_cast<uint2 *>(turned + (cg * 8 + j) * kB + ((rg ^ cg) << 3)) = make_uint2(lo, hi);
     }
     __syncthreads();
