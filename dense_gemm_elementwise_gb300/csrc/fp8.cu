@@ -1,5 +1,4 @@
-// fp8.cu -- host side of the block-scaled 8-bit products (gemm_epi_fp8_*), and the kernel that
-// joins the slices of a split sum; the product is in fp8_kernel.cuh.
+// fp8.cu -- host side of the block-scaled 8-bit products (gemm_epi_fp8_*); the product is in fp8_kernel.cuh.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -16,35 +15,6 @@ using namespace ge;
 
 namespace {
 
-struct JoinParams {
-  Fp8Params p;  // c, d, part, sizes
-};
-
-// The slices of 8 columns of a row, added in order.
-__global__ void __launch_bounds__(256) fp8_join_kernel(const __grid_constant__ JoinParams q) {
-  const Fp8Params &p = q.p;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t groups = p.ld_part / 8, all = groups * p.M;
-  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < all; i += int64_t(gridDim.x) * blockDim.x) {
-    const int64_t m = i / groups, n = (i - m * groups) * 8;
-    if (n >= p.N) continue;
-    float v[8] = {};
-    const float4 *s = reinterpret_cast<const float4 *>(p.part + m * p.ld_part + n);
-#pragma unroll 4
-    for (int z = 0; z < p.slices; ++z) {
-      const float4 a = __ldcg(s), b = __ldcg(s + 1);
-      v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-      v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-      s += int64_t(p.M) * p.ld_part / 4;
-    }
-    const int64_t at = m * p.ldd + n;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (n + e < p.N) store_one(p.d, at + e, p.dt, v[e] + (p.c ? load_one(p.c, at + e, p.dt) : 0.f));
-  }
-}
-
 int64_t size_of(int t) { return t == GE_F32 ? 4 : 2; }
 
 }  // namespace
@@ -52,7 +22,7 @@ int64_t size_of(int t) { return t == GE_F32 ? 4 : 2; }
 struct gemm_epi_fp8_plan {
   int64_t M = 0, N = 0, K = 0;
   ge_fp8_desc d{};
-  int sms = 0, cg = 1, grid = 1, smem = 0;
+  int sms = 0, cg = 1, cluster = 1, grid = 1, smem = 0;
   const void *fn = nullptr;
   Fp8Params p{};
 };
@@ -69,14 +39,7 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   pl->fn = pl->cg == 2 ? fp8_kernel_cg2(square) : fp8_kernel_cg1(square);
   const int64_t num_m = ceil_div(M, bm), num_n = ceil_div(N, bn), tiles = num_m * num_n;
   p.num_kb = static_cast<int32_t>(ceil_div(pl->K, kF8Block));
-  // too few tiles for the GPU: their sums are split
-  int64_t slices = 1;
-  if (tiles < units) slices = std::min<int64_t>(units / tiles, p.num_kb);
-  p.kb_split = static_cast<int32_t>(ceil_div(p.num_kb, slices));
-  slices = ceil_div(p.num_kb, p.kb_split);
-  if (tiles * slices > (int64_t(1) << 31) - 1) return GE_ERR_SHAPE;
-  p.slices = static_cast<int32_t>(slices);
-  p.ld_part = round_up(N, bn);
+  if (tiles > (int64_t(1) << 31) / kF8MaxSlices) return GE_ERR_SHAPE;
   p.num_m_blk = static_cast<int32_t>(num_m);
   p.num_n_blk = static_cast<int32_t>(num_n);
   p.raster_group = num_m <= 16 ? static_cast<int32_t>(num_m) : 12;
@@ -99,6 +62,31 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
     cudaGetLastError();
     return GE_ERR_CUDA;
   }
+  // Too few tiles for the GPU: their sums are split among the CTAs of clusters, all of which have to be there at once.
+  // A slice more has to save a k-block (of about 0.3 us) for each slice: what it costs to join them.
+  int slices = 1;
+  for (int s = 2; pl->cg == 1 && s <= kF8MaxSlices && s <= p.num_kb && tiles * s <= units; ++s) {
+    if (ceil_div(p.num_kb, s) + s > ceil_div(p.num_kb, slices) + slices) continue;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(s);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * s));
+    cfg.blockDim = dim3(kF8Threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(max_smem);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, pl->fn, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      continue;
+    }
+    if (clusters >= tiles) slices = s;
+  }
+  p.slices = slices;
+  p.kb_split = static_cast<int32_t>(ceil_div(p.num_kb, slices));
+  pl->cluster = pl->cg == 2 ? 2 : slices;
   pl->grid = static_cast<int>(std::min<int64_t>(units, tiles * slices)) * pl->cg;
   return GE_OK;
 }
@@ -164,11 +152,8 @@ int gemm_epi_fp8_plan_create(gemm_epi_fp8_plan **plan, int64_t M, int64_t N, int
 
 void gemm_epi_fp8_plan_destroy(gemm_epi_fp8_plan *plan) { delete plan; }
 
-size_t gemm_epi_fp8_workspace_bytes(const gemm_epi_fp8_plan *pl) {
-  if (!pl || pl->p.slices == 1) return 0;
-  // (16 more, to start on a whole 32 bytes)
-  return 16 + sizeof(float) * static_cast<size_t>(pl->p.slices) * static_cast<size_t>(pl->M) * static_cast<size_t>(pl->p.ld_part);
-}
+// (sums that are split are joined in shared memory)
+size_t gemm_epi_fp8_workspace_bytes(const gemm_epi_fp8_plan *) { return 0; }
 
 int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a, const void *B, const float *scale_b,
                      const void *C, void *D, void *workspace, size_t workspace_bytes, void *stream) {
@@ -178,9 +163,8 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
     if (!is_aligned16(q)) return GE_ERR_MISALIGNED;
   for (const float *q : {scale_a, scale_b})
     if ((reinterpret_cast<uintptr_t>(q) & 3u) != 0) return GE_ERR_MISALIGNED;
-  const size_t need = gemm_epi_fp8_workspace_bytes(pl);
-  if (need && (!workspace || workspace_bytes < need)) return GE_ERR_WORKSPACE;
-  if (need && !is_aligned16(workspace)) return GE_ERR_MISALIGNED;
+  if (!is_aligned16(workspace)) return GE_ERR_MISALIGNED;
+  if (workspace_bytes < gemm_epi_fp8_workspace_bytes(pl)) return GE_ERR_WORKSPACE;
   Fp8Params p = pl->p;
   if (!encode_rows(&p.tmA, GE_E4M3, A, pl->K, pl->M, 1, pl->d.lda, pl->d.lda * pl->M, kF8Block, p.a_rows) ||
       !encode_rows(&p.tmB, GE_E4M3, B, pl->K, pl->N, 1, pl->d.ldb, pl->d.ldb * pl->N, kF8Block, 128))
@@ -189,19 +173,11 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
   p.sb = scale_b;
   p.c = C;
   p.d = D;
-  p.part = need ? reinterpret_cast<float *>(round_up(static_cast<int64_t>(reinterpret_cast<uintptr_t>(workspace)), 32)) : nullptr;
   auto rows32 = [&](const void *q) { return !q || ((reinterpret_cast<uintptr_t>(q) | static_cast<uintptr_t>(p.ldd * size_of(p.dt))) & 31u) == 0; };
   p.vec = rows32(C) && rows32(D);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   void *args[] = {&p};
-  if (launch_pdl(pl->fn, dim3(pl->grid), dim3(kF8Threads), pl->smem, args, s, pl->cg) != cudaSuccess) return GE_ERR_CUDA;
-  if (p.slices == 1) return GE_OK;
-  JoinParams q;
-  q.p = p;
-  const int64_t threads = p.ld_part / 8 * pl->M;
-  void *jargs[] = {&q};
-  return launch_pdl(reinterpret_cast<const void *>(fp8_join_kernel), dim3(static_cast<unsigned>(std::min<int64_t>(ceil_div(threads, 256), pl->sms * 8))),
-                    dim3(256), 0, jargs, s) == cudaSuccess ? GE_OK : GE_ERR_CUDA;
+  return launch_pdl(pl->fn, dim3(static_cast<unsigned>(pl->grid)), dim3(kF8Threads), pl->smem, args, static_cast<cudaStream_t>(stream),
+                    pl->cluster) == cudaSuccess ? GE_OK : GE_ERR_CUDA;
 }
 
 }  // extern "C"

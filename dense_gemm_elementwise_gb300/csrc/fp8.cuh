@@ -15,11 +15,10 @@ struct Fp8Params {
   int64_t lds_a, lds_b;
   const void *c;           // added, or nullptr
   void *d;
-  float *part;             // slices: [slice][M][ld_part] sums instead of D
-  int64_t ldd, ld_part;
+  int64_t ldd;
   int32_t M, N;
   int32_t num_kb, num_m_blk, num_n_blk, raster_group;
-  int32_t slices, kb_split;  // a tile's k-blocks are shared by `slices` units, kb_split each
+  int32_t slices, kb_split;  // a tile's k-blocks are shared by the `slices` CTAs of a cluster, kb_split each
   int32_t stages;
   int32_t a_e5m2, b_e5m2, dt, vec;  // vec: rows of C and D are whole 32-byte units
   int32_t a_rows;          // rows of an A tile that are loaded (one CTA)
@@ -39,6 +38,9 @@ __host__ __device__ constexpr int fp8_batch(bool square) { return square ? 8 : 4
 __host__ __device__ constexpr uint32_t fp8_scale_bytes(int bn, bool square) {
   return 2u * 4u * static_cast<uint32_t>(fp8_batch(square)) * static_cast<uint32_t>(128 + (square ? 2 : bn));
 }
+
+constexpr int kF8MaxSlices = 8;
+constexpr int kF8PartPitch = 128 + 4;  // floats between the rows of a slice's sums in shared memory
 
 // square: B's scales are one for each 128 columns
 const void *fp8_kernel_cg1(bool square);  // 128 x 128 tiles, one CTA

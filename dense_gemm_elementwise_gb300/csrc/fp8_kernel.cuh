@@ -25,6 +25,10 @@
 //   * 32 columns are on their way to an epilogue thread while it adds 32 others, which its registers
 //     have room for because the other warps give theirs away.  (Sixteen epilogue warps took 530 us.)
 //
+// Few tiles (128 x 128, single CTAs) share their sums over K with the other CTAs of a cluster, which leave them in
+// shared memory, where each CTA then adds its part of the tile in the order of the slices: one launch, no
+// workspace (1 x 8192 x 4096: TODO us, with slices in memory and a second launch 11.0).
+//
 // Every wait is bounded, as in gemm_kernel.cuh.  No epilogue warp waits for another.
 #pragma once
 
@@ -76,7 +80,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-// n (up to 8) consecutive outputs of a row: 16 bytes at a time where rows allow it
 __device__ __forceinline__ float load_one(const void *p, int64_t at, int dt) {
   if (dt == GE_F32) return static_cast<const float *>(p)[at];
   const uint16_t v = static_cast<const uint16_t *>(p)[at];
@@ -190,13 +193,14 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
   griddep_wait();
 
   const Waiter wt{abort_flag, p.status, p.timeout_ns};
-  const int tiles = p.num_m_blk * p.num_n_blk, num_units = tiles * p.slices;
+  const int num_units = p.num_m_blk * p.num_n_blk * p.slices;
   struct Tile { int z, m0, n0, kb0, kb1; };
   auto tile = [&](int at) {
     Tile t;
-    t.z = at / tiles;
+    const int whole = at / p.slices;
+    t.z = at - whole * p.slices;
     int l, mb, nb;
-    tile_coords(p.num_m_blk, p.num_n_blk, p.raster_group, at - t.z * tiles, l, mb, nb);
+    tile_coords(p.num_m_blk, p.num_n_blk, p.raster_group, whole, l, mb, nb);
     t.m0 = mb * T::kMmaM + static_cast<int>(rank) * BM;
     t.n0 = nb * BN;
     t.kb0 = t.z * p.kb_split;
@@ -438,6 +442,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
       }
       if (!ok) break;
       if (!live) continue;
+      if (CG == 1 && p.slices > 1) {  // the ring is free: all of this CTA's products are complete
+        float *to = reinterpret_cast<float *>(smem) + (q * 32 + lane) * kF8PartPitch + grp * kCols;
+#pragma unroll
+        for (int e = 0; e < kCols / 2; e += 2)
+          *reinterpret_cast<float4 *>(to + 2 * e) = make_float4(acc[e].x, acc[e].y, acc[e + 1].x, acc[e + 1].y);
+        continue;
+      }
 #pragma unroll
       for (int c = 0; c < kCols / 16; ++c) {
         const int n = n0 + 16 * c;
@@ -448,16 +459,39 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
           v[2 * e] = acc[8 * c + e].x;
           v[2 * e + 1] = acc[8 * c + e].y;
         }
-        if (p.part) {  // rows of whole tiles
-          float *o = p.part + (int64_t(t.z) * p.M + m) * p.ld_part + n;
-          store_words(o, reinterpret_cast<const uint32_t *>(v));
-          store_words(o + 8, reinterpret_cast<const uint32_t *>(v + 8));
-        } else {
-          finish16(p, m, n, v);
-        }
+        finish16(p, m, n, v);
       }
     }
     __syncwarp();
+  }
+
+  if (CG == 1 && p.slices > 1) {
+    // A cluster has one tile.  Its rows' groups of 4 columns are dealt out to the cluster's threads.  (After a
+    // timeout what is added here is undefined, like the run's outputs.)
+    __syncwarp();
+    cluster_sync_all();
+    const Tile t = tile(unit);
+    const int rows = min(BM, p.M - t.m0), groups = rows * (BN / 4);
+    for (int i = t.z * kF8Threads + static_cast<int>(threadIdx.x); i < groups; i += p.slices * kF8Threads) {
+      const int r = i / (BN / 4), n = t.n0 + i % (BN / 4) * 4;
+      const uint32_t at = sb + static_cast<uint32_t>(r * kF8PartPitch + i % (BN / 4) * 4) * 4u;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int z = 0; z < p.slices; ++z) {
+        float4 x;
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                     : "r"(mapa_shared(at, static_cast<uint32_t>(z)))
+                     : "memory");
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      const float w[4] = {v.x, v.y, v.z, v.w};
+      const int64_t out = int64_t(t.m0 + r) * p.ldd + n;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < p.N) store_one(p.d, out + e, p.dt, w[e] + (p.c ? load_one(p.c, out + e, p.dt) : 0.f));
+    }
+    __syncwarp();
+    cluster_sync_all();  // no CTA leaves while its sums are read
   }
 
   // -------------------------------------------------------------- teardown --

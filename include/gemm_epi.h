@@ -657,12 +657,13 @@ typedef struct gemm_epi_fp8_plan gemm_epi_fp8_plan;
 int gemm_epi_fp8_plan_create(gemm_epi_fp8_plan **plan, int64_t M, int64_t N, int64_t K,
                              const ge_fp8_desc *desc);
 
-/* Bytes of caller-owned device workspace (0: none is needed). */
+/* Bytes of caller-owned device workspace: 0 for every plan as of now (sums that are split among CTAs are joined in
+ * their shared memory). */
 size_t gemm_epi_fp8_workspace_bytes(const gemm_epi_fp8_plan *plan);
 
 /*
- * Run on `stream`: one or two launches, asynchronous, nothing allocates; any run can be captured
- * into a CUDA graph.  C may be NULL (0) or D itself.  D must not overlap the other inputs.
+ * Run on `stream`: one launch, asynchronous, nothing allocates; any run can be captured
+ * into a CUDA graph.  workspace may be NULL where none is needed.  C may be NULL (0) or D itself.  D must not overlap the other inputs.
  * Errors: GE_ERR_INVALID, _MISSING_ARG, _MISALIGNED (A, B, C, D or the workspace not 16-byte aligned,
  * scales not 4-byte), _WORKSPACE, _CUDA; a device-side timeout is reported later by
  * gemm_epi_last_error.

@@ -134,6 +134,14 @@ def test_outputs_sums_and_pitches(d, M, N, K, pad, block):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(1, 100), (1, 3000), (20, 2500), (130, 300), (128, 1290)])
+@pytest.mark.parametrize("K", [128, 256, 1152, 1408, 2000, 5000])
+def test_sums_split_among_the_ctas_of_a_cluster(M, N, K):
+    """Numbers of k-blocks that the slices do and do not divide."""
+    Case(M, N, K, d="f32", add=True, block="row").run().check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(5, 300, 1000), (300, 300, 700), (600, 5000, 400)])
 def test_sum_in_place(M, N, K):
     c = Case(M, N, K, d="f32", add=True)
@@ -253,17 +261,14 @@ def test_null_plans():
 @pytest.mark.gpu
 def test_run_refusals():
     c = Case(300, 300, 4096)
-    assert c.ws is not None
-    run = lambda A=c.A, sa=c.sa, Bm=c.B, sb=c.sb, C=None, D=c.buf, ws=c.ws, n=None: B.gemm_epi_fp8_run(  # noqa: E731
-        c.plan, A, sa, Bm, sb, C, D, ws, n if n is not None or ws is not None else 0, check=False)
+    run = lambda A=c.A, sa=c.sa, Bm=c.B, sb=c.sb, C=None, D=c.buf, ws=None: B.gemm_epi_fp8_run(  # noqa: E731
+        c.plan, A, sa, Bm, sb, C, D, ws, 0, check=False)
     for name in ("A", "sa", "Bm", "sb", "D"):
         assert run(**{name: 0}) == B.GE_ERR_MISSING_ARG
     for name, t in (("A", c.A), ("Bm", c.B), ("C", c.buf), ("D", c.buf)):
         assert run(**{name: t.data_ptr() + 8}) == B.GE_ERR_MISALIGNED
     assert run(sa=c.sa.data_ptr() + 2) == B.GE_ERR_MISALIGNED
-    assert run(ws=None) == B.GE_ERR_WORKSPACE
-    assert run(n=c.ws.numel() - 1) == B.GE_ERR_WORKSPACE
-    assert run(ws=c.ws.data_ptr() + 8, n=c.ws.numel()) == B.GE_ERR_MISALIGNED
+    assert run(ws=c.buf.data_ptr() + 8) == B.GE_ERR_MISALIGNED
 
 
 @pytest.mark.gpu
