@@ -18,13 +18,13 @@
 // weights once.  So a CTA's warps are there to keep that reading going:
 //   producers take tickets and copy their rows, 1 KiB of 32 rows at a time, into a ring of
 //             shared memory (cp.async, 16 bytes a lane), several units ahead of
-//   consumers, three groups of four warps with a unit each, so that one group's waits are filled by
-//             others' work.  A group's warps share a stage's columns and multiply them by mma.sync (tcgen05
-//             would want 128 rows of tokens): a lane reads 16 consecutive bytes of a row, and what it holds
+//   consumers, a group or two of eight warps, which share a stage's columns and multiply them by mma.sync
+//             (tcgen05 would want 128 rows of tokens): a lane reads 16 consecutive bytes of a row, and what it holds
 //             is called columns 2q, 2q + 1, 2q + 8, 2q + 9 of a step; the tokens' side is read
 //             the same way, so the sum runs over the same columns
 //   watcher   waits for the h of units that are still on their way into the ring
-//   finisher  tells the GPU that a unit is done, and adds the shares of y
+//   finisher  tells the GPU that a unit is done.  Where it was the last one of its columns of y, their shares
+//             are added by the producers, which have no more to copy by then, or by the finisher
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,10 +40,11 @@
 namespace ge {
 namespace {
 
-constexpr int kGroups = GE_MOE_GROUPS, kWarps = 8;  // consumers: groups of warps that share a unit; then the
-constexpr int kProducers = 2;       // producers, each with half of the rows of every stage, ...
+constexpr int kGroups = GE_MOE_GROUPS, kWarps = 8;  // consumers: groups of warps that share a unit, ...
+constexpr int kProducers = 2;       // ... producers, each with half of the rows of every stage, ...
 constexpr int kProducer = kGroups * kWarps, kWatcher = kProducer + kProducers, kFinisher = kWatcher + 1;  // watcher, finisher
 constexpr int kThreads = 32 * (kFinisher + 1);
+constexpr int kJobs = 4;            // columns of y whose shares are to be added, at most
 constexpr int kBlock = 128;        // columns that share a scale
 constexpr int kRows = 32, kRowTiles = kRows / 16;  // a unit's rows of weights
 constexpr int kTile = 8;           // tokens of one mma
@@ -77,7 +78,7 @@ __device__ __forceinline__ int ordered(float f) {
 // One warp, one token: the k best experts and their weights.  `keys`: room for twice GE_MOE_MAX_EXPERTS pairs: what
 // experts are chosen by, in two floats (a larger one first, then the lower index), and the logits.  This runs once in
 // every CTA, so its code is short: loops are not unrolled.  (Unrolled over keys in registers it took 8 us
-// for one token and 124 us for 64; so 4 and 33.)
+// for one token and 124 us for 64 with 128 experts; so 4 and 30.)
 __device__ __noinline__ void choose(const MoeParams &p, int t, Choice &c, float2 *keys, bool say) {
   const int lane = threadIdx.x & 31;
   float2 *l = keys + GE_MOE_MAX_EXPERTS;
@@ -103,20 +104,33 @@ __device__ __noinline__ void choose(const MoeParams &p, int t, Choice &c, float2
   auto pick = [&](int some) {  // the best ones in order; whether two neighbours are close
     bool close = false;
     float last = INFINITY;
-#pragma unroll 1
-    for (int j = 0; j < some; ++j) {
-      int hi = 0x80000000, lo = 0x80000000, at = 0x7fffffff;
-#pragma unroll 1
+    int hi, lo, at;  // this lane's best, found again when it has been taken
+    auto look = [&]() {
+      hi = lo = 0x80000000;
+      at = 0x7fffffff;
+#pragma unroll 4
       for (int e = lane; e < p.E; e += 32) {
         const int h = ordered(keys[e].x), w = ordered(keys[e].y);
         if (h > hi || (h == hi && w > lo)) hi = h, lo = w, at = e;
       }
+    };
+    look();
+#pragma unroll 1
+    for (int j = 0; j < some; ++j) {
       const int best = __reduce_max_sync(0xffffffffu, hi);
-      const int rest = __reduce_max_sync(0xffffffffu, hi == best ? lo : int(0x80000000));
-      const int e = __reduce_min_sync(0xffffffffu, hi == best && lo == rest ? at : 0x7fffffff);
-      // taken: below all that are not
-      if (e % 32 == lane) keys[e] = make_float2(__int_as_float(0xffffffff), 0.f);
+      uint32_t who = __ballot_sync(0xffffffffu, hi == best);
+      if (who & (who - 1)) {  // several: the larger remainder, then the lowest index
+        const int rest = __reduce_max_sync(0xffffffffu, hi == best ? lo : int(0x80000000));
+        const int first = __reduce_min_sync(0xffffffffu, hi == best && lo == rest ? at : 0x7fffffff);
+        who = 1u << (first & 31);
+      }
+      const int e = __shfl_sync(0xffffffffu, at, __ffs(who) - 1);
       if (lane == j) expert = e;
+      if (lane == (e & 31)) {
+        keys[e] = make_float2(__int_as_float(0xffffffff), 0.f);  // taken: below all that are not
+        look();
+      }
+      __syncwarp();
       const float now = __int_as_float(ordered(__int_as_float(best)));
       close = close || last - now <= 2e-6f * fmaxf(1.f, fabsf(now));
       last = now;
@@ -248,12 +262,12 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two 8-bit floats, in the upper bytes of w's halves, as two values of type XT (exact).  FAST: all of them finite
-// numbers, to bf16 by shifting their bits into its exponent and mantissa, whose bias then is off by a power of two.
-template <int XT, int WT, bool FAST>
+// Two 8-bit floats, in the upper bytes of w's halves, as two values of type XT (exact, if they are finite).  To bf16 by
+// shifting their bits into its exponent and mantissa, whose bias then is off by a power of two.
+template <int XT, int WT>
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
   constexpr bool e4 = WT == GE_E4M3;
-  if constexpr (XT == GE_BF16 && FAST) {
+  if constexpr (XT == GE_BF16) {
     const uint32_t bits = ((w >> (e4 ? 4 : 3)) & (e4 ? 0x07f007f0u : 0x0fe00fe0u)) | (w & 0x80008000u);
     constexpr uint32_t by = e4 ? 0x7b807b80u : 0x77807780u;  // 2^120, 2^112
     const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&bits), *reinterpret_cast<const __nv_bfloat162 *>(&by));
@@ -263,13 +277,12 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
     uint32_t h;
     if constexpr (e4) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
     else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(two));
-    if constexpr (XT == GE_F16) return h;
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    return pack16(true, f.x, f.y);
+    return h;
   }
 }
 
-// whether one of four 8-bit floats is no finite number
+// Whether one of four 8-bit floats is no finite number.  A row of weights that holds one gives NaN.  (The flags are looked
+// at once for a unit: a branch for each 16 bytes took 905 us, not 791, with 64 tokens and 128 experts of 4096 x 2048.)
 template <int WT>
 __device__ __forceinline__ uint32_t special(uint32_t w) {
   return WT == GE_E4M3 ? ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w & 0x7c7c7c7cu) + 0x04040404u) & 0x80808080u;
@@ -313,11 +326,11 @@ __device__ __forceinline__ void fetch(typename Shape<WT, LO>::Tokens &b, const u
 
 // acc[row tile][token tile][chain] += a stage's rows (32) x tokens (8 per tile)^T over this warp's columns.  With one
 // tile its tokens are in b, with more they are fetched here.  8-bit weights: scales of the warp's 128 columns at s[0] (rows g)
-// and s[1] (rows g + 8), the same for both row tiles.
+// and s[1] (rows g + 8), the same for both row tiles; `odd`: what special() says of those rows.
 template <int XT, int WT, int NT, bool LO>
 __device__ __forceinline__ void consume(float (&acc)[kRowTiles][NT][kChains<NT, LO>][4], const uint8_t *stage, typename Shape<WT, LO>::Tokens &b,
-                                        int first, int bytes, const uint16_t *const (&from)[NT], int64_t rest, const float *const (&s)[2],
-                                        int warp, int lane) {
+                                        uint32_t (&odd)[kRowTiles][2], int first, int bytes, const uint16_t *const (&from)[NT], int64_t rest,
+                                        const float *const (&s)[2], int warp, int lane) {
   using S = Shape<WT, LO>;
   constexpr bool k8 = S::k8;
   const int g = lane >> 2, q = lane & 3, at = warp * S::kSteps * 64;
@@ -337,24 +350,14 @@ __device__ __forceinline__ void consume(float (&acc)[kRowTiles][NT][kChains<NT, 
       const uint4 w1 = on ? *reinterpret_cast<const uint4 *>(row + 8 * kPitch) : zero;
       if constexpr (k8) {
         const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
-        auto all = [&](auto fast) {
-          constexpr bool kFast = decltype(fast)::value;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x0[i][2 * j] = widen<XT, WT, kFast>(__byte_perm(y0[j], 0, 0x1404));
-            x0[i][2 * j + 1] = widen<XT, WT, kFast>(__byte_perm(y0[j], 0, 0x3424));
-            x1[i][2 * j] = widen<XT, WT, kFast>(__byte_perm(y1[j], 0, 0x1404));
-            x1[i][2 * j + 1] = widen<XT, WT, kFast>(__byte_perm(y1[j], 0, 0x3424));
-          }
-        };
-        if constexpr (XT == GE_BF16) {
-          uint32_t odd = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) odd |= special<WT>(y0[j]) | special<WT>(y1[j]);
-          if (__any_sync(0xffffffffu, odd != 0)) all(std::false_type{});
-          else all(std::true_type{});
-        } else {
-          all(std::false_type{});
+        for (int j = 0; j < 4; ++j) {
+          x0[i][2 * j] = widen<XT, WT>(__byte_perm(y0[j], 0, 0x1404));
+          x0[i][2 * j + 1] = widen<XT, WT>(__byte_perm(y0[j], 0, 0x3424));
+          x1[i][2 * j] = widen<XT, WT>(__byte_perm(y1[j], 0, 0x1404));
+          x1[i][2 * j + 1] = widen<XT, WT>(__byte_perm(y1[j], 0, 0x3424));
+          odd[m][0] |= special<WT>(y0[j]);
+          odd[m][1] |= special<WT>(y1[j]);
         }
       } else {
         x0[i][0] = w0.x, x0[i][1] = w0.y, x0[i][2] = w0.z, x0[i][3] = w0.w;
@@ -418,6 +421,8 @@ struct Shared {
   alignas(8) uint64_t full[kStages], empty[kStages];          // stages of the ring
   alignas(8) uint64_t taken[kQueue], ready[kQueue], out[kQueue], free[kQueue];  // a unit: named, its h there, written, forgotten
   uint32_t unit[kQueue], first[kQueue];  // which one, and its first stage's number
+  alignas(8) uint64_t given[kJobs], added[kJobs];  // shares to be added
+  int job[kJobs];                                  // of which columns
   volatile uint32_t quit;
   alignas(128) uint8_t ring[kStages][kRows * kPitch];
 };
@@ -570,18 +575,33 @@ __device__ bool do_unit(const MoeParams &p, Shared &sh, const Unit &u, Turn<kSta
     from[i] = at >= n ? nullptr : UP ? static_cast<const uint16_t *>(p.x) + int64_t(list[at] / p.k) * p.ldx : p.h + int64_t(list[at]) * p.F;
   }
   float acc[kRowTiles][NT][kChains<NT, !UP>][4] = {};
+  uint32_t odd[kRowTiles][2] = {};
   for (int j = 0; j < segments; ++j) {
     const int first = j * (kSegment / ws), bytes = K * ws - j * kSegment;
     typename Shape<WT, !UP>::Tokens b;  // (one tile's tokens are on their way while the stage is waited for)
     if constexpr (NT == 1) fetch<WT, !UP>(b, from[0], rest, first, bytes, warp, lane);
     if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.full[st.at], st.phase))) return false;
-    consume<XT, WT, NT, !UP>(acc, sh.ring[st.at], b, first, bytes, from, rest, scale, warp, lane);
+    consume<XT, WT, NT, !UP>(acc, sh.ring[st.at], b, odd, first, bytes, from, rest, scale, warp, lane);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st.at]));
     st.next();
     if constexpr (k8) {
       scale[0] += kSegment / kBlock * ld_s;
       scale[1] += kSegment / kBlock * ld_s;
+    }
+  }
+  if constexpr (k8) {
+#pragma unroll
+    for (int m = 0; m < kRowTiles; ++m) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        odd[m][i] |= __shfl_xor_sync(0xffffffffu, odd[m][i], 1);  // the lanes of a row
+        odd[m][i] |= __shfl_xor_sync(0xffffffffu, odd[m][i], 2);
+        if (odd[m][i]) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[m][n][0][2 * i] = acc[m][n][0][2 * i + 1] = NAN;
+        }
+      }
     }
   }
   // the warps' sums, 8 tokens at a time (a buffer's last readers have passed the barrier of the round between)
@@ -635,34 +655,46 @@ __device__ bool any_unit(const MoeParams &p, Shared &sh, const Unit &u, Turn<kSt
   return do_unit<XT, WT, kMostTokens / kTile, UP>(p, sh, u, st, round);
 }
 
-// y's 32 columns of all tokens: a lane adds 8 columns of a token, in the order of its choice (and of four tokens at
-// a time: what it costs is the way to the shares and back)
+// y's 32 columns of all tokens, shared by `adders` warps: a lane adds 8 columns of a token, in the order of its
+// choice.  What that costs is the way to the shares and back: eight of two tokens are under way at a time.
 template <int XT>
-__device__ void add_shares(const MoeParams &p, int col) {
-  constexpr int kAtOnce = 4;
+__device__ void add_shares(const MoeParams &p, int col, int adder, int adders) {
+  constexpr int kTokens = 2, kAtOnce = 8;
   const int lane = threadIdx.x & 31, d0 = col + (lane & 3) * 8;
   if (d0 >= p.D) return;
 #pragma unroll 1
-  for (int t0 = lane >> 2; t0 < p.T; t0 += 8 * kAtOnce) {
-    float v[kAtOnce][8] = {};
-#pragma unroll 2
-    for (int j = 0; j < p.k; ++j) {
+  for (int t0 = adder * 8 + (lane >> 2); t0 < p.T; t0 += 8 * adders * kTokens) {
+    float v[kTokens][8] = {};
+#pragma unroll 1
+    for (int j0 = 0; j0 < p.k; j0 += kAtOnce) {
+      float4 x[kTokens][kAtOnce][2];
 #pragma unroll
-      for (int i = 0; i < kAtOnce; ++i) {
-        if (t0 + 8 * i >= p.T) continue;
-        const float4 *f = reinterpret_cast<const float4 *>(p.part + (int64_t(t0 + 8 * i) * p.k + j) * p.D + d0);
-        const float4 x = __ldcg(f), y = __ldcg(f + 1);
-        v[i][0] += x.x, v[i][1] += x.y, v[i][2] += x.z, v[i][3] += x.w;
-        v[i][4] += y.x, v[i][5] += y.y, v[i][6] += y.z, v[i][7] += y.w;
-      }
+      for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const int t = t0 + i * 8 * adders;
+          const bool on = t < p.T && j0 + j < p.k;
+          const float4 *f = reinterpret_cast<const float4 *>(p.part + (int64_t(t) * p.k + j0 + j) * p.D + d0);
+          x[i][j][0] = on ? __ldcg(f) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[i][j][1] = on ? __ldcg(f + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i)
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) {
+          const float4 a = x[i][j][0], c = x[i][j][1];
+          v[i][0] += a.x, v[i][1] += a.y, v[i][2] += a.z, v[i][3] += a.w;
+          v[i][4] += c.x, v[i][5] += c.y, v[i][6] += c.z, v[i][7] += c.w;
+        }
     }
 #pragma unroll
-    for (int i = 0; i < kAtOnce; ++i) {
-      if (t0 + 8 * i >= p.T) continue;
+    for (int i = 0; i < kTokens; ++i) {
+      const int t = t0 + i * 8 * adders;
+      if (t >= p.T) continue;
       uint32_t w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = pack16(XT == GE_BF16, v[i][2 * e], v[i][2 * e + 1]);
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + int64_t(t0 + 8 * i) * p.ldy + d0) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + int64_t(t) * p.ldy + d0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
@@ -683,6 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       mbar_init(smem_u32(&sh.ready[i]), 1);
       mbar_init(smem_u32(&sh.out[i]), kWarps);
       mbar_init(smem_u32(&sh.free[i]), 1);
+    }
+    for (int i = 0; i < kJobs; ++i) {
+      mbar_init(smem_u32(&sh.given[i]), 1);
+      mbar_init(smem_u32(&sh.added[i]), kProducers);
     }
     sh.quit = 0u;
     fence_mbarrier_init();
@@ -705,8 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
     static_assert(kProducers == kRowTiles, "a row tile each");
     uint32_t filled = 0, next = 0;
     if (part == 0 && lane == 0) next = atomicAdd(&p.head->ticket, 1u);
-    int ends = 0;
     bool ok = true;
+    int ends = 0;
     while (ok) {
       uint32_t t;
       if (part == 0) {
@@ -756,6 +792,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
     }
     // (what is on its way lands before the CTA's shared memory is another's)
     asm volatile("cp.async.wait_all;" ::: "memory");
+    for (Turn<kJobs> job(0);; job.next()) {
+      if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.given[job.at], job.phase))) break;
+      const int col = sh.job[job.at];
+      if (col < 0) break;
+      add_shares<XT>(p, col, part, kProducers);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.added[job.at]));
+    }
   } else if (warp == kWatcher) {
     // Lanes look after a unit each, as many as have been taken: one by one, a unit of few columns takes
     // less time than a look at another CTA's work does.
@@ -764,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       const uint32_t some = units_there(p, sh, sh.taken, n);
       if (!some) break;
       const Turn<kQueue> at(n + lane);
-      uint32_t t = kNoUnit;
+      uint32_t t = 0;
       bool ok = true;
       if (lane < some) {
         t = sh.unit[at.at];
@@ -772,17 +816,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
         if (ok) mbar_arrive(smem_u32(&sh.ready[at.at]));
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      ends += __popc(__ballot_sync(0xffffffffu, lane < some && t == kNoUnit));
+      ends += __popc(__ballot_sync(0xffffffffu, t == kNoUnit));
       n += some;
     }
   } else if (warp == kFinisher) {
     // the same for units that have been written (and one fence for all of them)
+    Turn<kJobs> job(0);
+    auto give = [&](int col) {
+      if (lane == 0) {
+        sh.job[job.at] = col;
+        mbar_arrive(smem_u32(&sh.given[job.at]));
+      }
+      __syncwarp();
+      job.next();
+    };
     int ends = 0;
     for (uint32_t n = 0; ends < kGroups;) {
       const uint32_t some = units_there(p, sh, sh.out, n);
       if (!some) break;
       const Turn<kQueue> at(n + lane);
-      uint32_t t = kNoUnit;
+      uint32_t t = 0;
       bool last = false;
       if (lane < some) {
         t = sh.unit[at.at];
@@ -793,11 +846,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
           else if (t != 0 || !(p.debug_flags & GE_DEBUG_SKIP_FIRST_LOAD)) add_release(&p.done[sh.c.active[u.a]], 1u);
         }
       }
-      ends += __popc(__ballot_sync(0xffffffffu, lane < some && t == kNoUnit));
-      for (uint32_t left = __ballot_sync(0xffffffffu, last); left; left &= left - 1)
-        add_shares<XT>(p, units.of(__shfl_sync(0xffffffffu, t, __ffs(left) - 1)).col);
+      for (uint32_t left = __ballot_sync(0xffffffffu, last); left; left &= left - 1) {
+        const int col = units.of(__shfl_sync(0xffffffffu, t, __ffs(left) - 1)).col;
+        // (not to wait for the producers, who may wait for units that this warp forgets)
+        if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&sh.added[job.at]), job.phase ^ 1u))) give(col);
+        else add_shares<XT>(p, col, 0, 1);
+      }
+      ends += __popc(__ballot_sync(0xffffffffu, t == kNoUnit));
       n += some;
     }
+    if (__all_sync(0xffffffffu, wait_bar(p, sh, sh.added[job.at], job.phase ^ 1u))) give(-1);
   } else {
     // group i takes units i, i + kGroups, ... of the CTA
     int round = 0;
