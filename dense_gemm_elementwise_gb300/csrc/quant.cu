@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 4) quant_ker
   __shared__ __align__(16) float inverse[kB];        // columns' inverse scales
   __shared__ __align__(16) uint8_t turned[COLS ? kB * kB : 16];
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t d0 = int64_t(blockIdx.x) * kB, t0 = int64_t(blockIdx.y) * kB;
+  const int tiles_d = (p.D + kB - 1) / kB, td = blockIdx.x % tiles_d, tt = blockIdx.x / tiles_d;
+  const int64_t d0 = int64_t(td) * kB, t0 = int64_t(tt) * kB;
   const int64_t d = d0 + cg * 8, t = t0 + rg * 8;
   const int cols = static_cast<int>(min(int64_t(8), p.D - d)), rows = static_cast<int>(min(int64_t(8), p.T - t));
   constexpr int es = XT == GE_F32 ? 4 : 2;
@@ -191,8 +192,8 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 4) quant_ker
 #pragma unroll
     for (int i = 0; i < 8; ++i) row_inv[i] = col_inv[i] = inv;
     if (threadIdx.x == 0) {
-      if (p.q) p.scale[blockIdx.x * p.lds + blockIdx.y] = s;
-      if (COLS) p.scale_t[blockIdx.y * p.ldst + blockIdx.x] = s;
+      if (p.q) p.scale[td * p.lds + tt] = s;
+      if (COLS) p.scale_t[tt * p.ldst + td] = s;
     }
   } else {
     if (COLS) {
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 4) quant_ker
         for (int w = 1; w < 8; ++w) m = fmaxf(m, part[w][threadIdx.x]);
         const float s = scale_of(m, p.largest);
         inverse[threadIdx.x] = __frcp_rn(s);
-        if (d0 + threadIdx.x < p.D) p.scale_t[blockIdx.y * p.ldst + d0 + threadIdx.x] = s;
+        if (d0 + threadIdx.x < p.D) p.scale_t[tt * p.ldst + d0 + threadIdx.x] = s;
       }
     }
     if (p.q) {
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 4) quant_ker
       const float m = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], 1));
       const float s = scale_of(m, p.largest), inv = __frcp_rn(s);
       const int i = cg >> 1;
-      if ((cg & 1) == 0 && i < rows) p.scale[blockIdx.x * p.lds + t + i] = s;
+      if ((cg & 1) == 0 && i < rows) p.scale[td * p.lds + t + i] = s;
 #pragma unroll
       for (int k = 0; k < 8; ++k) row_inv[k] = __shfl_sync(0xffffffffu, inv, (lane & 16) | (2 * k));
     }
@@ -295,8 +296,7 @@ int gemm_epi_quant_plan_create(gemm_epi_quant_plan **plan, int64_t T, int64_t D,
     else if (q.bytes && *q.ld % 16 != 0) return GE_ERR_MISALIGNED;
     if (*q.ld < q.least || *q.ld > kMost) return GE_ERR_SHAPE;
   }
-  // one CTA for each 128 rows in the grid's second dimension
-  if (ceil_div(T, kB) > 65535) return GE_ERR_SHAPE;
+  if (ceil_div(T, kB) * ceil_div(D, kB) > kMost) return GE_ERR_SHAPE;  // a CTA each
   int dev = 0, sms = 0, smem = 0;
   const int st = current_device(&dev, &sms, &smem);
   if (st != GE_OK) return st;
@@ -337,7 +337,7 @@ int gemm_epi_quant_run(gemm_epi_quant_plan *pl, const void *x, void *q, float *s
   p.qt = static_cast<uint8_t *>(qt);
   p.scale_t = scale_t;
   const void *fn = pl->x == GE_F32 ? pick<GE_F32>(qt) : pl->x == GE_BF16 ? pick<GE_BF16>(qt) : pick<GE_F16>(qt);
-  const dim3 grid(static_cast<unsigned>(ceil_div(p.D, kB)), static_cast<unsigned>(ceil_div(p.T, kB)));
+  const dim3 grid(static_cast<unsigned>(ceil_div(p.D, kB) * ceil_div(p.T, kB)));
   void *args[] = {&p, &pl->vec};
   return launch_pdl(fn, grid, dim3(kQuantThreads), 0, args, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GE_OK
                                                                                                               : GE_ERR_CUDA;

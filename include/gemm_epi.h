@@ -605,8 +605,8 @@ typedef struct {
 typedef struct gemm_epi_quant_plan gemm_epi_quant_plan;
 
 /* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID (NULL, bad block or
- * option), _UNSUPPORTED (types), _SHAPE (T or D <= 0 or above 2^31 - 1, a pitch too small),
- * _MISALIGNED (a pitch of q or qt that is given and is no multiple of 16), _ARCH. */
+ * option), _UNSUPPORTED (types), _SHAPE (T or D <= 0 or above 2^31 - 1, 2^31 blocks of 128 by 128 or more, a pitch
+ * too small), _MISALIGNED (a pitch of q or qt that is given and is no multiple of 16), _ARCH. */
 int gemm_epi_quant_plan_create(gemm_epi_quant_plan **plan, int64_t T, int64_t D,
                                const ge_quant_desc *desc);
 
@@ -695,7 +695,7 @@ void gemm_epi_fp8_plan_destroy(gemm_epi_fp8_plan *plan);
  * Arithmetic: logits in fp32 pairs (about 2^-40), so that the choice is that of exact logits;
  * the experts' products are exact and summed in fp32; act(gate) * up is passed on as the sum of two
  * values of type `x` (fp16: infinite above 65504); one rounding per output.  A NaN in a token
- * reaches that token alone.  Results are bit-for-bit repeatable for a given plan and device.
+ * reaches that token alone; an 8-bit weight that is no finite number makes its row's results NaN.  Results are bit-for-bit repeatable for a given plan and device.
  */
 typedef enum { GE_SCORE_SOFTMAX = 0, GE_SCORE_SIGMOID = 1 } ge_score;
 #define GE_MOE_MAX_TOKENS 128

@@ -233,6 +233,65 @@ def test_an_expert_of_nan_reaches_those_who_chose_it():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+@pytest.mark.parametrize("w,code", [("e4m3", 0x7F), ("e4m3", 0xFF), ("e5m2", 0x7C), ("e5m2", 0xFE)])
+def test_weights_of_8_bits_that_are_no_numbers(x, w, code):
+    """A row of w_down, and of gate or up, through which it reaches all of y; no other code counts as one."""
+    for name, row in (("down", 100), ("up", 37), ("up", 128 + 90)):
+        c = Case(12, 256, 128, 6, 2, x, w)
+        c.w[name].view(torch.uint8)[2, row, 77] = code
+        c.run()
+        torch.cuda.synchronize()
+        hit = (c.routing()[0] == 2).any(1)
+        nan = c.buf[:12, :256].isnan()
+        if name == "down":
+            assert torch.equal(nan[:, 100], hit)
+            nan[:, 100] = False
+            assert not bool(nan.any())
+        else:
+            assert torch.equal(nan.all(1), hit) and torch.equal(nan.any(1), hit)
+        B.gemm_epi_moe_plan_destroy(c.plan)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("w", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("x", ["bf16", "f16"])
+def test_every_8_bit_value(x, w):
+    """All finite codes, subnormals among them, in both products."""
+    c = Case(5, 512, 256, 3, 2, x, w)
+    codes = torch.arange(256, dtype=torch.uint8, device=c.x.device)
+    codes = codes[codes.view(TYPE[w]).float().isfinite()]
+    for name in ("up", "down"):
+        v = c.w[name].view(torch.uint8)
+        v.copy_(codes[torch.arange(v.numel(), device=v.device) * 7 % codes.numel()].view(v.shape))
+        c.s[name].mul_(2.0 ** -3)
+    c.run().check()
+
+
+@pytest.mark.gpu
+def test_weights_from_the_quantiser():
+    """A layer whose experts gemm_epi_quant_run has quantised, against 64 bits of what the values stand for and, in the
+    2-norm, of the weights themselves: three products with roundings of 2^-4 at most, independent for each weight."""
+    c, d = Case(9, 400, 272, 5, 2), Case(9, 400, 272, 5, 2, w="e4m3")
+    for name in ("up", "down"):
+        for e in range(5):
+            w = c.w[name][e].contiguous()
+            rows, cols = w.shape
+            plan = B.gemm_epi_quant_plan_create(rows, cols, B.make_quant_desc("bf16", "e4m3", block="square"))
+            s = torch.empty(blocks(cols), blocks(rows), device=w.device)
+            B.gemm_epi_quant_run(plan, w, d.w[name][e], s)
+            torch.cuda.synchronize()
+            d.s[name][e] = s
+            B.gemm_epi_quant_plan_destroy(plan)
+    for k in ("x", "router"):
+        getattr(d, k).copy_(getattr(c, k))
+    c.run().check()
+    d.run().check()
+    a, b = c.buf[:9, :400].double(), d.buf[:9, :400].double()
+    assert float((a - b).norm() / a.norm()) <= 3 * 2.0 ** -4
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("w", ["bf16", "e4m3"])
 def test_another_stream_a_graph_and_the_same_bits(w):
     c = Case(10, 512, 256, 12, 3, w=w, score="sigmoid", bias=True)
@@ -255,6 +314,13 @@ def test_another_stream_a_graph_and_the_same_bits(w):
     c.x.copy_(torch.flip(c.x, [0]))  # another input, in place
     graph.replay()
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k,D", [(2, 72), (16, 1000)])
+def test_many_columns_of_y_at_once(k, D):
+    """Units of one column of k: the shares of many columns become complete faster than they are added."""
+    Case(128, D, 8, 16, k).run().check()
 
 
 @pytest.mark.gpu
