@@ -1,4 +1,4 @@
-// one group: with two, 8 tokens and 32 experts of 4096 x 1536 take 152 us instead of 145
+// one group: with two, 8 tokens and 32 experts of 4096 x 1536 take 151 us instead of 143
 #define GE_MOE_GROUPS 1
 #include "moe_kernel.cuh"
 namespace ge {

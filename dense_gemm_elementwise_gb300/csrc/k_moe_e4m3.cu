@@ -1,5 +1,5 @@
-// two groups: conversions need more warps to fill their waits (64 tokens, 128 experts of 4096 x 2048 in 791 us
-// against 885 with one)
+// two groups: conversions need more warps to fill their waits (64 tokens, 128 experts of 4096 x 2048 in 725 us
+// against 791 with one)
 #define GE_MOE_GROUPS 2
 #include "moe_kernel.cuh"
 namespace ge {

@@ -60,7 +60,8 @@ constexpr int kQueue = 8;          // units under way in a CTA
 struct Choice {
   uint16_t expert[kPairs];
   float weight[kPairs];
-  uint16_t list[kPairs];             // pairs token * k + j, those of an expert together
+  uint16_t list[kPairs];             // pairs token * k + j, those of an expert together, ...
+  uint8_t token[kPairs];             // ... and their tokens
   // experts that some token chose, once for every 32 pairs: how many of them, where in the list, and of how many entries
   uint16_t active[kEntries];
   uint8_t count[kEntries], parts[kEntries];
@@ -231,7 +232,11 @@ __device__ void make_lists(const MoeParams &p, Choice &c) {
   // An expert's pairs in any order, another one in another CTA: each has a column of its own.  But those of several
   // entries have to be shared out alike by all CTAs: in order, by a warp.
   for (int i = threadIdx.x; i < pairs; i += kThreads)
-    if (c.counter[c.expert[i]] >= 0) c.list[atomicAdd(&c.counter[c.expert[i]], 1)] = static_cast<uint16_t>(i);
+    if (c.counter[c.expert[i]] >= 0) {
+      const int at = atomicAdd(&c.counter[c.expert[i]], 1);
+      c.list[at] = static_cast<uint16_t>(i);
+      c.token[at] = static_cast<uint8_t>(i / p.k);
+    }
   const int lane = threadIdx.x & 31;
   for (int a = threadIdx.x >> 5; a < c.n_active; a += kThreads / 32) {
     const int e = c.active[a];
@@ -241,7 +246,11 @@ __device__ void make_lists(const MoeParams &p, Choice &c) {
     for (int i0 = 0; i0 < pairs; i0 += 32) {
       const bool hit = i0 + lane < pairs && c.expert[i0 + lane] == e;
       const uint32_t hits = __ballot_sync(0xffffffffu, hit);
-      if (hit) c.list[at + __popc(hits & ((1u << lane) - 1u))] = static_cast<uint16_t>(i0 + lane);
+      const int place = at + __popc(hits & ((1u << lane) - 1u));
+      if (hit) {
+        c.list[place] = static_cast<uint16_t>(i0 + lane);
+        c.token[place] = static_cast<uint8_t>((i0 + lane) / p.k);
+      }
       at += __popc(hits);
     }
   }
@@ -282,7 +291,7 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {
 }
 
 // Whether one of four 8-bit floats is no finite number.  A row of weights that holds one gives NaN.  (The flags are looked
-// at once for a unit: a branch for each 16 bytes took 905 us, not 791, with 64 tokens and 128 experts of 4096 x 2048.)
+// at once for a unit: a branch for each 16 bytes took 905 us where this took 791, with 64 tokens and 128 experts of 4096 x 2048.)
 template <int WT>
 __device__ __forceinline__ uint32_t special(uint32_t w) {
   return WT == GE_E4M3 ? ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w & 0x7c7c7c7cu) + 0x04040404u) & 0x80808080u;
@@ -300,42 +309,41 @@ struct Shape {
   static constexpr int kPer = k8 ? 16 : 8;               // columns of a lane's 16 bytes
   static constexpr int kSteps = kSegment / 64 / kWarps;  // of 64 bytes of a row, for each warp: a scale's 128 columns
   static constexpr int kHalves = LO ? 2 : 1;
-  static_assert(!k8 || kSteps * 64 == kBlock, "a block's columns");
+  static_assert(kSteps * 64 == 128, "a scale's columns; zeros are copied up to as many bytes");
   using Tokens = uint4[kSteps][kHalves][kPer / 8];       // the tokens' side of a step
 };
 
-// One token's side (nullptr: zeros) of this warp's columns of a stage, which are `first` and up of the whole; `bytes`
-// of a row exist.  (h is written by other CTAs of this launch: no __ldg.)
+// One token's side of this lane's columns of a stage, from `from` and, of what their rounding left, `rest` on; `bytes` of a
+// row exist from the lane's first on (0 for a token that does not exist).  (h is written by other CTAs of this launch: no
+// __ldg.)
 template <int WT, bool LO>
-__device__ __forceinline__ void fetch(typename Shape<WT, LO>::Tokens &b, const uint16_t *from, int64_t rest, int first, int bytes, int warp, int lane) {
+__device__ __forceinline__ void fetch(typename Shape<WT, LO>::Tokens &b, const uint16_t *from, int64_t rest, int bytes) {
   using S = Shape<WT, LO>;
-  const int q = lane & 3, at = warp * S::kSteps * 64 + q * 16;
 #pragma unroll
-  for (int i = 0; i < S::kSteps; ++i) {
-    const bool on = from && at + i * 64 < bytes;
-    const int col = first + (at + i * 64) / (S::k8 ? 1 : 2);
+  for (int l = 0; l < S::kHalves; ++l) {
+    const uint4 *v = reinterpret_cast<const uint4 *>(from + (l ? rest : 0));
 #pragma unroll
-    for (int l = 0; l < S::kHalves; ++l)
+    for (int i = 0; i < S::kSteps; ++i)
 #pragma unroll
       for (int u = 0; u < S::kPer / 8; ++u) {
-        const uint4 *v = reinterpret_cast<const uint4 *>(from + (l ? rest : 0) + col + 8 * u);
-        b[i][l][u] = !on ? make_uint4(0, 0, 0, 0) : LO ? *v : __ldg(v);
+        const uint4 *at = v + i * (S::kPer / 2) + u;  // 4 kPer columns of 2 bytes a step
+        b[i][l][u] = i * 64 >= bytes ? make_uint4(0, 0, 0, 0) : LO ? *at : __ldg(at);
       }
   }
 }
 
-// acc[row tile][token tile][chain] += a stage's rows (32) x tokens (8 per tile)^T over this warp's columns.  With one
+// acc[row tile][token tile][chain] += a stage's rows (32) x tokens (8 per tile)^T over this warp's columns, of which `bytes`
+// of a row exist (and are zeros up to whole scales' columns).  With one
 // tile its tokens are in b, with more they are fetched here.  8-bit weights: scales of the warp's 128 columns at s[0] (rows g)
 // and s[1] (rows g + 8), the same for both row tiles; `odd`: what special() says of those rows.
 template <int XT, int WT, int NT, bool LO>
 __device__ __forceinline__ void consume(float (&acc)[kRowTiles][NT][kChains<NT, LO>][4], const uint8_t *stage, typename Shape<WT, LO>::Tokens &b,
-                                        uint32_t (&odd)[kRowTiles][2], int first, int bytes, const uint16_t *const (&from)[NT], int64_t rest,
+                                        uint32_t (&odd)[kRowTiles][2], int bytes, const uint16_t *const (&from)[NT], const bool (&there)[NT], int64_t rest,
                                         const float *const (&s)[2], int warp, int lane) {
   using S = Shape<WT, LO>;
   constexpr bool k8 = S::k8;
   const int g = lane >> 2, q = lane & 3, at = warp * S::kSteps * 64;
   if (at >= bytes) return;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   float s0 = 0.f, s1 = 0.f;
   if constexpr (k8) s0 = __ldg(s[0]), s1 = __ldg(s[1]);
 #pragma unroll
@@ -343,11 +351,8 @@ __device__ __forceinline__ void consume(float (&acc)[kRowTiles][NT][kChains<NT, 
     uint32_t x0[S::kSteps][S::kPer / 2], x1[S::kSteps][S::kPer / 2];
 #pragma unroll
     for (int i = 0; i < S::kSteps; ++i) {
-      const int byte = at + i * 64 + q * 16;
-      const bool on = byte < bytes;
-      const uint8_t *row = stage + (m * 16 + g) * kPitch + byte;
-      const uint4 w0 = on ? *reinterpret_cast<const uint4 *>(row) : zero;
-      const uint4 w1 = on ? *reinterpret_cast<const uint4 *>(row + 8 * kPitch) : zero;
+      const uint8_t *row = stage + (m * 16 + g) * kPitch + at + i * 64 + q * 16;
+      const uint4 w0 = *reinterpret_cast<const uint4 *>(row), w1 = *reinterpret_cast<const uint4 *>(row + 8 * kPitch);
       if constexpr (k8) {
         const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
@@ -366,7 +371,7 @@ __device__ __forceinline__ void consume(float (&acc)[kRowTiles][NT][kChains<NT, 
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      if constexpr (NT > 1) fetch<WT, LO>(b, from[n], rest, first, bytes, warp, lane);
+      if constexpr (NT > 1) fetch<WT, LO>(b, from[n], rest, there[n] ? bytes - at - q * 16 : 0);
       float sum[kChains<NT, LO>][4] = {};
 #pragma unroll
       for (int i = 0; i < S::kSteps; ++i)
@@ -415,12 +420,19 @@ __device__ __forceinline__ float round_trip(uint16_t v) {
   else return __half2float(__ushort_as_half(v));
 }
 
+// A unit of work: `a` the active expert, `col` its first column of h or of y.
+struct Unit {
+  int a, col;
+  bool up;
+};
+
 struct Shared {
   Choice c;
   Sums sums[kGroups][2];
   alignas(8) uint64_t full[kStages], empty[kStages];          // stages of the ring
   alignas(8) uint64_t taken[kQueue], ready[kQueue], out[kQueue], free[kQueue];  // a unit: named, its h there, written, forgotten
   uint32_t unit[kQueue], first[kQueue];  // which one, and its first stage's number
+  Unit what[kQueue];
   alignas(8) uint64_t given[kJobs], added[kJobs];  // shares to be added
   int job[kJobs];                                  // of which columns
   volatile uint32_t quit;
@@ -430,7 +442,12 @@ struct Shared {
 constexpr uint32_t kNoUnit = 0xffffffffu;
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// zeros in their place
+__device__ __forceinline__ void clear16(uint32_t dst, const void *any) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, 0;" ::"r"(dst), "l"(any) : "memory");
 }
 
 // this thread arrives on a barrier once its copies so far have landed
@@ -498,12 +515,6 @@ __device__ bool wait_for(const MoeParams &p, Shared &sh, const uint32_t *counter
   }
 }
 
-// A unit of work: `a` the active expert, `col` its first column of h or of y.
-struct Unit {
-  int a, col;
-  bool up;
-};
-
 struct Units {
   uint32_t up_cols, down_cols, n_up, n_all;
   __device__ __forceinline__ Units(const MoeParams &p, int n_active) {
@@ -556,7 +567,8 @@ __device__ bool do_unit(const MoeParams &p, Shared &sh, const Unit &u, Turn<kSta
   const Choice &c = sh.c;
   const int e = c.active[u.a], n = c.count[u.a];
   const uint16_t *list = c.list + c.begin[u.a];
-  const int K = UP ? p.D : p.F, segments = (K * ws + kSegment - 1) / kSegment;
+  using S = Shape<WT, !UP>;
+  const int K = UP ? p.D : p.F;
   const int64_t rest = int64_t(p.T) * p.k * p.F;
   // Scales of rows: a unit's columns start at a multiple of 16 (of 32), so gate's lie in one block of rows, w_down's too;
   // up's start at F more, a multiple of 16.
@@ -569,22 +581,28 @@ __device__ bool do_unit(const MoeParams &p, Shared &sh, const Unit &u, Turn<kSta
     scale[1] = f + (UP ? p.F + u.col : u.col) / kBlock;
   }
   const uint16_t *from[NT];
+  bool there[NT];
+  // this lane's first column of a stage
+  const int mine = warp * S::kSteps * 64 + q * 16, col0 = mine / ws;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int at = i * kTile + g;
-    from[i] = at >= n ? nullptr : UP ? static_cast<const uint16_t *>(p.x) + int64_t(list[at] / p.k) * p.ldx : p.h + int64_t(list[at]) * p.F;
+    there[i] = at < n;
+    from[i] = (UP ? static_cast<const uint16_t *>(p.x) : p.h) + col0;
+    if (there[i]) from[i] += UP ? int64_t(c.token[c.begin[u.a] + at]) * p.ldx : int64_t(list[at]) * p.F;
   }
   float acc[kRowTiles][NT][kChains<NT, !UP>][4] = {};
   uint32_t odd[kRowTiles][2] = {};
-  for (int j = 0; j < segments; ++j) {
-    const int first = j * (kSegment / ws), bytes = K * ws - j * kSegment;
-    typename Shape<WT, !UP>::Tokens b;  // (one tile's tokens are on their way while the stage is waited for)
-    if constexpr (NT == 1) fetch<WT, !UP>(b, from[0], rest, first, bytes, warp, lane);
+  for (int bytes = K * ws; bytes > 0; bytes -= kSegment) {
+    typename S::Tokens b;  // (one tile's tokens are on their way while the stage is waited for)
+    if constexpr (NT == 1) fetch<WT, !UP>(b, from[0], rest, there[0] ? bytes - mine : 0);
     if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.full[st.at], st.phase))) return false;
-    consume<XT, WT, NT, !UP>(acc, sh.ring[st.at], b, odd, first, bytes, from, rest, scale, warp, lane);
+    consume<XT, WT, NT, !UP>(acc, sh.ring[st.at], b, odd, bytes, from, there, rest, scale, warp, lane);
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.empty[st.at]));
     st.next();
+#pragma unroll
+    for (int i = 0; i < NT; ++i) from[i] += kSegment / ws;
     if constexpr (k8) {
       scale[0] += kSegment / kBlock * ld_s;
       scale[1] += kSegment / kBlock * ld_s;
@@ -754,6 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
         if (lane == 0) {
           sh.unit[slot.at] = t;
           sh.first[slot.at] = filled;
+          if (t != kNoUnit) sh.what[slot.at] = units.of(t);
           mbar_arrive(smem_u32(&sh.taken[slot.at]));
         }
         __syncwarp();
@@ -762,12 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
         if (!ok) break;
         t = sh.unit[slot.at];
       }
+      const Unit u = sh.what[slot.at];
       slot.next();
       if (t == kNoUnit) {
         if (++ends == kGroups) break;  // one for each group
         continue;
       }
-      const Unit u = units.of(t);
       const int e = sh.c.active[u.a], K = u.up ? p.D : p.F;
       const uint8_t *w = static_cast<const uint8_t *>(u.up ? p.w_up : p.w_down);
       w += (int64_t(e) * (u.up ? 2 * int64_t(p.F) : int64_t(p.D)) + u.col) * K * ws + lane * 16;
@@ -778,13 +797,32 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       for (int at = 0; at < K * ws; at += kSegment, w += kSegment) {
         ok = __all_sync(0xffffffffu, wait_bar(p, sh, sh.empty[st.at], st.phase ^ 1u));
         if (!ok) break;
-        const int bytes = min(kSegment, K * ws - at) - lane * 16;
+        const int left = min(kSegment, K * ws - at), bytes = left - lane * 16;
         const uint32_t to = smem_u32(sh.ring[st.at]) + part * 16 * kPitch + lane * 16;
+        if (rows == 16 && left == kSegment) {
+          // (with as few instructions as can be: two warps issue all of an SM's copies)
+          const uint8_t *row = w;
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
+          for (int r = 0; r < 8; ++r, row += pitch) {
+            const uint8_t *row8 = row + second;
 #pragma unroll
-          for (int j = 0; j < kSegment; j += 512)
-            if (r < rows && j < bytes) copy16(to + r * kPitch + j, w + (r & 7) * pitch + (r & 8 ? second : 0) + j);
+            for (int j = 0; j < kSegment; j += 512) {
+              copy16(to + r * kPitch + j, row + j);
+              copy16(to + (r + 8) * kPitch + j, row8 + j);
+            }
+          }
+        } else {
+#pragma unroll 4
+          for (int r = 0; r < rows; ++r)
+#pragma unroll
+            for (int j = 0; j < kSegment; j += 512)
+              if (j < bytes) copy16(to + r * kPitch + j, w + (r & 7) * pitch + (r & 8 ? second : 0) + j);
+        }
+        if (left % 128 != 0) {  // up to a consumer's whole columns: fewer than 8 lanes' worth in each row
+          const int end = left + (lane & 7) * 16;
+          if (end < (left + 127) / 128 * 128)
+            for (int r = lane >> 3; r < 16; r += 4) clear16(to + r * kPitch - lane * 16 + end, w);
+        }
         arrive_after_copies(smem_u32(&sh.full[st.at]));
         st.next();
         ++filled;
@@ -812,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       bool ok = true;
       if (lane < some) {
         t = sh.unit[at.at];
-        ok = t == kNoUnit || t < units.n_up || wait_for(p, sh, &p.done[sh.c.active[units.of(t).a]], units.up_cols * sh.c.parts[units.of(t).a]);
+        ok = t == kNoUnit || t < units.n_up || wait_for(p, sh, &p.done[sh.c.active[sh.what[at.at].a]], units.up_cols * sh.c.parts[sh.what[at.at].a]);
         if (ok) mbar_arrive(smem_u32(&sh.ready[at.at]));
       }
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -836,21 +874,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       if (!some) break;
       const Turn<kQueue> at(n + lane);
       uint32_t t = 0;
+      int col = 0;
       bool last = false;
       if (lane < some) {
         t = sh.unit[at.at];
+        const Unit u = sh.what[at.at];
+        col = u.col;
         mbar_arrive(smem_u32(&sh.free[at.at]));
         if (t != kNoUnit) {
-          const Unit u = units.of(t);
           if (!u.up) last = add_acq_rel(&p.shares[u.col / kDownCols], 1u) == static_cast<uint32_t>(sh.c.n_active) - 1u;
           else if (t != 0 || !(p.debug_flags & GE_DEBUG_SKIP_FIRST_LOAD)) add_release(&p.done[sh.c.active[u.a]], 1u);
         }
       }
       for (uint32_t left = __ballot_sync(0xffffffffu, last); left; left &= left - 1) {
-        const int col = units.of(__shfl_sync(0xffffffffu, t, __ffs(left) - 1)).col;
+        const int its = __shfl_sync(0xffffffffu, col, __ffs(left) - 1);
         // (not to wait for the producers, who may wait for units that this warp forgets)
-        if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&sh.added[job.at]), job.phase ^ 1u))) give(col);
-        else add_shares<XT>(p, col, 0, 1);
+        if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&sh.added[job.at]), job.phase ^ 1u))) give(its);
+        else add_shares<XT>(p, its, 0, 1);
       }
       ends += __popc(__ballot_sync(0xffffffffu, t == kNoUnit));
       n += some;
@@ -864,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       if (!__all_sync(0xffffffffu, wait_bar(p, sh, sh.ready[at.at], at.phase))) break;
       const uint32_t t = sh.unit[at.at];
       if (t != kNoUnit) {
-        const Unit u = units.of(t);
+        const Unit u = sh.what[at.at];
         const Turn<kStages> from(sh.first[at.at]);
         if (!(u.up ? any_unit<XT, WT, true>(p, sh, u, from, round) : any_unit<XT, WT, false>(p, sh, u, from, round))) break;
       }
