@@ -76,81 +76,123 @@ __device__ __forceinline__ int ordered(float f) {
   return b ^ ((b >> 31) & 0x7fffffff);
 }
 
-// One warp, one token: the k best experts and their weights.  `keys`: room for twice GE_MOE_MAX_EXPERTS pairs: what
-// experts are chosen by, in two floats (a larger one first, then the lower index), and the logits.  This runs once in
-// every CTA, so its code is short: loops are not unrolled.  (Unrolled over keys in registers it took 8 us
-// for one token and 124 us for 64 with 128 experts; so 4 and 30.)
-__device__ __noinline__ void choose(const MoeParams &p, int t, Choice &c, float2 *keys, bool say) {
+// What an expert is chosen by, two floats, as integers of the same order; an upper one of 0 is below all.
+__device__ __forceinline__ uint32_t key_of(float f) { return static_cast<uint32_t>(ordered(f + 0.f)) ^ 0x80000000u; }  // (-0 is 0)
+__device__ __forceinline__ float of_key(uint32_t k) { return __int_as_float(ordered(__int_as_float(static_cast<int>(k ^ 0x80000000u)))); }
+
+__device__ __forceinline__ float sigmoid(float2 v) {  // v.y: what the rounding of the argument left
+  const float e = expf(-fabsf(v.x)) * (v.x < 0.f ? 1.f + v.y : 1.f - v.y);
+  return (v.x < 0.f ? e : 1.f) / (1.f + e);
+}
+
+struct ChoiceSpace {  // a warp's
+  float2 logits[GE_MOE_MAX_EXPERTS];
+  alignas(16) uint32_t upper[GE_MOE_MAX_EXPERTS];
+  uint32_t lower[GE_MOE_MAX_EXPERTS];
+  uint32_t best[32];   // upper keys of the chosen
+  int32_t which[32];
+  __device__ __forceinline__ void put(int e, float hi, float lo) {  // a NaN counts as -infinity
+    upper[e] = key_of(hi == hi ? hi : -INFINITY);
+    lower[e] = key_of(isfinite(hi) ? lo : 0.f);
+  }
+};
+
+// The `some` best of up to 32 N experts, by how many are above each: a single warp's time is what it issues one after
+// another, and these comparisons do not wait for each other.  Upper keys alone: false where two of the best are equal.
+template <int N>
+__device__ __forceinline__ bool rank(int E, int some, ChoiceSpace &s) {
   const int lane = threadIdx.x & 31;
-  float2 *l = keys + GE_MOE_MAX_EXPERTS;
-  constexpr float kNone = -INFINITY;
-  const bool softmax = p.score == GE_SCORE_SOFTMAX;
-  float top = kNone;
-#pragma unroll 4
-  for (int e = lane; e < p.E; e += 32) {
-    const float2 v = __ldcg(p.logits + int64_t(t) * p.E + e);
-    keys[e] = l[e] = v;
-    top = fmaxf(top, v.x);
+  uint32_t mine[N];
+  int above[N] = {};
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine[i] = i * 32 + lane < E ? s.upper[i * 32 + lane] : 0;
+  for (int e = E + lane; e < (E + 3) / 4 * 4; e += 32) s.upper[e] = 0;
+  __syncwarp();
+#pragma unroll 2
+  for (int e = 0; e < E; e += 4) {
+    const uint4 o = *reinterpret_cast<const uint4 *>(&s.upper[e]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) above[i] += (o.x > mine[i]) + (o.y > mine[i]) + (o.z > mine[i]) + (o.w > mine[i]);
   }
-  top = __int_as_float(ordered(__int_as_float(__reduce_max_sync(0xffffffffu, ordered(top)))));
-  float sum = 0.f;
-  if (softmax) {
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) sum += expf((keys[e].x - top) + keys[e].y);
-#pragma unroll 1
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  // lane j: the j-th expert
-  int expert = 0;
-  auto pick = [&](int some) {  // the best ones in order; whether two neighbours are close
-    bool close = false;
-    float last = INFINITY;
-    int hi, lo, at;  // this lane's best, found again when it has been taken
+  uint32_t places = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (mine[i] != 0 && above[i] < some) {
+      s.best[above[i]] = mine[i];
+      s.which[above[i]] = i * 32 + lane;
+      places |= 1u << above[i];
+    }
+  return __reduce_or_sync(0xffffffffu, places) == (1u << some) - 1u;
+}
+
+// The `some` best experts in order, of equal keys the lower index first; whether two neighbours' upper keys are close.
+__device__ __forceinline__ bool find_best(int E, int some, ChoiceSpace &s) {
+  const int lane = threadIdx.x & 31;
+  const bool ranked = E <= 32 ? rank<1>(E, some, s) : E <= 64 ? rank<2>(E, some, s) : E <= 128 ? rank<4>(E, some, s) : false;
+  if (!ranked) {
+    uint32_t hi, lo;  // this lane's best, found again when it has been taken
+    int at;
     auto look = [&]() {
-      hi = lo = 0x80000000;
-      at = 0x7fffffff;
+      hi = lo = 0;
+      at = E;
 #pragma unroll 4
-      for (int e = lane; e < p.E; e += 32) {
-        const int h = ordered(keys[e].x), w = ordered(keys[e].y);
-        if (h > hi || (h == hi && w > lo)) hi = h, lo = w, at = e;
+      for (int e = lane; e < E; e += 32) {
+        const uint32_t h = s.upper[e], w = s.lower[e];
+        if (h > hi || (h == hi && h != 0 && w > lo)) hi = h, lo = w, at = e;
       }
     };
     look();
 #pragma unroll 1
     for (int j = 0; j < some; ++j) {
-      const int best = __reduce_max_sync(0xffffffffu, hi);
-      uint32_t who = __ballot_sync(0xffffffffu, hi == best);
-      if (who & (who - 1)) {  // several: the larger remainder, then the lowest index
-        const int rest = __reduce_max_sync(0xffffffffu, hi == best ? lo : int(0x80000000));
-        const int first = __reduce_min_sync(0xffffffffu, hi == best && lo == rest ? at : 0x7fffffff);
-        who = 1u << (first & 31);
-      }
-      const int e = __shfl_sync(0xffffffffu, at, __ffs(who) - 1);
-      if (lane == j) expert = e;
-      if (lane == (e & 31)) {
-        keys[e] = make_float2(__int_as_float(0xffffffff), 0.f);  // taken: below all that are not
+      const uint32_t most = __reduce_max_sync(0xffffffffu, hi), rest = __reduce_max_sync(0xffffffffu, hi == most ? lo : 0u);
+      const int e = __reduce_min_sync(0xffffffffu, hi == most && lo == rest ? at : E);
+      if (at == e) {
+        s.best[j] = most;
+        s.which[j] = e;
+        s.upper[e] = 0;
         look();
       }
       __syncwarp();
-      const float now = __int_as_float(ordered(__int_as_float(best)));
-      close = close || last - now <= 2e-6f * fmaxf(1.f, fabsf(now));
-      last = now;
     }
-    return close;
-  };
-  // keys: without a bias the logits themselves.  (A NaN is no key, but its weight is NaN all the same; -0 is 0.)
-  auto clean = [](float f) { return f == f ? f + 0.f : kNone; };
+  }
   __syncwarp();
+  const float now = lane < some ? of_key(s.best[lane]) : 0.f;
+  const float next = __shfl_down_sync(0xffffffffu, now, 1);
+  return __any_sync(0xffffffffu, lane + 1 < some && now - next <= 2e-6f * fmaxf(1.f, fabsf(now)));
+}
+
+// One warp, one token: the k best experts and their weights.  This runs once in every CTA, so its code is short.
+// (Unrolled over keys in registers it took 8 us for one token and 124 us for 64 with 128 experts.)
+__device__ __noinline__ void choose(const MoeParams &p, int t, Choice &c, ChoiceSpace &s, bool say) {
+  const int lane = threadIdx.x & 31;
+  const bool softmax = p.score == GE_SCORE_SOFTMAX;
+  const float2 *l = s.logits;
+  float top = -INFINITY;
+#pragma unroll 4
+  for (int e = lane; e < p.E; e += 32) {
+    const float2 v = __ldcg(p.logits + int64_t(t) * p.E + e);
+    s.logits[e] = v;
+    if (!p.bias) s.put(e, v.x, v.y);
+    top = fmaxf(top, v.x);
+  }
+  float sum = 0.f;
+  if (softmax && (p.bias || !p.renormalise)) {
+    top = __int_as_float(ordered(__int_as_float(__reduce_max_sync(0xffffffffu, ordered(top)))));
+#pragma unroll 1
+    for (int e = lane; e < p.E; e += 32) sum += expf((l[e].x - top) + l[e].y);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
   if (p.bias) {
 #pragma unroll 1
     for (int e = lane; e < p.E; e += 32) {
-      const float2 v = keys[e];
-      const float s = softmax ? expf((v.x - top) + v.y) / sum : 1.f / (1.f + expf(-v.x) * (1.f - v.y));
-      keys[e] = make_float2(clean(s + __ldg(p.bias + e)), 0.f);
+      const float2 v = l[e];
+      s.put(e, (softmax ? expf((v.x - top) + v.y) / sum : sigmoid(v)) + __ldg(p.bias + e), 0.f);
     }
+    __syncwarp();
     // Scores in fp32 are off by a few 1e-7 of themselves: where two of the k + 1 best lie closer than
     // that, all are computed again in 64 bits, which the GPU does slowly.
-    if (pick(min(p.k + 1, p.E))) {
+    if (find_best(p.E, min(p.k + 1, p.E), s)) {
       double all = 0.0;
       if (softmax) {
 #pragma unroll 1
@@ -160,31 +202,34 @@ __device__ __noinline__ void choose(const MoeParams &p, int t, Choice &c, float2
       }
 #pragma unroll 1
       for (int e = lane; e < p.E; e += 32) {
-        const float2 v = l[e];
-        const double x = double(v.x) + double(v.y);
-        const double key = exp(softmax ? x - double(top) : -x);
-        const double s = (softmax ? key / all : 1.0 / (1.0 + key)) + double(__ldg(p.bias + e));
-        const float hi = clean(static_cast<float>(s));
-        const float lo = isfinite(hi) ? static_cast<float>(s - double(hi)) + 0.f : 0.f;
-        keys[e] = make_float2(hi, lo);
+        const double x = double(l[e].x) + double(l[e].y), ex = exp(softmax ? x - double(top) : -x);
+        const double score = (softmax ? ex / all : 1.0 / (1.0 + ex)) + double(__ldg(p.bias + e));
+        const float hi = static_cast<float>(score);
+        s.put(e, hi, static_cast<float>(score - double(hi)));
       }
-      pick(p.k);
+      __syncwarp();
+      find_best(p.E, p.k, s);
     }
   } else {
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) keys[e] = make_float2(clean(keys[e].x), keys[e].x == keys[e].x ? keys[e].y + 0.f : 0.f);
-    pick(p.k);
+    __syncwarp();
+    find_best(p.E, p.k, s);
   }
-  float w = 0.f;
-  if (lane < p.k) {
-    const float2 v = l[expert];
-    w = softmax ? expf((v.x - top) + v.y) / sum : 1.f / (1.f + expf(-v.x) * (1.f - v.y));
-  }
+  // lane j: the j-th expert
+  const int expert = lane < p.k ? s.which[lane] : 0;
+  const float2 v = lane < p.k ? l[expert] : make_float2(-INFINITY, 0.f);
+  float w;
   if (p.renormalise) {
-    float total = 0.f;
-#pragma unroll 1
-    for (int j = 0; j < p.k; ++j) total += __shfl_sync(0xffffffffu, w, j);
+    // what cancels is left out, so that scores of nothing but far experts do not vanish: softmax's sum, and
+    // the largest one's exponential where all are small
+    const float m = __int_as_float(ordered(__int_as_float(__reduce_max_sync(0xffffffffu, ordered(v.x == v.x ? v.x : -INFINITY)))));
+    w = softmax || m < 0.f ? expf((v.x - m) + v.y) : 0.f;
+    if (!softmax) w = m < 0.f ? w / (1.f + expf(v.x)) : sigmoid(v);
+    float total = lane < p.k ? w : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     w /= total;
+  } else {
+    w = softmax ? expf((v.x - top) + v.y) / sum : sigmoid(v);
   }
   if (lane < p.k) {
     w *= p.route_scale;
@@ -742,11 +787,11 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
     fence_mbarrier_init();
   }
   // (the ring is not in use yet: keys lie there)
-  static_assert((kThreads / 32) * 2 * GE_MOE_MAX_EXPERTS * sizeof(float2) <= sizeof(sh.ring), "room for keys");
-  float2 *keys = reinterpret_cast<float2 *>(&sh.ring[0][0]) + warp * 2 * GE_MOE_MAX_EXPERTS;
+  static_assert((kThreads / 32) * sizeof(ChoiceSpace) <= sizeof(sh.ring), "room for choices");
+  ChoiceSpace &space = reinterpret_cast<ChoiceSpace *>(&sh.ring[0][0])[warp];
   griddep_wait();
   griddep_launch_dependents();
-  for (int t = warp; t < p.T; t += kThreads / 32) choose(p, t, sh.c, keys, blockIdx.x == 0);
+  for (int t = warp; t < p.T; t += kThreads / 32) choose(p, t, sh.c, space, blockIdx.x == 0);
   __syncthreads();
   make_lists(p, sh.c);
   const Units units(p, sh.c.n_active);

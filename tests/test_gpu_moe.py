@@ -196,6 +196,27 @@ def test_choices_between_logits_that_fp32_does_not_tell_apart(kw, router):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("score,bias", [("sigmoid", False), ("sigmoid", True), ("softmax", True)])
+def test_scores_too_small_for_fp32_are_weighed_against_each_other(score, bias):
+    c = Case(6, 64, 64, 41, 5, score=score, bias=bias)
+    e = torch.arange(41, device=c.x.device)
+    c.x.zero_()
+    c.x[:, 0] = 1.0
+    c.router.zero_()
+    c.router[:, 0] = -(100.0 + e) if score == "sigmoid" else -4.0 * e
+    if bias:
+        c.bias.copy_(2.0 * e)
+    c.run().check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(31, 5), (32, 16), (33, 1), (128, 16), (129, 16), (512, 16), (511, 3)])
+@pytest.mark.parametrize("kw", [dict(), dict(bias=True, score="sigmoid"), dict(bias=True)])
+def test_numbers_of_experts(E, k, kw):
+    Case(19, 128, 16, E, k, **kw).run().check()
+
+
+@pytest.mark.gpu
 def test_large_logits():
     for score in ("softmax", "sigmoid"):
         c = Case(9, 256, 64, 10, 3, score=score, norm=False)
