@@ -542,24 +542,6 @@ __device__ __forceinline__ bool wait_bar(const MoeParams &p, Shared &sh, const u
   }
 }
 
-// an expert's h: false where the time ran out or another CTA's did
-__device__ bool wait_for(const MoeParams &p, Shared &sh, const uint32_t *counter, uint32_t want) {
-  if (load_acquire(counter) >= want) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    if (load_acquire(counter) >= want) return true;
-    if (load_acquire(&p.head->abort)) {
-      sh.quit = 1u;
-      return false;
-    }
-    if (globaltimer_ns() - t0 > p.timeout_ns) {
-      give_up(p, sh);
-      return false;
-    }
-    __nanosleep(64);
-  }
-}
-
 struct Units {
   uint32_t up_cols, down_cols, n_up, n_all;
   __device__ __forceinline__ Units(const MoeParams &p, int n_active) {
@@ -885,21 +867,45 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
     }
   } else if (warp == kWatcher) {
     // Lanes look after a unit each, as many as have been taken: one by one, a unit of few columns takes
-    // less time than a look at another CTA's work does.
+    // less time than a look at another CTA's work does.  (Units that wait for nothing are passed on before any
+    // wait: h may be theirs.)
     int ends = 0;
     for (uint32_t n = 0; ends < kGroups;) {
       const uint32_t some = units_there(p, sh, sh.taken, n);
       if (!some) break;
       const Turn<kQueue> at(n + lane);
-      uint32_t t = 0;
+      const uint32_t t = lane < some ? sh.unit[at.at] : 0;
+      ends += __popc(__ballot_sync(0xffffffffu, t == kNoUnit));
+      bool waits = lane < some && t != kNoUnit && t >= units.n_up;
+      if (lane < some && !waits) mbar_arrive(smem_u32(&sh.ready[at.at]));
+      const uint32_t *counter = p.done;
+      uint32_t want = 0;
+      if (waits) {
+        const int a = sh.what[at.at].a;
+        counter += sh.c.active[a];
+        want = units.up_cols * sh.c.parts[a];
+      }
       bool ok = true;
-      if (lane < some) {
-        t = sh.unit[at.at];
-        ok = t == kNoUnit || t < units.n_up || wait_for(p, sh, &p.done[sh.c.active[sh.what[at.at].a]], units.up_cols * sh.c.parts[sh.what[at.at].a]);
-        if (ok) mbar_arrive(smem_u32(&sh.ready[at.at]));
+      const uint64_t t0 = __any_sync(0xffffffffu, waits) ? globaltimer_ns() : 0;
+      while (true) {
+        if (waits && load_acquire(counter) >= want) {
+          mbar_arrive(smem_u32(&sh.ready[at.at]));
+          waits = false;
+        }
+        if (!__any_sync(0xffffffffu, waits)) break;
+        if (lane == 0) {
+          if (load_acquire(&p.head->abort)) {
+            sh.quit = 1u;
+          } else if (globaltimer_ns() - t0 > p.timeout_ns) {
+            give_up(p, sh);
+          }
+        }
+        __syncwarp();
+        ok = !sh.quit;
+        if (!__all_sync(0xffffffffu, ok)) break;
+        __nanosleep(64);
       }
       if (!__all_sync(0xffffffffu, ok)) break;
-      ends += __popc(__ballot_sync(0xffffffffu, t == kNoUnit));
       n += some;
     }
   } else if (warp == kFinisher) {
@@ -933,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
       }
       for (uint32_t left = __ballot_sync(0xffffffffu, last); left; left &= left - 1) {
         const int its = __shfl_sync(0xffffffffu, col, __ffs(left) - 1);
+        __syncwarp();  // (what that lane's counter has shown is there for all)
         // (not to wait for the producers, who may wait for units that this warp forgets)
         if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&sh.added[job.at]), job.phase ^ 1u))) give(its);
         else add_shares<XT>(p, its, 0, 1);

@@ -345,6 +345,17 @@ def test_many_columns_of_y_at_once(k, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("w", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T,D,F,E,k", [(1, 32, 16, 1, 1), (1, 96, 48, 2, 1), (2, 4096, 16, 3, 2), (5, 32, 512, 4, 2)])
+def test_a_cta_with_units_that_wait_for_its_own(T, D, F, E, k, w):
+    """Few units: a CTA takes some of h together with those that wait for it, in every mixture that comes up."""
+    c = Case(T, D, F, E, k, w=w)
+    for _ in range(200):
+        c.run()
+    c.check()
+
+
+@pytest.mark.gpu
 def test_two_at_once():
     """Two layers on two streams, each with its own workspace, more work than the GPU holds at a time."""
     cs = [Case(64, 1024, 512, 40, 4, seed=i) for i in range(2)]
