@@ -45,11 +45,13 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   p.raster_group = num_m <= 16 ? static_cast<int32_t>(num_m) : 12;
   p.a_rows = pl->cg == 1 ? static_cast<int32_t>(std::min<int64_t>(128, round_up(M, 8))) : 128;
   const int stage = 128 * 128 + 128 * bn / pl->cg;
-  const int fixed = 1024 + static_cast<int>(kF8BarBytes + fp8_scale_bytes(bn, square));
+  const bool turned = pl->d.ldd * size_of(pl->d.d) % 16 != 0;
+  const int fixed = 1024 + static_cast<int>(kF8BarBytes + fp8_scale_bytes(bn, square) + (turned ? kF8TurnBytes : 0u));
   p.stages = std::min(kMaxStages, (max_smem - fixed) / stage);
   if (p.stages < 2) return GE_ERR_SMEM;
   p.off_B = static_cast<uint32_t>(p.stages * 128 * 128);
   p.off_bar = static_cast<uint32_t>(p.stages * stage);
+  p.off_turn = p.off_bar + kF8BarBytes + fp8_scale_bytes(bn, square);
   // the kernel's warps pass registers on, which have to be there
   cudaFuncAttributes fa;
   if (cudaFuncGetAttributes(&fa, pl->fn) != cudaSuccess || fa.numRegs < kF8Regs) {
@@ -173,8 +175,9 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
   p.sb = scale_b;
   p.c = C;
   p.d = D;
-  auto rows32 = [&](const void *q) { return !q || ((reinterpret_cast<uintptr_t>(q) | static_cast<uintptr_t>(p.ldd * size_of(p.dt))) & 31u) == 0; };
-  p.vec = rows32(C) && rows32(D);
+  // (bases are whole 16 bytes)
+  const int64_t pitch = p.ldd * size_of(p.dt);
+  p.vec = pitch % 16 != 0 ? 0 : pitch % 32 != 0 || ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(D)) & 31u) != 0 ? 1 : 2;
   void *args[] = {&p};
   return launch_pdl(pl->fn, dim3(static_cast<unsigned>(pl->grid)), dim3(kF8Threads), pl->smem, args, static_cast<cudaStream_t>(stream),
                     pl->cluster) == cudaSuccess ? GE_OK : GE_ERR_CUDA;

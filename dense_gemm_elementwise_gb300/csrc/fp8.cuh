@@ -20,10 +20,10 @@ struct Fp8Params {
   int32_t num_kb, num_m_blk, num_n_blk, raster_group;
   int32_t slices, kb_split;  // a tile's k-blocks are shared by the `slices` CTAs of a cluster, kb_split each
   int32_t stages;
-  int32_t a_e5m2, b_e5m2, dt, vec;  // vec: rows of C and D are whole 32-byte units
+  int32_t a_e5m2, b_e5m2, dt, vec;  // vec: rows of C and D are whole units of 32 bytes (2), of 16 (1), or neither (0)
   int32_t a_rows;          // rows of an A tile that are loaded (one CTA)
   uint32_t debug_flags;
-  uint32_t off_B, off_bar;
+  uint32_t off_B, off_bar, off_turn;
 };
 
 constexpr int kF8Epi0 = 4;                // warps: producer, two MMA, scales, 8 epilogue
@@ -38,6 +38,10 @@ __host__ __device__ constexpr int fp8_batch(bool square) { return square ? 8 : 4
 __host__ __device__ constexpr uint32_t fp8_scale_bytes(int bn, bool square) {
   return 2u * 4u * static_cast<uint32_t>(fp8_batch(square)) * static_cast<uint32_t>(128 + (square ? 2 : bn));
 }
+
+// Rows of no whole 16 bytes: an epilogue warp's 32 x 32 sums on their way to D
+constexpr int kF8TurnPitch = 33;
+constexpr uint32_t kF8TurnBytes = 8u * 32u * kF8TurnPitch * 4u;
 
 constexpr int kF8MaxSlices = 8;
 constexpr int kF8PartPitch = 128 + 4;  // floats between the rows of a slice's sums in shared memory
