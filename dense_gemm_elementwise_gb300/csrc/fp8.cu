@@ -36,7 +36,8 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   pl->cg = M > 128 && ctas >= 2 && ceil_div(M, 256) * ceil_div(N, 256) > ctas / 4 ? 2 : 1;
   const int bm = 128 * pl->cg, bn = 128 * pl->cg, units = ctas / pl->cg;
   const bool square = pl->d.b_block == GE_BLOCK_SQUARE;
-  pl->fn = pl->cg == 2 ? fp8_kernel_cg2(square) : fp8_kernel_cg1(square);
+  const bool turned = pl->d.ldd * size_of(pl->d.d) % 16 != 0;
+  pl->fn = pl->cg == 2 ? fp8_kernel_cg2(square, turned) : fp8_kernel_cg1(square, turned);
   const int64_t num_m = ceil_div(M, bm), num_n = ceil_div(N, bn), tiles = num_m * num_n;
   p.num_kb = static_cast<int32_t>(ceil_div(pl->K, kF8Block));
   if (tiles > (int64_t(1) << 31) / kF8MaxSlices) return GE_ERR_SHAPE;
@@ -45,7 +46,6 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   p.raster_group = num_m <= 16 ? static_cast<int32_t>(num_m) : 12;
   p.a_rows = pl->cg == 1 ? static_cast<int32_t>(std::min<int64_t>(128, round_up(M, 8))) : 128;
   const int stage = 128 * 128 + 128 * bn / pl->cg;
-  const bool turned = pl->d.ldd * size_of(pl->d.d) % 16 != 0;
   const int fixed = 1024 + static_cast<int>(kF8BarBytes + fp8_scale_bytes(bn, square) + (turned ? kF8TurnBytes : 0u));
   p.stages = std::min(kMaxStages, (max_smem - fixed) / stage);
   if (p.stages < 2) return GE_ERR_SMEM;
@@ -177,7 +177,7 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
   p.d = D;
   // (bases are whole 16 bytes)
   const int64_t pitch = p.ldd * size_of(p.dt);
-  p.vec = pitch % 16 != 0 ? 0 : pitch % 32 != 0 || ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(D)) & 31u) != 0 ? 1 : 2;
+  p.vec = pitch % 32 != 0 || ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(D)) & 31u) != 0 ? 1 : 2;
   void *args[] = {&p};
   return launch_pdl(pl->fn, dim3(static_cast<unsigned>(pl->grid)), dim3(kF8Threads), pl->smem, args, static_cast<cudaStream_t>(stream),
                     pl->cluster) == cudaSuccess ? GE_OK : GE_ERR_CUDA;

@@ -20,7 +20,7 @@ struct Fp8Params {
   int32_t num_kb, num_m_blk, num_n_blk, raster_group;
   int32_t slices, kb_split;  // a tile's k-blocks are shared by the `slices` CTAs of a cluster, kb_split each
   int32_t stages;
-  int32_t a_e5m2, b_e5m2, dt, vec;  // vec: rows of C and D are whole units of 32 bytes (2), of 16 (1), or neither (0)
+  int32_t a_e5m2, b_e5m2, dt, vec;  // vec: rows of C and D are whole units of 32 bytes (2) or of 16 (1)
   int32_t a_rows;          // rows of an A tile that are loaded (one CTA)
   uint32_t debug_flags;
   uint32_t off_B, off_bar, off_turn;
@@ -46,8 +46,8 @@ constexpr uint32_t kF8TurnBytes = 8u * 32u * kF8TurnPitch * 4u;
 constexpr int kF8MaxSlices = 8;
 constexpr int kF8PartPitch = 128 + 4;  // floats between the rows of a slice's sums in shared memory
 
-// square: B's scales are one for each 128 columns
-const void *fp8_kernel_cg1(bool square);  // 128 x 128 tiles, one CTA
-const void *fp8_kernel_cg2(bool square);  // 256 x 256 tiles, a CTA pair
+// square: B's scales are one for each 128 columns; turned: rows of C and D are no whole 16 bytes
+const void *fp8_kernel_cg1(bool square, bool turned);  // 128 x 128 tiles, one CTA
+const void *fp8_kernel_cg2(bool square, bool turned);  // 256 x 256 tiles, a CTA pair
 
 }  // namespace ge

@@ -120,7 +120,7 @@ __device__ __forceinline__ void store_words(void *p, const uint32_t *w, bool wid
 __device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float (&v)[16]) {
   const int left = p.N - n;
   const int64_t at = int64_t(m) * p.ldd + n;
-  if (p.vec && left >= 16) {
+  if (left >= 16) {  // (rows are whole 16 bytes)
     if (p.dt == GE_F32) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -158,7 +158,8 @@ __device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float
     if (e < left) store_one(p.d, at + e, p.dt, v[e] + (p.c ? load_one(p.c, at + e, p.dt) : 0.f));
 }
 
-template <int CG, int BN, bool SQUARE>
+// TURN: rows of C and D are no whole 16 bytes
+template <int CG, int BN, bool SQUARE, bool TURN>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
   using T = TileCfg<CG, BN>;
   constexpr int kEpi0 = kF8Epi0;
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
         }
       }
       if (!ok) break;
-      if (!p.vec && !(CG == 1 && p.slices > 1)) {
+      if (TURN && !(CG == 1 && p.slices > 1)) {
         // Rows that start anywhere: 32 columns of 32 rows through shared memory, so that a warp writes a row's
         // columns together (4096 x 10473 x 393 bf16: 353 us when each thread wrote its own row)
         float *turn = reinterpret_cast<float *>(smem + p.off_turn) + (warp - kEpi0) * 32 * kF8TurnPitch;
@@ -541,10 +542,10 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
   }
 }
 
-template <int CG, int BN>
-const void *pick_fp8(bool square) {
-  return square ? reinterpret_cast<const void *>(fp8_kernel<CG, BN, true>)
-                : reinterpret_cast<const void *>(fp8_kernel<CG, BN, false>);
+template <int CG, int BN, bool SQUARE>
+const void *pick_fp8(bool turned) {
+  return turned ? reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, true>)
+                : reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, false>);
 }
 
 }  // namespace ge

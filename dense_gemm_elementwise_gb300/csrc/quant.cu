@@ -326,6 +326,7 @@ int gemm_epi_quant_run(gemm_epi_quant_plan *pl, const void *x, void *q, float *s
                        void *stream) {
   if (!pl) return GE_ERR_INVALID;
   if (!x || (!q && !qt) || (!q) != (!scale) || (!qt) != (!scale_t)) return GE_ERR_MISSING_ARG;
+  if ((q && q == qt) || (scale && scale == scale_t)) return GE_ERR_INVALID;
   for (const void *a : {x, static_cast<const void *>(q), static_cast<const void *>(scale),
                         static_cast<const void *>(qt), static_cast<const void *>(scale_t)})
     if (!is_aligned16(a)) return GE_ERR_MISALIGNED;

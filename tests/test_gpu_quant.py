@@ -237,6 +237,8 @@ def test_run_refusals():
     assert run(c.x, None, None, None, None) == B.GE_ERR_MISSING_ARG
     assert run(c.x, c.q, None, None, None) == B.GE_ERR_MISSING_ARG
     assert run(c.x, c.q, c.scale, c.qt, None) == B.GE_ERR_MISSING_ARG
+    assert run(c.x, c.q, c.scale, c.q, c.scale_t) == B.GE_ERR_INVALID
+    assert run(c.x, c.q, c.scale, c.qt, c.scale) == B.GE_ERR_INVALID
     assert run(c.x.data_ptr() + 2, c.q, c.scale, None, None) == B.GE_ERR_MISALIGNED
     assert run(c.x, c.q.data_ptr() + 8, c.scale, None, None) == B.GE_ERR_MISALIGNED
     # a default pitch that is no whole 16 bytes, of the output that is asked for
