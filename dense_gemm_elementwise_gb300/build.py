@@ -20,7 +20,7 @@ LIB = os.path.join(LIBDIR, "libgemm_epi.so")
 UNITS = ["plan", "unfused", "jit", "k_cg1_n64", "k_cg1_n128", "k_cg1_n256", "k_cg2_n128", "k_cg2_n256",
          "norm", "k_norm_run", "k_norm_grad", "k_norm_grad_whole",
          "k_norm_run_small", "k_norm_grad_small", "k_norm_grad_whole_small", "k_norm_run_odd", "k_norm_grad_odd",
-         "k_norm_grad_whole_odd", "xent", "k_xent_cg1", "k_xent_cg2", "quant", "fp8", "k_fp8_cg1", "k_fp8_cg2", "moe", "k_moe_16", "k_moe_e4m3", "k_moe_e5m2"]
+         "k_norm_grad_whole_odd", "xent", "k_xent_cg1", "k_xent_cg2", "quant", "fp8", "k_fp8_cg1", "k_fp8_cg2", "fp8_few", "moe", "k_moe_16", "k_moe_e4m3", "k_moe_e5m2"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -25,6 +25,7 @@ struct gemm_epi_fp8_plan {
   int sms = 0, cg = 1, cluster = 1, grid = 1, smem = 0;
   const void *fn = nullptr;
   Fp8Params p{};
+  bool few = false;  // fp8_few.cu's kernel
 };
 
 namespace {
@@ -32,14 +33,33 @@ namespace {
 int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   Fp8Params &p = pl->p;
   const int64_t M = pl->M, N = pl->N;
+  // Up to 16 rows of A have a kernel of their own (from memory, us: 8 x 2048 x 7168 5.3, the other one 9.4; 8 x 40000 x 4096 29.5
+  // and 41.1; 16 x 2048 x 7168 6.2 and 9.6).  It wants blocks for its warps where there are many columns (1 x 100000 x 256 16.3 and
+  // 14.1, x 512 16.7 and 17.3, but 1 x 20000 x 256 4.5 and 5.7), and with more than 8 rows its arithmetic shows
+  // (16 x 100000 x 512 23.2 and 17.6, 12 x 16384 x 8192 33.0 and 27.0, but 16 x 8192 x 4096 10.7 and 11.6).
+  // (What tests that a load which never comes is reported is the other kernel's: here nothing waits for another.)
+  p.num_kb = static_cast<int32_t>(ceil_div(pl->K, kF8Block));
+  const int64_t units = ceil_div(N, kF8FewUnit), slots = int64_t(pl->sms) * kF8FewPerSm;
+  pl->few = M <= kF8FewRows && p.debug_flags == 0 &&
+            (M <= 8 ? units <= 8 * slots || p.num_kb >= 4 : units <= 8 * slots && N * pl->K <= int64_t(1) << 26);
+  if (pl->few) {
+    const Fp8Few few = fp8_few(p.a_e5m2 != 0, p.b_e5m2 != 0, static_cast<int>(M));
+    pl->fn = few.fn;
+    pl->smem = few.smem;
+    if (cudaFuncSetAttribute(pl->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl->smem) != cudaSuccess) {
+      cudaGetLastError();
+      return GE_ERR_CUDA;
+    }
+    pl->grid = static_cast<int>(std::min<int64_t>(units, pl->d.max_ctas > 0 ? pl->d.max_ctas : slots));
+    return GE_OK;
+  }
   const int ctas = pl->d.max_ctas > 0 ? std::min(pl->d.max_ctas, pl->sms) : pl->sms;
   pl->cg = M > 128 && ctas >= 2 && ceil_div(M, 256) * ceil_div(N, 256) > ctas / 4 ? 2 : 1;
-  const int bm = 128 * pl->cg, bn = 128 * pl->cg, units = ctas / pl->cg;
+  const int bm = 128 * pl->cg, bn = 128 * pl->cg, groups = ctas / pl->cg;
   const bool square = pl->d.b_block == GE_BLOCK_SQUARE;
   const bool turned = pl->d.ldd * size_of(pl->d.d) % 16 != 0;
   pl->fn = pl->cg == 2 ? fp8_kernel_cg2(square, turned) : fp8_kernel_cg1(square, turned);
   const int64_t num_m = ceil_div(M, bm), num_n = ceil_div(N, bn), tiles = num_m * num_n;
-  p.num_kb = static_cast<int32_t>(ceil_div(pl->K, kF8Block));
   if (tiles > (int64_t(1) << 31) / kF8MaxSlices) return GE_ERR_SHAPE;
   p.num_m_blk = static_cast<int32_t>(num_m);
   p.num_n_blk = static_cast<int32_t>(num_n);
@@ -67,7 +87,7 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   // Too few tiles for the GPU: their sums are split among the CTAs of clusters, all of which have to be there at once.
   // A slice more has to save a k-block (of about 0.3 us) for each slice: what it costs to join them.
   int slices = 1;
-  for (int s = 2; pl->cg == 1 && s <= kF8MaxSlices && s <= p.num_kb && tiles * s <= units; ++s) {
+  for (int s = 2; pl->cg == 1 && s <= kF8MaxSlices && s <= p.num_kb && tiles * s <= groups; ++s) {
     if (ceil_div(p.num_kb, s) + s > ceil_div(p.num_kb, slices) + slices) continue;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -89,7 +109,7 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   p.slices = slices;
   p.kb_split = static_cast<int32_t>(ceil_div(p.num_kb, slices));
   pl->cluster = pl->cg == 2 ? 2 : slices;
-  pl->grid = static_cast<int>(std::min<int64_t>(units, tiles * slices)) * pl->cg;
+  pl->grid = static_cast<int>(std::min<int64_t>(groups, tiles * slices)) * pl->cg;
   return GE_OK;
 }
 
@@ -168,13 +188,21 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
   if (!is_aligned16(workspace)) return GE_ERR_MISALIGNED;
   if (workspace_bytes < gemm_epi_fp8_workspace_bytes(pl)) return GE_ERR_WORKSPACE;
   Fp8Params p = pl->p;
-  if (!encode_rows(&p.tmA, GE_E4M3, A, pl->K, pl->M, 1, pl->d.lda, pl->d.lda * pl->M, kF8Block, p.a_rows) ||
-      !encode_rows(&p.tmB, GE_E4M3, B, pl->K, pl->N, 1, pl->d.ldb, pl->d.ldb * pl->N, kF8Block, 128))
-    return GE_ERR_CUDA;
   p.sa = scale_a;
   p.sb = scale_b;
   p.c = C;
   p.d = D;
+  if (pl->few) {
+    int32_t K = static_cast<int32_t>(pl->K);
+    bool square = pl->d.b_block == GE_BLOCK_SQUARE;
+    void *args[] = {&p, &A, &B, &pl->d.lda, &pl->d.ldb, &K, &square};
+    return launch_pdl(pl->fn, dim3(static_cast<unsigned>(pl->grid)), dim3(kF8FewThreads), pl->smem, args, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GE_OK
+               : GE_ERR_CUDA;
+  }
+  if (!encode_rows(&p.tmA, GE_E4M3, A, pl->K, pl->M, 1, pl->d.lda, pl->d.lda * pl->M, kF8Block, p.a_rows) ||
+      !encode_rows(&p.tmB, GE_E4M3, B, pl->K, pl->N, 1, pl->d.ldb, pl->d.ldb * pl->N, kF8Block, 128))
+    return GE_ERR_CUDA;
   // (bases are whole 16 bytes)
   const int64_t pitch = p.ldd * size_of(p.dt);
   p.vec = pitch % 32 != 0 || ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(D)) & 31u) != 0 ? 1 : 2;

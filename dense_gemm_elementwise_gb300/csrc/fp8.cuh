@@ -1,7 +1,10 @@
 // fp8.cuh -- parameters and handles of the block-scaled 8-bit products.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
+#include "xent_math.cuh"
 
 namespace ge {
 
@@ -49,5 +52,28 @@ constexpr int kF8PartPitch = 128 + 4;  // floats between the rows of a slice's s
 // square: B's scales are one for each 128 columns; turned: rows of C and D are no whole 16 bytes
 const void *fp8_kernel_cg1(bool square, bool turned);  // 128 x 128 tiles, one CTA
 const void *fp8_kernel_cg2(bool square, bool turned);  // 256 x 256 tiles, a CTA pair
+
+
+// few rows of A (fp8_few.cu)
+constexpr int kF8FewRows = 16, kF8FewUnit = 16;  // rows of A at most, rows of B that a CTA takes at a time
+constexpr int kF8FewThreads = 256, kF8FewPerSm = 2;
+struct Fp8Few {
+  const void *fn;
+  int smem;
+};
+Fp8Few fp8_few(bool a_e5m2, bool b_e5m2, int M);
+
+#ifdef __CUDACC__
+__device__ __forceinline__ float load_one(const void *p, int64_t at, int dt) {
+  if (dt == GE_F32) return static_cast<const float *>(p)[at];
+  const uint16_t v = static_cast<const uint16_t *>(p)[at];
+  return dt == GE_BF16 ? __uint_as_float(uint32_t(v) << 16) : __half2float(__ushort_as_half(v));
+}
+
+__device__ __forceinline__ void store_one(void *p, int64_t at, int dt, float v) {
+  if (dt == GE_F32) static_cast<float *>(p)[at] = v;
+  else static_cast<uint16_t *>(p)[at] = static_cast<uint16_t>(pack16(dt == GE_BF16, v, 0.f));
+}
+#endif
 
 }  // namespace ge

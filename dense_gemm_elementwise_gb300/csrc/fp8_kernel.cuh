@@ -80,17 +80,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
-__device__ __forceinline__ float load_one(const void *p, int64_t at, int dt) {
-  if (dt == GE_F32) return static_cast<const float *>(p)[at];
-  const uint16_t v = static_cast<const uint16_t *>(p)[at];
-  return dt == GE_BF16 ? __uint_as_float(uint32_t(v) << 16) : __half2float(__ushort_as_half(v));
-}
-
-__device__ __forceinline__ void store_one(void *p, int64_t at, int dt, float v) {
-  if (dt == GE_F32) static_cast<float *>(p)[at] = v;
-  else static_cast<uint16_t *>(p)[at] = static_cast<uint16_t>(pack16(dt == GE_BF16, v, 0.f));
-}
-
 // 8 words of a row, 32 bytes or twice 16 at a time
 __device__ __forceinline__ void load_words(const void *p, uint32_t (&w)[8], bool wide) {
   if (wide) {

@@ -640,7 +640,7 @@ typedef struct {
   int32_t d;            /* GE_F16, GE_BF16 or GE_F32: C and D                                 */
   int32_t b_block;      /* ge_block of B's scales                                             */
   int32_t timeout_ms;   /* 0 = 1000; bound on every device-side wait                          */
-  int32_t max_ctas;     /* 0 = one CTA per SM, else a cap on the product's grid               */
+  int32_t max_ctas;     /* 0 = as many as the SMs hold, else a cap on the product's grid      */
   uint32_t debug_flags; /* 0; GE_DEBUG_SKIP_FIRST_LOAD for tests only                         */
   int32_t reserved;     /* 0                                                                  */
   int64_t lda, ldb;     /* row pitches in bytes, multiples of 16; 0 = K                       */

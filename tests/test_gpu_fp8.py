@@ -151,6 +151,14 @@ def test_sum_in_place(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 2, 3, 7, 8, 9, 13, 16])
+@pytest.mark.parametrize("N,K,ctas", [(6, 2, 0), (40, 100, 0), (129, 128, 0), (300, 2100, 2), (900, 1160, 3), (5500, 1024, 0), (9800, 390, 0), (80000, 130, 0)])
+@pytest.mark.parametrize("block", ["square", "row"])
+def test_few_rows(M, N, K, ctas, block):
+    Case(M, N, K, block=block, max_ctas=ctas, more_scales=1, seed=5).run().check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("ctas", [1, 2, 3, 7, 20])
 @pytest.mark.parametrize("block", ["square", "row"])
 def test_many_tiles_for_a_cta(ctas, block):
