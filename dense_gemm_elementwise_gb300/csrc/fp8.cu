@@ -23,7 +23,7 @@ struct gemm_epi_fp8_plan {
   int64_t M = 0, N = 0, K = 0;
   ge_fp8_desc d{};
   int sms = 0, cg = 1, cluster = 1, grid = 1, smem = 0;
-  const void *fn = nullptr;
+  const void *fn = nullptr, *fn_add = nullptr;  // without and with C
   Fp8Params p{};
   bool few = false;  // fp8_few.cu's kernel
 };
@@ -44,7 +44,7 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
             (M <= 8 ? units <= 8 * slots || p.num_kb >= 4 : units <= 8 * slots && N * pl->K <= int64_t(1) << 26);
   if (pl->few) {
     const Fp8Few few = fp8_few(p.a_e5m2 != 0, p.b_e5m2 != 0, static_cast<int>(M));
-    pl->fn = few.fn;
+    pl->fn = pl->fn_add = few.fn;
     pl->smem = few.smem;
     if (cudaFuncSetAttribute(pl->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, pl->smem) != cudaSuccess) {
       cudaGetLastError();
@@ -58,7 +58,9 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   const int bm = 128 * pl->cg, bn = 128 * pl->cg, groups = ctas / pl->cg;
   const bool square = pl->d.b_block == GE_BLOCK_SQUARE;
   const bool turned = pl->d.ldd * size_of(pl->d.d) % 16 != 0;
-  pl->fn = pl->cg == 2 ? fp8_kernel_cg2(square, turned) : fp8_kernel_cg1(square, turned);
+  const auto pick = pl->cg == 2 ? fp8_kernel_cg2 : fp8_kernel_cg1;
+  pl->fn = pick(square, false, turned);
+  pl->fn_add = pick(square, true, turned);
   const int64_t num_m = ceil_div(M, bm), num_n = ceil_div(N, bn), tiles = num_m * num_n;
   if (tiles > (int64_t(1) << 31) / kF8MaxSlices) return GE_ERR_SHAPE;
   p.num_m_blk = static_cast<int32_t>(num_m);
@@ -73,16 +75,15 @@ int configure(gemm_epi_fp8_plan *pl, int max_smem) {
   p.off_bar = static_cast<uint32_t>(p.stages * stage);
   p.off_turn = p.off_bar + kF8BarBytes + fp8_scale_bytes(bn, square);
   // the kernel's warps pass registers on, which have to be there
-  cudaFuncAttributes fa;
-  if (cudaFuncGetAttributes(&fa, pl->fn) != cudaSuccess || fa.numRegs < kF8Regs) {
-    cudaGetLastError();
-    return GE_ERR_CUDA;
-  }
-  // all of an SM's shared memory, so that its TMEM is this CTA's alone
   pl->smem = max_smem;
-  if (cudaFuncSetAttribute(pl->fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess) {
-    cudaGetLastError();
-    return GE_ERR_CUDA;
+  for (const void *fn : {pl->fn, pl->fn_add}) {
+    cudaFuncAttributes fa;
+    // (all of an SM's shared memory, so that its TMEM is this CTA's alone)
+    if (cudaFuncGetAttributes(&fa, fn) != cudaSuccess || fa.numRegs < kF8Regs ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem) != cudaSuccess) {
+      cudaGetLastError();
+      return GE_ERR_CUDA;
+    }
   }
   // Too few tiles for the GPU: their sums are split among the CTAs of clusters, all of which have to be there at once.
   // A slice more has to save a k-block (of about 0.3 us) for each slice: what it costs to join them.
@@ -207,7 +208,7 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *pl, const void *A, const float *scale_a,
   const int64_t pitch = p.ldd * size_of(p.dt);
   p.vec = pitch % 32 != 0 || ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(D)) & 31u) != 0 ? 1 : 2;
   void *args[] = {&p};
-  return launch_pdl(pl->fn, dim3(static_cast<unsigned>(pl->grid)), dim3(kF8Threads), pl->smem, args, static_cast<cudaStream_t>(stream),
+  return launch_pdl(C ? pl->fn_add : pl->fn, dim3(static_cast<unsigned>(pl->grid)), dim3(kF8Threads), pl->smem, args, static_cast<cudaStream_t>(stream),
                     pl->cluster) == cudaSuccess ? GE_OK : GE_ERR_CUDA;
 }
 

@@ -49,9 +49,9 @@ constexpr uint32_t kF8TurnBytes = 8u * 32u * kF8TurnPitch * 4u;
 constexpr int kF8MaxSlices = 8;
 constexpr int kF8PartPitch = 128 + 4;  // floats between the rows of a slice's sums in shared memory
 
-// square: B's scales are one for each 128 columns; turned: rows of C and D are no whole 16 bytes
-const void *fp8_kernel_cg1(bool square, bool turned);  // 128 x 128 tiles, one CTA
-const void *fp8_kernel_cg2(bool square, bool turned);  // 256 x 256 tiles, a CTA pair
+// square: B's scales are one for each 128 columns; add: there is a C; turned: rows of C and D are no whole 16 bytes
+const void *fp8_kernel_cg1(bool square, bool add, bool turned);  // 128 x 128 tiles, one CTA
+const void *fp8_kernel_cg2(bool square, bool add, bool turned);  // 256 x 256 tiles, a CTA pair
 
 
 // few rows of A (fp8_few.cu)

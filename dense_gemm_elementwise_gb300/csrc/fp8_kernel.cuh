@@ -22,7 +22,7 @@
 //     took 490 us and more: A is then read twice from shared memory.)
 //   * Scales come through shared memory, some k-blocks at a time: loaded by the epilogue itself, a
 //     k-block ahead, they came too late (with constants in their place it took 30 us less).
-//   * 32 columns are on their way to an epilogue thread while it adds 32 others, which its registers
+//   * 32 columns (16) are on their way to an epilogue thread while it adds as many others, which its registers
 //     have room for because the other warps give theirs away.  (Sixteen epilogue warps took 530 us.)
 //
 // Few tiles (128 x 128, single CTAs) share their sums over K with the other CTAs of a cluster, which leave them in
@@ -105,8 +105,38 @@ __device__ __forceinline__ void store_words(void *p, const uint32_t *w, bool wid
   }
 }
 
-// 16 sums of a row, C added, into D
-__device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float (&v)[16]) {
+// C's 64 columns from `at` on added to as many sums: asked for together, since D may be C and no load passes a store
+__device__ __forceinline__ void add64(const Fp8Params &p, int64_t at, float2 *sums) {
+  if (p.dt == GE_F32) {
+    uint32_t w[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) load_words(static_cast<const float *>(p.c) + at + 8 * i, w[i], p.vec == 2);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        sums[4 * i + e].x += __uint_as_float(w[i][2 * e]);
+        sums[4 * i + e].y += __uint_as_float(w[i][2 * e + 1]);
+      }
+  } else {
+    const bool bf16 = p.dt == GE_BF16;
+    uint32_t w[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_words(static_cast<const uint16_t *>(p.c) + at + 16 * i, w[i], p.vec == 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 c = bf16 ? make_float2(__uint_as_float(w[i][e] << 16), __uint_as_float(w[i][e] & 0xffff0000u))
+                              : __half22float2(*reinterpret_cast<const __half2 *>(&w[i][e]));
+        sums[8 * i + e].x += c.x;
+        sums[8 * i + e].y += c.y;
+      }
+  }
+}
+
+// 16 sums of a row, C added where `add`, into D
+__device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float (&v)[16], bool add) {
   const int left = p.N - n;
   const int64_t at = int64_t(m) * p.ldd + n;
   if (left >= 16) {  // (rows are whole 16 bytes)
@@ -114,7 +144,7 @@ __device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[8];
-        if (p.c) {
+        if (add) {
           load_words(static_cast<const float *>(p.c) + at + 8 * h, w, p.vec == 2);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[8 * h + e] += __uint_as_float(w[e]);
@@ -126,7 +156,7 @@ __device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float
     } else {
       const bool bf16 = p.dt == GE_BF16;
       uint32_t w[8];
-      if (p.c) {
+      if (add) {
         load_words(static_cast<const uint16_t *>(p.c) + at, w, p.vec == 2);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -144,11 +174,14 @@ __device__ __forceinline__ void finish16(const Fp8Params &p, int m, int n, float
   }
 #pragma unroll
   for (int e = 0; e < 16; ++e)
-    if (e < left) store_one(p.d, at + e, p.dt, v[e] + (p.c ? load_one(p.c, at + e, p.dt) : 0.f));
+    if (e < left) store_one(p.d, at + e, p.dt, v[e] + (add ? load_one(p.c, at + e, p.dt) : 0.f));
 }
 
-// TURN: rows of C and D are no whole 16 bytes
-template <int CG, int BN, bool SQUARE, bool TURN>
+// How D is written: rows of whole 16 bytes without C, the same with C (a kernel of its own: the loads' registers took 2 % of the
+// other's time), or rows that start anywhere
+enum Fp8Out { kF8Plain, kF8Add, kF8Turn };
+
+template <int CG, int BN, bool SQUARE, Fp8Out OUT>
 __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constant__ Fp8Params p) {
   using T = TileCfg<CG, BN>;
   constexpr int kEpi0 = kF8Epi0;
@@ -323,6 +356,8 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
     bool ok = true;
     for (int at = unit; ok && at < num_units; at += n_units) {
       const Tile t = tile(at);
+      const int es = p.dt == GE_F32 ? 4 : 2, lines = BN * es / 128;  // C's lines of a row
+      int asked = OUT == kF8Add ? lane : BM * lines;
       for (int kb0 = t.kb0; kb0 < t.kb1; kb0 += kBatch) {
         // all of a batch's loads are under way before one is waited for
         float a[kBatch][4], b[SQUARE ? 1 : kBatch][SQUARE ? 1 : kSb / 32];
@@ -365,6 +400,13 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
         if (lane == 0) mbar_arrive(bar + kFScaleFull + 8 * slot);
         slot ^= 1;
         if (slot == 0) phase ^= 1u;
+        // some of C on its way to the L2 (all at once, the next scales came late)
+#pragma unroll 1
+        for (int i = 0; i < kBatch && asked < BM * lines; ++i, asked += 32) {
+          const int m = t.m0 + asked / lines, n = t.n0 + asked % lines * (128 / es);
+          if (m < p.M && n < p.N)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char *>(p.c) + (int64_t(m) * p.ldd + n) * es));
+        }
       }
     }
   }
@@ -400,33 +442,54 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
         if (!ok) break;
         tc_fence_after();
         const uint32_t src = tq + static_cast<uint32_t>(abuf * BN);
-        // 32 columns are on their way while the 32 before them are added
-        float v[2][32];
-        tmem_ld32(src, v[0]);
+        auto back = [&]() {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            const uint32_t tb = bar + kFTmemEmpty + 8 * abuf;
+            if constexpr (CG == 2) mbar_arrive_remote_relaxed(mapa_shared(tb, 0));
+            else mbar_arrive(tb);
+          }
+        };
+        if constexpr (!SQUARE) {
+          // 16 columns at a time leave registers for the next ones' scales, which then are there when their sums are (32 columns
+          // without them: 4096 x 2048 x 6016 into fp32 69.2 us, here 67.9)
+          float v[2][16];
+          float4 b[2][4];
+          tmem_ld16(src, v[0]);
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) {
-          tmem_wait_ld();
-          if (c + 1 < kCols / 32) {
-            tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              const uint32_t tb = bar + kFTmemEmpty + 8 * abuf;
-              if constexpr (CG == 2) mbar_arrive_remote_relaxed(mapa_shared(tb, 0));
-              else mbar_arrive(tb);
+          for (int e = 0; e < 4; ++e) b[0][e] = *reinterpret_cast<const float4 *>(sb_now + 4 * e);
+#pragma unroll
+          for (int c = 0; c < kCols / 16; ++c) {
+            tmem_wait_ld();
+            if (c + 1 < kCols / 16) {
+              tmem_ld16(src + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) b[(c + 1) & 1][e] = *reinterpret_cast<const float4 *>(sb_now + 16 * (c + 1) + 4 * e);
+            } else {
+              back();
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float4 w = b[c & 1][e];
+              const float2 x = mul2(make_float2(v[c & 1][4 * e], v[c & 1][4 * e + 1]), make_float2(w.x, w.y));
+              const float2 y = mul2(make_float2(v[c & 1][4 * e + 2], v[c & 1][4 * e + 3]), make_float2(w.z, w.w));
+              acc[8 * c + 2 * e] = fma2(x, s2, acc[8 * c + 2 * e]);
+              acc[8 * c + 2 * e + 1] = fma2(y, s2, acc[8 * c + 2 * e + 1]);
             }
           }
+        } else {
+          // 32 columns are on their way while the 32 before them are added
+          float v[2][32];
+          tmem_ld32(src, v[0]);
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 x = make_float2(v[c & 1][2 * e], v[c & 1][2 * e + 1]), y = make_float2(v[c & 1][2 * e + 2], v[c & 1][2 * e + 3]);
-            if constexpr (!SQUARE) {
-              const float4 b = *reinterpret_cast<const float4 *>(sb_now + 32 * c + 2 * e);
-              x = mul2(x, make_float2(b.x, b.y));
-              y = mul2(y, make_float2(b.z, b.w));
-            }
-            acc[16 * c + e] = fma2(x, s2, acc[16 * c + e]);
-            acc[16 * c + e + 1] = fma2(y, s2, acc[16 * c + e + 1]);
+          for (int c = 0; c < kCols / 32; ++c) {
+            tmem_wait_ld();
+            if (c + 1 < kCols / 32) tmem_ld32(src + 32 * (c + 1), v[(c + 1) & 1]);
+            else back();
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              acc[16 * c + e] = fma2(make_float2(v[c & 1][2 * e], v[c & 1][2 * e + 1]), s2, acc[16 * c + e]);
           }
         }
         abuf ^= 1;
@@ -443,7 +506,7 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
         }
       }
       if (!ok) break;
-      if (TURN && !(CG == 1 && p.slices > 1)) {
+      if (OUT == kF8Turn && !(CG == 1 && p.slices > 1)) {
         // Rows that start anywhere: 32 columns of 32 rows through shared memory, so that a warp writes a row's
         // columns together (4096 x 10473 x 393 bf16: 353 us when each thread wrote its own row)
         float *turn = reinterpret_cast<float *>(smem + p.off_turn) + (warp - kEpi0) * 32 * kF8TurnPitch;
@@ -480,13 +543,15 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
       for (int c = 0; c < kCols / 16; ++c) {
         const int n = n0 + 16 * c;
         if (n >= p.N) break;
+        const bool whole = n0 + c / 4 * 64 + 64 <= p.N;
+        if (OUT == kF8Add && c % 4 == 0 && whole) add64(p, int64_t(m) * p.ldd + n, acc + 8 * c);
         float v[16];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           v[2 * e] = acc[8 * c + e].x;
           v[2 * e + 1] = acc[8 * c + e].y;
         }
-        finish16(p, m, n, v);
+        finish16(p, m, n, v, OUT == kF8Add && !whole);
       }
     }
     __syncwarp();
@@ -532,9 +597,10 @@ __global__ void __launch_bounds__(kF8Threads, 1) fp8_kernel(const __grid_constan
 }
 
 template <int CG, int BN, bool SQUARE>
-const void *pick_fp8(bool turned) {
-  return turned ? reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, true>)
-                : reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, false>);
+const void *pick_fp8(bool add, bool turned) {
+  return turned ? reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, kF8Turn>)
+         : add  ? reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, kF8Add>)
+                : reinterpret_cast<const void *>(fp8_kernel<CG, BN, SQUARE, kF8Plain>);
 }
 
 }  // namespace ge

@@ -151,6 +151,14 @@ def test_sum_in_place(M, N, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(600, 4992, 400), (590, 5000, 130), (1300, 2100, 2100), (130, 700, 150)])
+@pytest.mark.parametrize("d", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("block", ["square", "row"])
+def test_large_sums_added(M, N, K, d, block):
+    Case(M, N, K, d=d, block=block, add=True, pad=(0, 0, 8), seed=9).run().check()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M", [1, 2, 3, 7, 8, 9, 13, 16])
 @pytest.mark.parametrize("N,K,ctas", [(6, 2, 0), (40, 100, 0), (129, 128, 0), (300, 2100, 2), (900, 1160, 3), (5500, 1024, 0), (9800, 390, 0), (80000, 130, 0)])
 @pytest.mark.parametrize("block", ["square", "row"])
