@@ -30,6 +30,8 @@ struct MoeParams {
   uint32_t *done;   // units of the first kind, by expert
   uint32_t *shares;  // experts' shares of 16 columns of y
   float2 *logits;   // (T, E)
+  uint16_t *expert;  // the choice (T, k), where it has a kernel of its own, and
+  float *share;      // ... its weights
   uint16_t *h;      // (T k, F) twice: values, and what their rounding left
   float *part;      // (T k, D)
   uint32_t *status;

@@ -1,10 +1,11 @@
-// moe_kernel.cuh -- a mixture-of-experts layer for a few tokens (gemm_epi_moe_*), in two launches: the
-// experts' kernel; the router's is in moe.cu.
+// moe_kernel.cuh -- a mixture-of-experts layer for a few tokens (gemm_epi_moe_*): the experts' kernel; the
+// router's, and where it has one the choice's, are in moe.cu.
 //
 //   router   l = x w_router^T, in pairs of fp32 (TwoSum): the choice of experts has to be that
 //            of exact logits, or a token's output is another's
-//   experts  every CTA chooses the experts from the logits (cheaper than a third launch or
-//            a grid-wide wait), then takes units of work by ticket:
+//   choice   of a token's experts, by a warp.  Where a CTA has a warp for each token, every CTA of the experts'
+//            kernel chooses for itself (cheaper than a third launch or a grid-wide wait)
+//   experts  CTAs take units of work by ticket:
 //              1. 16 columns of h = act(gate) * up of one expert: 16 gate and 16 up rows against
 //                 the tokens that chose it, up to 32 (more are another unit)
 //              2. 32 columns of y's share of one expert: 32 rows of w_down against its h,
@@ -34,6 +35,7 @@
 #include <type_traits>
 
 #include "moe.h"
+#include "moe_choice.cuh"
 #include "ptx.cuh"
 #include "xent_math.cuh"
 
@@ -55,7 +57,8 @@ constexpr int kSegment = 1024;     // bytes of a row in a stage
 constexpr int kPitch = kSegment + 64;  // lanes of two rows touch different banks
 constexpr int kStages = 5;
 constexpr int kQueue = 8;          // units under way in a CTA
-// -------------------------------------------------------------- the choice --
+
+// --------------------------------------------------------------- the lists --
 
 struct Choice {
   uint16_t expert[kPairs];
@@ -69,178 +72,6 @@ struct Choice {
   int32_t n_active;
   int32_t counter[GE_MOE_MAX_EXPERTS];
 };
-
-// floats as integers in the same order
-__device__ __forceinline__ int ordered(float f) {
-  const int b = __float_as_int(f);
-  return b ^ ((b >> 31) & 0x7fffffff);
-}
-
-// What an expert is chosen by, two floats, as integers of the same order; an upper one of 0 is below all.
-__device__ __forceinline__ uint32_t key_of(float f) { return static_cast<uint32_t>(ordered(f + 0.f)) ^ 0x80000000u; }  // (-0 is 0)
-__device__ __forceinline__ float of_key(uint32_t k) { return __int_as_float(ordered(__int_as_float(static_cast<int>(k ^ 0x80000000u)))); }
-
-__device__ __forceinline__ float sigmoid(float2 v) {  // v.y: what the rounding of the argument left
-  const float e = expf(-fabsf(v.x)) * (v.x < 0.f ? 1.f + v.y : 1.f - v.y);
-  return (v.x < 0.f ? e : 1.f) / (1.f + e);
-}
-
-struct ChoiceSpace {  // a warp's
-  float2 logits[GE_MOE_MAX_EXPERTS];
-  alignas(16) uint32_t upper[GE_MOE_MAX_EXPERTS];
-  uint32_t lower[GE_MOE_MAX_EXPERTS];
-  uint32_t best[32];   // upper keys of the chosen
-  int32_t which[32];
-  __device__ __forceinline__ void put(int e, float hi, float lo) {  // a NaN counts as -infinity
-    upper[e] = key_of(hi == hi ? hi : -INFINITY);
-    lower[e] = key_of(isfinite(hi) ? lo : 0.f);
-  }
-};
-
-// The `some` best of up to 32 N experts, by how many are above each: a single warp's time is what it issues one after
-// another, and these comparisons do not wait for each other.  (For more than 64 experts they are too many: 64 tokens'
-// choice among 128 took 44 us instead of 27.)  Upper keys alone: false where two of the best are equal.
-template <int N>
-__device__ __forceinline__ bool rank(int E, int some, ChoiceSpace &s) {
-  const int lane = threadIdx.x & 31;
-  uint32_t mine[N];
-  int above[N] = {};
-#pragma unroll
-  for (int i = 0; i < N; ++i) mine[i] = i * 32 + lane < E ? s.upper[i * 32 + lane] : 0;
-  for (int e = E + lane; e < (E + 3) / 4 * 4; e += 32) s.upper[e] = 0;
-  __syncwarp();
-#pragma unroll 2
-  for (int e = 0; e < E; e += 4) {
-    const uint4 o = *reinterpret_cast<const uint4 *>(&s.upper[e]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) above[i] += (o.x > mine[i]) + (o.y > mine[i]) + (o.z > mine[i]) + (o.w > mine[i]);
-  }
-  uint32_t places = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (mine[i] != 0 && above[i] < some) {
-      s.best[above[i]] = mine[i];
-      s.which[above[i]] = i * 32 + lane;
-      places |= 1u << above[i];
-    }
-  return __reduce_or_sync(0xffffffffu, places) == (1u << some) - 1u;
-}
-
-// The `some` best experts in order, of equal keys the lower index first; whether two neighbours' upper keys are close.
-__device__ __forceinline__ bool find_best(int E, int some, ChoiceSpace &s) {
-  const int lane = threadIdx.x & 31;
-  const bool ranked = E <= 32 ? rank<1>(E, some, s) : E <= 64 ? rank<2>(E, some, s) : false;
-  if (!ranked) {
-    uint32_t hi, lo;  // this lane's best, found again when it has been taken
-    int at;
-    auto look = [&]() {
-      hi = lo = 0;
-      at = E;
-#pragma unroll 4
-      for (int e = lane; e < E; e += 32) {
-        const uint32_t h = s.upper[e], w = s.lower[e];
-        if (h > hi || (h == hi && h != 0 && w > lo)) hi = h, lo = w, at = e;
-      }
-    };
-    look();
-#pragma unroll 1
-    for (int j = 0; j < some; ++j) {
-      const uint32_t most = __reduce_max_sync(0xffffffffu, hi), rest = __reduce_max_sync(0xffffffffu, hi == most ? lo : 0u);
-      const int e = __reduce_min_sync(0xffffffffu, hi == most && lo == rest ? at : E);
-      if (at == e) {
-        s.best[j] = most;
-        s.which[j] = e;
-        s.upper[e] = 0;
-        look();
-      }
-      __syncwarp();
-    }
-  }
-  __syncwarp();
-  const float now = lane < some ? of_key(s.best[lane]) : 0.f;
-  const float next = __shfl_down_sync(0xffffffffu, now, 1);
-  return __any_sync(0xffffffffu, lane + 1 < some && now - next <= 2e-6f * fmaxf(1.f, fabsf(now)));
-}
-
-// One warp, one token: the k best experts and their weights.  This runs once in every CTA, so its code is short.
-// (Unrolled over keys in registers it took 8 us for one token and 124 us for 64 with 128 experts.)
-__device__ __noinline__ void choose(const MoeParams &p, int t, Choice &c, ChoiceSpace &s, bool say) {
-  const int lane = threadIdx.x & 31;
-  const bool softmax = p.score == GE_SCORE_SOFTMAX;
-  const float2 *l = s.logits;
-  float top = -INFINITY;
-#pragma unroll 4
-  for (int e = lane; e < p.E; e += 32) {
-    const float2 v = __ldcg(p.logits + int64_t(t) * p.E + e);
-    s.logits[e] = v;
-    if (!p.bias) s.put(e, v.x, v.y);
-    top = fmaxf(top, v.x);
-  }
-  float sum = 0.f;
-  if (softmax && (p.bias || !p.renormalise)) {
-    top = __int_as_float(ordered(__int_as_float(__reduce_max_sync(0xffffffffu, ordered(top)))));
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) sum += expf((l[e].x - top) + l[e].y);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  }
-  if (p.bias) {
-#pragma unroll 1
-    for (int e = lane; e < p.E; e += 32) {
-      const float2 v = l[e];
-      s.put(e, (softmax ? expf((v.x - top) + v.y) / sum : sigmoid(v)) + __ldg(p.bias + e), 0.f);
-    }
-    __syncwarp();
-    // Scores in fp32 are off by a few 1e-7 of themselves: where two of the k + 1 best lie closer than
-    // that, all are computed again in 64 bits, which the GPU does slowly.
-    if (find_best(p.E, min(p.k + 1, p.E), s)) {
-      double all = 0.0;
-      if (softmax) {
-#pragma unroll 1
-        for (int e = lane; e < p.E; e += 32) all += exp((double(l[e].x) - double(top)) + double(l[e].y));
-#pragma unroll 1
-        for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-      }
-#pragma unroll 1
-      for (int e = lane; e < p.E; e += 32) {
-        const double x = double(l[e].x) + double(l[e].y), ex = exp(softmax ? x - double(top) : -x);
-        const double score = (softmax ? ex / all : 1.0 / (1.0 + ex)) + double(__ldg(p.bias + e));
-        const float hi = static_cast<float>(score);
-        s.put(e, hi, static_cast<float>(score - double(hi)));
-      }
-      __syncwarp();
-      find_best(p.E, p.k, s);
-    }
-  } else {
-    __syncwarp();
-    find_best(p.E, p.k, s);
-  }
-  // lane j: the j-th expert
-  const int expert = lane < p.k ? s.which[lane] : 0;
-  const float2 v = lane < p.k ? l[expert] : make_float2(-INFINITY, 0.f);
-  float w;
-  if (p.renormalise) {
-    // what cancels is left out, so that scores of nothing but far experts do not vanish: softmax's sum, and
-    // the largest one's exponential where all are small
-    const float m = __int_as_float(ordered(__int_as_float(__reduce_max_sync(0xffffffffu, ordered(v.x == v.x ? v.x : -INFINITY)))));
-    w = softmax || m < 0.f ? expf((v.x - m) + v.y) : 0.f;
-    if (!softmax) w = m < 0.f ? w / (1.f + expf(v.x)) : sigmoid(v);
-    float total = lane < p.k ? w : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    w /= total;
-  } else {
-    w = softmax ? expf((v.x - top) + v.y) / sum : sigmoid(v);
-  }
-  if (lane < p.k) {
-    w *= p.route_scale;
-    c.expert[t * p.k + lane] = static_cast<uint16_t>(expert);
-    c.weight[t * p.k + lane] = w;
-    if (say && p.index) p.index[t * p.k + lane] = expert;
-    if (say && p.weight) p.weight[t * p.k + lane] = w;
-  }
-  __syncwarp();
-}
 
 // The experts that some token chose, and each one's pairs.
 __device__ void make_lists(const MoeParams &p, Choice &c) {
@@ -774,7 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_experts_kernel(const __grid_c
   ChoiceSpace &space = reinterpret_cast<ChoiceSpace *>(&sh.ring[0][0])[warp];
   griddep_wait();
   griddep_launch_dependents();
-  for (int t = warp; t < p.T; t += kThreads / 32) choose(p, t, sh.c, space, blockIdx.x == 0);
+  if (p.expert) {
+    for (int i = threadIdx.x; i < p.T * p.k; i += kThreads) {
+      sh.c.expert[i] = __ldcg(p.expert + i);
+      sh.c.weight[i] = __ldcg(p.share + i);
+    }
+  } else {
+    for (int t = warp; t < p.T; t += kThreads / 32) choose(p, t, sh.c.expert, sh.c.weight, space, blockIdx.x == 0);
+  }
   __syncthreads();
   make_lists(p, sh.c);
   const Units units(p, sh.c.n_active);

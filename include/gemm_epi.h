@@ -675,7 +675,7 @@ int gemm_epi_fp8_run(gemm_epi_fp8_plan *plan, const void *A, const float *scale_
 void gemm_epi_fp8_plan_destroy(gemm_epi_fp8_plan *plan);
 
 /*
- * A mixture-of-experts layer for a few tokens, whole, in two launches: its experts' weights
+ * A mixture-of-experts layer for a few tokens, whole, in two or three launches: its experts' weights
  * are read once for all tokens that chose them.
  *
  *   l      = x @ w_router^T                             (T, E)
