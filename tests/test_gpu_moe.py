@@ -314,8 +314,9 @@ def test_weights_from_the_quantiser():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("w", ["bf16", "e4m3"])
-def test_another_stream_a_graph_and_the_same_bits(w):
-    c = Case(10, 512, 256, 12, 3, w=w, score="sigmoid", bias=True)
+@pytest.mark.parametrize("T", [10, 40])
+def test_another_stream_a_graph_and_the_same_bits(T, w):
+    c = Case(T, 512, 256, 12, 3, w=w, score="sigmoid", bias=True)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     c.run(stream=s)
