@@ -22,6 +22,14 @@ __device__ __forceinline__ float sigmoid_of(float2 v) {  // v.y: what the roundi
   return (v.x < 0.f ? e : 1.f) / (1.f + e);
 }
 
+// exp(v - m).  A difference of 16 is off by up to 2^-20, and so is then its exponential, by that much of itself: what the
+// rounding left is kept, as for v (infinities and NaN have no remainder).
+__device__ __forceinline__ float exp_from(float2 v, float m) {
+  const float d = __fsub_rn(v.x, m), b = __fsub_rn(d, v.x);
+  const float left = __fadd_rn(__fsub_rn(v.x, __fsub_rn(d, b)), __fsub_rn(-m, b));
+  return expf(d) * (isfinite(d) ? 1.f + (left + v.y) : 1.f);
+}
+
 struct ChoiceSpace {  // a warp's
   float2 logits[GE_MOE_MAX_EXPERTS];
   alignas(16) uint32_t upper[GE_MOE_MAX_EXPERTS];
@@ -160,14 +168,14 @@ static __device__ __noinline__ void choose(const MoeParams &p, int t, uint16_t *
     // what cancels is left out, so that scores of nothing but far experts do not vanish: softmax's sum, and
     // the largest one's exponential where all are small
     const float m = __int_as_float(ordered(__int_as_float(__reduce_max_sync(0xffffffffu, ordered(v.x == v.x ? v.x : -INFINITY)))));
-    w = softmax || m < 0.f ? expf((v.x - m) + v.y) : 0.f;
+    w = softmax || m < 0.f ? exp_from(v, m) : 0.f;
     if (!softmax) w = m < 0.f ? w / (1.f + expf(v.x)) : sigmoid_of(v);
     float total = lane < p.k ? w : 0.f;
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     w /= total;
   } else {
-    w = softmax ? expf((v.x - top) + v.y) / sum : sigmoid_of(v);
+    w = softmax ? exp_from(v, top) / sum : sigmoid_of(v);
   }
   if (lane < p.k) {
     w *= p.route_scale;

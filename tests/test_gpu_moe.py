@@ -452,3 +452,19 @@ def test_run_refusals():
     assert run(c, workspace=None) == B.GE_ERR_WORKSPACE
     assert run(c, n=c.ws.numel() - 1) == B.GE_ERR_WORKSPACE
     assert run(c, workspace=c.ws.data_ptr() + 8) == B.GE_ERR_MISALIGNED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_weights_of_far_logits(score, bias, norm, T):
+    """Logits up to 80 apart, each of 24 bits and more: weights from 1 to 1e-35 are within 2^-20 of themselves."""
+    c = Case(T, 64, 16, 41, 16, score=score, bias=bias, norm=norm, router="f32")
+    g = torch.Generator().manual_seed(2)
+    c.x.zero_()
+    c.x[:, 0] = 1 + torch.arange(T, device=c.x.device) % 8 / 32
+    c.router.zero_()
+    c.router[:, 0] = (-65 * torch.rand(41, generator=g)).to(c.x.device)
+    c.run().check()
