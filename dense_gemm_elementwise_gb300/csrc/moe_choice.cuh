@@ -44,7 +44,8 @@ struct ChoiceSpace {  // a warp's
 
 // The `some` best of up to 32 N experts, by how many are above each: a single warp's time is what it issues one after
 // another, and these comparisons do not wait for each other.  (For more than 64 experts they are too many: 64 tokens'
-// choice among 128 took 44 us instead of 27.)  Upper keys alone: false where two of the best are equal.
+// choice among 128 took 44 us instead of 27.)  Upper keys alone: false, with nothing stored, where one of the best is equal
+// to another of them or to one that is left out.
 template <int N>
 __device__ __forceinline__ bool rank(int E, int some, ChoiceSpace &s) {
   const int lane = threadIdx.x & 31;
@@ -60,15 +61,21 @@ __device__ __forceinline__ bool rank(int E, int some, ChoiceSpace &s) {
 #pragma unroll
     for (int i = 0; i < N; ++i) above[i] += (o.x > mine[i]) + (o.y > mine[i]) + (o.z > mine[i]) + (o.w > mine[i]);
   }
+  // How many have a place, above the sum of 2^place (64 times 2^16 at most).  Groups of equal keys g at place a add g to the
+  // number and g 2^a to the sum; as many as wanted with a sum of 2^some - 1 are one for each place.
+  constexpr uint32_t kOne = 1u << 25;
   uint32_t places = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (mine[i] != 0 && above[i] < some) places += kOne + (1u << above[i]);
+  if (__reduce_add_sync(0xffffffffu, places) != some * kOne + (1u << some) - 1u) return false;
 #pragma unroll
   for (int i = 0; i < N; ++i)
     if (mine[i] != 0 && above[i] < some) {
       s.best[above[i]] = mine[i];
       s.which[above[i]] = i * 32 + lane;
-      places |= 1u << above[i];
     }
-  return __reduce_or_sync(0xffffffffu, places) == (1u << some) - 1u;
+  return true;
 }
 
 // The `some` best experts in order, of equal keys the lower index first; whether two neighbours' upper keys are close.

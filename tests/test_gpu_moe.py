@@ -468,3 +468,72 @@ def test_weights_of_far_logits(score, bias, norm, T):
     c.router.zero_()
     c.router[:, 0] = (-65 * torch.rand(41, generator=g)).to(c.x.device)
     c.run().check()
+
+
+SCORES = [dict(), dict(norm=False), dict(score="sigmoid"), dict(bias=True), dict(bias=True, score="sigmoid")]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("E,k", [(2, 1), (7, 1), (32, 1), (33, 1), (64, 1), (70, 1), (32, 2), (40, 3), (64, 15), (64, 16), (128, 3)])
+@pytest.mark.parametrize("kw", SCORES)
+def test_equal_logits_of_all_experts(E, k, T, kw):
+    """Tokens of zeros between others, and equal biases: the first k experts, in both places where a choice is made."""
+    c = Case(T, 64, 16, E, k, **kw)
+    c.x[::2] = 0.0
+    if c.bias is not None:
+        c.bias.fill_(0.125)
+    c.run().check()
+    assert bool((c.index[:T:2] == torch.arange(k, device=c.x.device)).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("E,k", [(4, 1), (4, 3), (32, 1), (32, 7), (40, 5), (64, 1), (64, 3), (64, 15), (128, 7)])
+@pytest.mark.parametrize("apart", [False, True])
+@pytest.mark.parametrize("kw", SCORES)
+def test_a_last_place_between_two_equal_experts(E, k, T, apart, kw):
+    """Every expert is there twice, next to itself or half of all experts away, and an odd number of them is chosen."""
+    c = Case(T, 256, 16, E, k, **kw)
+    half = E // 2
+    copies, of = (slice(half, E), slice(0, half)) if apart else (slice(1, E, 2), slice(0, E, 2))
+    c.router[copies] = c.router[of]
+    if c.bias is not None:
+        c.bias[copies] = c.bias[of]
+    c.run().check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("E,k", [(32, 1), (32, 5), (64, 1), (64, 7), (64, 15), (128, 3)])
+@pytest.mark.parametrize("kw", SCORES)
+def test_a_last_place_between_logits_that_fp32_does_not_tell_apart(E, k, T, kw):
+    """As test_choices_between_logits_that_fp32_does_not_tell_apart, with an odd number chosen."""
+    c = Case(T, 2048, 16, E, k, **kw)
+    half = E // 2
+    c.router[half:] = c.router[:half]
+    c.router[half:, 5] += 2.0 ** -12 * (1 - 2 * (torch.arange(half, device=c.x.device) % 2))
+    c.router[:, 6:12] *= 50.0
+    if c.bias is not None:
+        c.bias[half:] = c.bias[:half]
+    c.run().check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 40])
+@pytest.mark.parametrize("E,k", [(2, 1), (17, 1), (17, 4), (32, 3), (33, 1), (64, 1), (64, 5), (64, 16), (100, 3)])
+def test_biased_scores_equal_in_fp32(E, k, T):
+    """Sigmoids of 20 and more are 1 in fp32, and 1 - e^-l, 2e-9 and less below it, in 64 bits.  Logits are exact."""
+    c = Case(T, 64, 16, E, k, score="sigmoid", bias=True, router="f32")
+    g = torch.Generator().manual_seed(E)
+    c.x[:, 0] = 1.0
+    c.x[:, 1:] = 0.0
+    c.router[:, 0] = (20.0 + torch.randperm(E, generator=g) / 32.0).to(c.x.device)
+    c.bias.fill_(0.25)
+    c.run().check()
+    c = Case(T, 64, 16, E, k, score="sigmoid", bias=True, router="f32")  # (and some that 64 bits do not tell apart either)
+    c.x[:, 0] = 1.0
+    c.x[:, 1:] = 0.0
+    c.router[:, 0] = (20.0 + torch.randperm(E, generator=g) // 2 / 32.0).to(c.x.device)
+    c.bias.fill_(0.25)
+    c.run().check()
