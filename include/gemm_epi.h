@@ -634,6 +634,10 @@ void gemm_epi_quant_plan_destroy(gemm_epi_quant_plan *plan);
  * Products are exact and summed in fp32 over a block, each block's sum is scaled and
  * added in fp32, C is added last, and the result is rounded once.  Results are bit-for-bit
  * repeatable for a given plan and device.
+ *
+ * Scales of B have to be at most 2^88 in magnitude and products of a scale of A and one of B below 2^128: some plans multiply
+ * the two scales first, others a block's sum by B's scale first, and past that an infinity on the way may replace what is
+ * finite or 0.  Where the scales' product, or a block's sum times B's scale, is below 2^-126 it is rounded to a multiple of 2^-149.
  */
 typedef struct {
   int32_t a, b;         /* GE_E4M3 or GE_E5M2 each                                            */

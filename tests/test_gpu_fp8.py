@@ -341,3 +341,40 @@ def test_a_linear_layer_forward_and_backward():
         lim = mag * (2.0 ** -16 + (blocks(k) + 4) * 2.0 ** -23) + ref.abs() * U[d]
         assert bool(((got.double() - ref).abs() <= lim).all())
         assert float((got.double() - plain).norm() / plain.norm()) <= 2.0 ** -3
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 300, 385), (7, 1000, 260), (16, 300, 385), (17, 300, 385), (100, 136, 128), (130, 700, 1500), (600, 5000, 260)])
+@pytest.mark.parametrize("block", ["square", "row"])
+@pytest.mark.parametrize("kind", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("ea,eb,least", [(-60, -62, False), (-30, -90, False), (-90, -30, False), (-100, 87, False), (120, -90, False), (60, 60, True), (38, 87, True)])
+def test_small_and_large_scales_in_every_kernel(ea, eb, least, kind, block, M, N, K):
+    """Scales of 2^ea and 2^eb up to twice that.  A block of A in three and one of B in four are zeros, which have the
+    quantiser's least scale in A; with `least` all other values are 0 or the least one.  What overflows when its terms' magnitudes
+    are added is left out.  Beside the file's bound each block's products and addition lose half of the least fp32 number
+    where they are below 2^-126, and slices once more: less than 2^-148 for each."""
+    c = Case(M, N, K, kind, kind, "f32", block=block)
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    dev = c.A.device
+    for s, e in ((c.sa, ea), (c.sb, eb)):
+        s.copy_((1 + torch.rand(s.shape, generator=g, device=dev)) * 2.0 ** e)
+    for v, n in ((c.A.view(torch.uint8), 3), (c.B.view(torch.uint8), 4)):
+        if least:
+            v.copy_((torch.rand(v.shape, generator=g, device=dev) < 0.05).to(torch.uint8))
+        for j in range(blocks(K)):
+            rows = torch.arange(v.shape[0], device=dev) % n == j % n
+            v[rows, 128 * j:128 * j + 128] = 0
+            if n == 3:
+                c.sa[j, rows] = 2.0 ** -126
+    c.run()
+    torch.cuda.synchronize()
+    assert B.gemm_epi_last_error() == B.GE_OK
+    got = c.buf[c.at:c.at + M, :N]
+    y, mag = c.want()
+    on = mag < 2.0 ** 127
+    assert bool(on.any()) and bool(got[on].isfinite().all())
+    lim = mag * (2.0 ** -16 + (blocks(K) + 4) * 2.0 ** -23) + y.abs() * U["f32"] + (blocks(K) + 4) * 2.0 ** -148
+    off = (got.double() - y).abs()
+    worst = (off / lim)[on].max().item()
+    assert worst <= 1.0, (worst, ((off > lim) & on).nonzero()[:4].tolist())
+    B.gemm_epi_fp8_plan_destroy(c.plan)
