@@ -606,7 +606,7 @@ typedef struct gemm_epi_quant_plan gemm_epi_quant_plan;
 
 /* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID (NULL, bad block or
  * option), _UNSUPPORTED (types), _SHAPE (T or D <= 0 or above 2^31 - 1, 2^31 blocks of 128 by 128 or more, a pitch
- * too small), _MISALIGNED (a pitch of q or qt that is given and is no multiple of 16), _ARCH. */
+ * too small or above 2^31 - 1), _MISALIGNED (a pitch of q or qt that is given and is no multiple of 16), _ARCH. */
 int gemm_epi_quant_plan_create(gemm_epi_quant_plan **plan, int64_t T, int64_t D,
                                const ge_quant_desc *desc);
 
@@ -656,8 +656,8 @@ typedef struct {
 typedef struct gemm_epi_fp8_plan gemm_epi_fp8_plan;
 
 /* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID, _UNSUPPORTED (types),
- * _SHAPE (M, N or K <= 0 or above 2^31 - 1, a pitch too small), _MISALIGNED (lda, ldb), _ARCH,
- * _SMEM, _CUDA. */
+ * _SHAPE (M, N or K <= 0 or above 2^31 - 257, more than 2^28 tiles of 128 x 128, a pitch too small or above 2^31 - 1),
+ * _MISALIGNED (lda, ldb), _ARCH, _SMEM, _CUDA. */
 int gemm_epi_fp8_plan_create(gemm_epi_fp8_plan **plan, int64_t M, int64_t N, int64_t K,
                              const ge_fp8_desc *desc);
 
@@ -725,7 +725,7 @@ typedef struct gemm_epi_moe_plan gemm_epi_moe_plan;
 
 /* Validate and build a plan (host state only).  Errors: GE_ERR_INVALID, _UNSUPPORTED (types,
  * activation), _SHAPE (T outside 1..GE_MOE_MAX_TOKENS, E outside 1..GE_MOE_MAX_EXPERTS, k outside
- * 1..min(E, GE_MOE_MAX_K), D or F <= 0 or above 2^20, a pitch below D), _MISALIGNED (D, F or
+ * 1..min(E, GE_MOE_MAX_K), D or F <= 0 or above 2^20, a pitch below D or above 2^31 - 1), _MISALIGNED (D, F or
  * a pitch not as above), _ARCH, _CUDA. */
 int gemm_epi_moe_plan_create(gemm_epi_moe_plan **plan, int64_t T, int64_t D, int64_t F, int64_t E,
                              int64_t k, const ge_moe_desc *desc);

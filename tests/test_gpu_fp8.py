@@ -378,3 +378,12 @@ def test_small_and_large_scales_in_every_kernel(ea, eb, least, kind, block, M, N
     worst = (off / lim)[on].max().item()
     assert worst <= 1.0, (worst, ((off > lim) & on).nonzero()[:4].tolist())
     B.gemm_epi_fp8_plan_destroy(c.plan)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=(1 << 31) - 256), "GE_ERR_SHAPE"), (dict(N=(1 << 31) - 256), "GE_ERR_SHAPE"), (dict(K=(1 << 31) - 256), "GE_ERR_SHAPE"),
+    (dict(lda=1 << 31), "GE_ERR_SHAPE"), (dict(ldd=1 << 31), "GE_ERR_SHAPE"),
+    (dict(M=(1 << 31) - 257, K=24), "GE_ERR_MISALIGNED"), (dict(N=(1 << 31) - 257, K=24), "GE_ERR_MISALIGNED"),
+    (dict(K=(1 << 31) - 257), "GE_ERR_MISALIGNED")])  # (sizes are looked at before pitches)
+def test_largest_sizes(kw, status):
+    assert bad(**kw) == getattr(B, status)

@@ -537,3 +537,8 @@ def test_biased_scores_equal_in_fp32(E, k, T):
     c.router[:, 0] = (20.0 + torch.randperm(E, generator=g) // 2 / 32.0).to(c.x.device)
     c.bias.fill_(0.25)
     c.run().check()
+
+
+@pytest.mark.parametrize("kw", [dict(ldx=1 << 31), dict(ldy=1 << 31), dict(D=(1 << 20) + 16)])
+def test_largest_pitches_and_widths(kw):
+    assert bad(**kw) == B.GE_ERR_SHAPE

@@ -247,3 +247,9 @@ def test_run_refusals():
     assert B.gemm_epi_quant_run(plan, c.x, c.q, c.scale, check=False) == B.GE_OK
     torch.cuda.synchronize()
     B.gemm_epi_quant_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("kw", [dict(ldx=1 << 31), dict(ldq=1 << 31), dict(ldqt=1 << 31), dict(lds=1 << 31), dict(ldst=1 << 31),
+                                dict(T=(1 << 31) - 1, D=1 << 15)])
+def test_largest_sizes_and_pitches(kw):
+    assert bad(**kw) == B.GE_ERR_SHAPE
