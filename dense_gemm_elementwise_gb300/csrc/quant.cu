@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kQuantThreads, XT == GE_F32 ? 2 : 4) quant_ker
   __shared__ __align__(16) float inverse[kB];        // columns' inverse scales
   __shared__ __align__(16) uint8_t turned[COLS ? kB * kB : 16];
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tiles_d = (p.D + kB - 1) / kB, td = blockIdx.x % tiles_d, tt = blockIdx.x / tiles_d;
+  const int tiles_d = (p.D - 1) / kB + 1, td = blockIdx.x % tiles_d, tt = blockIdx.x / tiles_d;
   const int64_t d0 = int64_t(td) * kB, t0 = int64_t(tt) * kB;
   const int64_t d = d0 + cg * 8, t = t0 + rg * 8;
   const int cols = static_cast<int>(min(int64_t(8), p.D - d)), rows = static_cast<int>(min(int64_t(8), p.T - t));

@@ -253,3 +253,40 @@ def test_run_refusals():
                                 dict(T=(1 << 31) - 1, D=1 << 15)])
 def test_largest_sizes_and_pitches(kw):
     assert bad(**kw) == B.GE_ERR_SHAPE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", ["row", "square"])
+def test_the_widest_rows(block):
+    """Numbers of columns next to 2^31, of which all but the last 368 and 383 are zeros."""
+    dev = torch.device("cuda", 0)
+
+    def wide(D, n, **kw):
+        x = torch.zeros(2, D, dtype=torch.bfloat16, device=dev)
+        tail = some(2, n)
+        x[:, -n:] = tail.to(dev)
+        return x, tail, B.gemm_epi_quant_plan_create(2, D, B.make_quant_desc("bf16", "e4m3", block=block, **kw))
+
+    D, n = (1 << 31) - 16, 368
+    x, tail, plan = wide(D, n)
+    q = torch.full((2, D), SENT, dtype=torch.uint8, device=dev)
+    s = torch.full((blocks(D), 1 if block == "square" else 2), -7.0, device=dev)
+    B.gemm_epi_quant_run(plan, x, q, s)
+    torch.cuda.synchronize()
+    B.gemm_epi_quant_plan_destroy(plan)
+    wq, ws = reference(tail, "e4m3", block == "square")
+    assert torch.equal(q[:, -n:].cpu(), wq) and torch.equal(s[-3:].cpu(), ws)
+    assert not bool(q[:, :-n].any()) and bool((s[:-3] == 2.0 ** -126).all())
+    del x, q, s
+    D, n = (1 << 31) - 1, 383
+    x, tail, plan = wide(D, n, ldqt=16)
+    qt = torch.full((D + 1, 16), SENT, dtype=torch.uint8, device=dev)
+    st = torch.full((1, blocks(D) if block == "square" else D), -7.0, device=dev)
+    B.gemm_epi_quant_run(plan, x, None, None, qt, st)
+    torch.cuda.synchronize()
+    B.gemm_epi_quant_plan_destroy(plan)
+    wq, ws = reference(tail.t().contiguous(), "e4m3", block == "square")
+    m = ws.shape[1]
+    assert torch.equal(qt[-n - 1:-1, :2].cpu(), wq) and torch.equal(st[:, -m:].cpu(), ws)
+    assert bool((st[:, :-m] == 2.0 ** -126).all()) and bool((qt[-1] == SENT).all()) and bool((qt[-n:, 2:] == SENT).all())
+    assert not bool(qt[:1 << 20, :2].any()) and not bool(qt[-1 << 20:-n - 1, :2].any())
