@@ -10,7 +10,8 @@
 // the other.  fp32 additions in registers are rounded, which the tensor unit's are not.
 //
 // That is a hand-over between the tensor unit and the epilogue for every 512 clocks of tensor work, whose
-// latencies bound the kernel (8192^3: 412 us, 2.67 PFLOP/s; without hand-overs, one sum over all of K, 375):
+// latencies bound the kernel (8192^3: 441 us in a row, 2.49 PFLOP/s, under the power cap; in bursts 413, and 375 without hand-overs, one sum
+// over all of K.  Times below are of bursts):
 //   * Accumulators are handed back by arrivals without release and waited for without acquire; nothing
 //     but tensor memory is passed on, which the tcgen05 fences order.  (975 -> 519 us: release and acquire at
 //     cluster scope take about 1000 clocks each.)
@@ -24,6 +25,9 @@
 //     k-block ahead, they came too late (with constants in their place it took 30 us less).
 //   * 32 columns (16) are on their way to an epilogue thread while it adds as many others, which its registers
 //     have room for because the other warps give theirs away.  (Sixteen epilogue warps took 530 us.)
+//   * The loop over a k-block has one way through it.  A second one, for scales whose product no normal fp32 number holds,
+//     made the compiler spill in the first: 8192^3 in a row 437 -> 447 us where it was chosen for eight k-blocks at a time, 480 to
+//     526 where for each.  So the range of the scales is the interface's.
 //
 // Few tiles (128 x 128, single CTAs) share their sums over K with the other CTAs of a cluster, which leave them in
 // shared memory, where each CTA then adds its part of the tile in the order of the slices: one launch, no

@@ -28,7 +28,7 @@ struct MoeParams {
   float *weight;
   MoeHead *head;
   uint32_t *done;   // units of the first kind, by expert
-  uint32_t *shares;  // experts' shares of 16 columns of y
+  uint32_t *shares;  // experts that have added their share of kDownCols columns of y
   float2 *logits;   // (T, E)
   uint16_t *expert;  // the choice (T, k), where it has a kernel of its own, and
   float *share;      // ... its weights

@@ -141,18 +141,6 @@ __device__ __forceinline__ bool mbar_try_wait_relaxed(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
-__device__ __forceinline__ bool mbar_test_wait_relaxed(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // ---------------------------------------------- programmatic dependent launch --
 // Wait until the grids this launch depends on have completed and their
 // memory is visible (returns at once when the launch was not overlapped).
